@@ -322,6 +322,118 @@ size_t ssd_calibrate_workspace_bytes(const ssd_shape* shape);
 int ssd_scales_from_amax(int64_t ngroups, int64_t nheads, int64_t headdim,
                          const float* amax, float* pack);
 
+/* ---------------------------------------------------------------------------
+ * The steps around the SSD in a Mamba-2 layer ("Overall framework": In Proj,
+ * Conv, SSD, RMSNorm, Out Proj):
+ *
+ *   residual + RMSNorm   ssd_add_norm          (rows in 8 bits for In Proj)
+ *   In Proj              ssd_matmul_i8         rows of  z | x B C | dt
+ *   Conv                 ssd_conv_forward      X, B, C and dt of ssd_forward
+ *   SSD                  ssd_forward
+ *   gated RMSNorm        ssd_gated_norm        (rows in 8 bits for Out Proj)
+ *   Out Proj             ssd_matmul_i8
+ *
+ * and, for single tokens, ssd_conv_decode_step in the place of Conv and SSD.
+ * Unlike the dense buffers above, inputs that are parts of In Proj's rows are
+ * read in place: "ld" is the distance between rows in elements, and such a
+ * pointer need only be aligned to its element (16-byte aligned rows are read
+ * in 16-byte pieces).
+ * ------------------------------------------------------------------------- */
+
+/* Parameters of the depthwise causal convolution over the Cd = H*P + 2*G*N
+ * channels x | B | C, and of the step size (device fp32 arrays). */
+typedef struct ssd_conv {
+  const float* weight;  /* [Cd, width]; weight[c, width - 1] meets the position itself */
+  const float* bias;    /* [Cd], or NULL: 0 */
+  const float* dt_bias; /* [H], or NULL: 0 */
+  int32_t width;        /* taps: 2, 3 or 4 (SSD_E_UNSUPPORTED otherwise) */
+} ssd_conv;
+
+/* Causal convolution, SiLU and softplus of a batch of prompts (or of chunks
+ * that continue them): the inputs of ssd_forward from In Proj's output.
+ *   u_t[c] = sum_{j<width} weight[c,j] xbc_{t-width+1+j}[c] + bias[c]
+ *   x | B | C = u / (1 + exp(-u)),   dt_t[h] = softplus(dt_raw_t[h] + dt_bias[h])
+ * in fp32, rounded once into shape->dtype.
+ * xbc: row (b, t) at xbc + (b*L + t)*ld_xbc, Cd channels; dt_raw likewise, H
+ * values (ld_xbc >= Cd, ld_dt >= H). X, B, C, dt: as ssd_forward takes them.
+ * lengths [B] (may be NULL: L): sequence b ends before position lengths[b]
+ * (taken into [0, L]). Rows from there on are written as zeros, so that
+ * ssd_forward's final_state is the state at each sequence's own end (dt = 0
+ * leaves it unchanged).
+ * conv_state [B, width, Cd] in shape->dtype, 16-byte aligned (may be NULL):
+ * the inputs of a sequence's last width positions, position p in slot
+ * p % width. pos [B] (may be NULL): positions already seen, >= 0. With pos,
+ * the taps before position 0 of the call read conv_state (required then);
+ * positions before the sequence's start, and without pos all taps before
+ * position 0, count as zero and need nothing in conv_state. On return
+ * conv_state holds the last width inputs up to the sequence's end; slots of
+ * older positions stay as they were. The caller then adds the lengths to pos.
+ * B * Cd < 2^32 (SSD_E_SHAPE otherwise). */
+int ssd_conv_forward(const ssd_shape* shape, const ssd_conv* conv, const void* xbc,
+                     int64_t ld_xbc, const void* dt_raw, int64_t ld_dt, const int32_t* lengths,
+                     const int32_t* pos, void* conv_state, void* X, void* B, void* C, void* dt,
+                     void* stream);
+
+/* One position of Conv and SSD in one launch: ssd_conv_forward's arithmetic on
+ * one row per sequence, then ssd_decode_step's on its results, which stay in
+ * fp32 (they are not rounded to shape->dtype in between). shape->seqlen must
+ * be 1 (or batch 0), batch * nheads <= 2^24.
+ * xbc [B rows, Cd] and dt_raw [B rows, H] with row distances; conv_state
+ * [B, width, Cd] and pos [B] as above, both required; the call writes slot
+ * pos % width and reads the width - 1 others. It does not change pos: the
+ * caller adds 1 once all layers have used it. state and Y as ssd_decode_step.
+ * scales: INT8 only. */
+int ssd_conv_decode_step(const ssd_shape* shape, int path, const ssd_conv* conv, const void* xbc,
+                         int64_t ld_xbc, const void* dt_raw, int64_t ld_dt, const float* A,
+                         const float* D, const ssd_scales* scales, void* conv_state,
+                         const int32_t* pos, void* state, void* Y, void* stream);
+
+/* The residual's addition and RMSNorm of rows, with the rows in 8 bits:
+ *   r = x + residual,   y = r / sqrt(mean(r^2) + eps) * weight
+ *   scale = max|y| / 127 (1 for a row of zeros),  q = RHAZ(y / scale)
+ * in fp32. x [rows, cols] at row distance ld_x, dtype SSD_DTYPE_*; residual
+ * and residual_out [rows, cols] dense in res_dtype (either may be NULL: no
+ * residual, and r not kept; they may be the same buffer). weight [cols] fp32.
+ * q int8 [rows, cols] and scale [rows] fp32 go together (both NULL: no codes).
+ * out [rows, cols] in dtype (NULL: not wanted; q or out is required): the rows
+ * y; where q is given too, the values scale * q that the codes stand for, so
+ * that a consumer in floating point sees what one in 8 bits sees.
+ * out may be x itself (at ld_x == cols). A row that holds NaN or infinity gets
+ * a scale that is not finite. rows <= 2^31 - 1, cols <= 16384 (SSD_E_SHAPE);
+ * rows == 0 is a valid empty problem. */
+int ssd_add_norm(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ld_x,
+                 const void* residual, int res_dtype, void* residual_out, const float* weight,
+                 float eps, void* out, int8_t* q, float* scale, void* stream);
+
+/* The gated RMSNorm between SSD and Out Proj: r = y * z / (1 + exp(-z)), the
+ * mean of r^2 taken over each of `groups` equal runs of channels, and the rest
+ * as ssd_add_norm. y [rows, cols] dense; z at row distance ld_z. out may be y. */
+int ssd_gated_norm(int64_t rows, int64_t cols, int64_t groups, int dtype, const void* y,
+                   const void* z, int64_t ld_z, const float* weight, float eps, void* out,
+                   int8_t* q, float* scale, void* stream);
+
+/* Matrix product in 8-bit integers (In Proj, Out Proj): exact int32 sums,
+ *   out[m,n] = a_scale[m] w_scale[n] sum_k a[m,k] w[n,k] + bias[n]
+ * a int8 [M, K] with a step for each row (token), w int8 [N, K] with a step for
+ * each row (output channel), bias [N] fp32 (may be NULL; at Out Proj it carries
+ * the mean correction of "Key design 4"), out [M, N] in out_dtype. K is a
+ * multiple of 16 (SSD_E_UNSUPPORTED) and at most 131056 (so that the sums of any
+ * codes fit), M, N <= 2^31 - 1; M == 0 is a valid empty problem. workspace: device memory
+ * of at least ssd_matmul_i8_workspace_bytes(M, N, K) bytes (may be NULL when
+ * that is 0); calls that may overlap need one each. */
+int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float* a_scale,
+                  const int8_t* w, const float* w_scale, const float* bias, int out_dtype,
+                  void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_matmul_i8 needs (0 for an invalid problem). Host only. */
+size_t ssd_matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/* Host-only: a weight matrix [N, K] (fp32, row-major) as 8-bit rows for
+ * ssd_matmul_i8: w_scale[n] = fp32(max_k |w[n,k]| / 127) (1 for a row of
+ * zeros), q = RHAZ(w / w_scale) evaluated in float64. A weight that is NaN or
+ * infinite returns SSD_E_VALUE and nothing is written. */
+int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w_scale);
+
 /* Static string for a status code. */
 const char* ssd_status_string(int status);
 

@@ -69,6 +69,11 @@ class SsdTaps(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q_xs", "s32", "s8_local", "passed")]
 
 
+class SsdConv(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("width", ctypes.c_int32)]
+
+
 class SSDError(RuntimeError):
     def __init__(self, name: str, rc: int):
         super().__init__(f"{name} failed: {status_string(rc)} (status {rc})")
@@ -82,6 +87,8 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     SP = ctypes.POINTER(SsdShape)
+    CP = ctypes.POINTER(SsdConv)
+    I64 = ctypes.c_int64
     sig = {
         "ssd_quantize_bc": [SP, P, P, ctypes.POINTER(SsdScales), P, P, P],
         "ssd_chunk_cumsum": [SP, P, P, P, P, P, P],
@@ -100,6 +107,13 @@ def _load() -> ctypes.CDLL:
         "ssd_mean_correction": [SP, P, P, P, P],
         "ssd_calibrate_amax": [SP, P, P, P, P, P, P, P, ctypes.c_size_t, P],
         "ssd_scales_from_amax": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P],
+        "ssd_conv_forward": [SP, CP, P, I64, P, I64, P, P, P, P, P, P, P, P],
+        "ssd_conv_decode_step": [SP, ctypes.c_int, CP, P, I64, P, I64, P, P, ctypes.POINTER(SsdScales), P, P,
+                                 P, P, P],
+        "ssd_add_norm": [I64, I64, ctypes.c_int, P, I64, P, ctypes.c_int, P, P, ctypes.c_float, P, P, P, P],
+        "ssd_gated_norm": [I64, I64, I64, ctypes.c_int, P, P, I64, P, ctypes.c_float, P, P, P, P],
+        "ssd_matmul_i8": [I64, I64, I64, P, P, P, P, P, ctypes.c_int, P, P, ctypes.c_size_t, P],
+        "ssd_pack_weight_i8": [I64, I64, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -109,6 +123,8 @@ def _load() -> ctypes.CDLL:
         f = getattr(lib, name)
         f.argtypes = [SP, ctypes.c_int]
         f.restype = ctypes.c_size_t
+    lib.ssd_matmul_i8_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.ssd_matmul_i8_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_calibrate_workspace_bytes.argtypes = [SP]
     lib.ssd_calibrate_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_status_string.argtypes = [ctypes.c_int]
@@ -123,6 +139,8 @@ EXPORTED = ("ssd_quantize_bc", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state
             "ssd_epilogue", "ssd_mean_correction",
             "ssd_workspace_bytes",
             "ssd_calibrate_amax", "ssd_calibrate_workspace_bytes", "ssd_scales_from_amax",
+            "ssd_conv_forward", "ssd_conv_decode_step", "ssd_add_norm", "ssd_gated_norm", "ssd_matmul_i8",
+            "ssd_matmul_i8_workspace_bytes", "ssd_pack_weight_i8",
             "ssd_status_string")
 
 
@@ -346,3 +364,198 @@ def calibrate(shape_of, seqs, A, device="cuda") -> ScalePack:
         ssd_calibrate_amax(shape_of(sq), sq["x"], sq["dt"], A, sq["B"], sq["C"], amax)
     host = amax.cpu().numpy()
     return ScalePack(ssd_scales_from_amax(G, H, P, host), device)
+
+
+# ---------------------------------------------------------------------------
+# the steps around the SSD in a layer
+# ---------------------------------------------------------------------------
+
+class ConvParams:
+    """The causal convolution's parameters on the device: weight [Cd, width] (or
+    [Cd, 1, width]), bias [Cd] and dt_bias [H] (either may be None), float32."""
+
+    def __init__(self, weight, bias=None, dt_bias=None):
+        self.weight = weight.reshape(weight.shape[0], -1)
+        self.bias, self.dt_bias = bias, dt_bias
+        for t in (self.weight, bias, dt_bias):
+            if t is not None and t.dtype != torch.float32:
+                raise ValueError("convolution parameters are float32")
+        if bias is not None and bias.numel() != self.channels:
+            raise ValueError("bias must hold one value for each channel")
+        self.struct = SsdConv(_p(self.weight), _p(bias), _p(dt_bias), self.width)
+
+    @property
+    def channels(self) -> int:
+        return self.weight.shape[0]
+
+    @property
+    def width(self) -> int:
+        return self.weight.shape[1]
+
+
+def _on_gpu(t, name):
+    """Kernels are launched on the current device: a tensor elsewhere is refused."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU, got {t.device}")
+
+
+def _rows(t, n):
+    """Address and row distance of a tensor whose rows of n values lie at equal
+    distances (a contiguous tensor, or a slice of the columns of one)."""
+    st, sh = t.stride(), t.shape
+    if sh[-1] != n:
+        raise ValueError(f"rows of {n} values expected, got {sh[-1]}")
+    if n > 1 and st[-1] != 1:
+        raise ValueError("the values of a row must be consecutive")
+    ld, rows = None, 1
+    for size, step in zip(reversed(sh[:-1]), reversed(st[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = step
+        elif step != ld * rows:
+            raise ValueError("rows must lie at equal distances")
+        rows *= size
+    _on_gpu(t, "the rows")
+    return t.data_ptr(), n if ld is None else ld
+
+
+def _expect(t, name, numel, dtype):
+    """A dense buffer of a given size and type (None passes: the C call decides)."""
+    if t is None:
+        return None
+    if t.numel() != numel or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor of {numel} values, got {tuple(t.shape)} {t.dtype}")
+    _on_gpu(t, name)
+    return _p(t)
+
+
+_TORCH_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
+
+
+def _conv_inputs(shape, conv, xbc, dt_raw):
+    cd = shape.nheads * shape.headdim + 2 * shape.ngroups * shape.dstate
+    td = _TORCH_DTYPE.get(shape.dtype)
+    if conv.channels != cd or (conv.dt_bias is not None and conv.dt_bias.numel() != shape.nheads):
+        raise ValueError(f"the shape has {cd} channels and {shape.nheads} heads, the parameters {conv.channels}")
+    n = shape.batch * shape.seqlen
+    if xbc.dtype != td or dt_raw.dtype != td or xbc.numel() != n * cd or dt_raw.numel() != n * shape.nheads:
+        raise ValueError("xbc and dt_raw must hold batch * seqlen rows in the shape's type")
+    if n == 0:
+        return cd, td, (None, cd), (None, shape.nheads)
+    return cd, td, _rows(xbc, cd), _rows(dt_raw, shape.nheads)
+
+
+def ssd_conv_forward(shape, conv, xbc, dt_raw, X, B, C, dt, conv_state=None, pos=None, lengths=None,
+                     stream=None):
+    """Causal convolution, SiLU and softplus of prompts. ``xbc`` and ``dt_raw`` may be
+    column slices of In Proj's output; ``pos`` and ``lengths`` are int32 [B]."""
+    cd, td, (px, ldx), (pt, ldt) = _conv_inputs(shape, conv, xbc, dt_raw)
+    b, n = shape.batch, shape.batch * shape.seqlen
+    if n == 0:
+        return  # empty tensors have no addresses
+    bc = n * shape.ngroups * shape.dstate
+    _check("ssd_conv_forward", LIB.ssd_conv_forward(
+        ctypes.byref(shape), ctypes.byref(conv.struct), px, ldx, pt, ldt,
+        _expect(lengths, "lengths", b, torch.int32), _expect(pos, "pos", b, torch.int32),
+        _expect(conv_state, "conv_state", b * conv.width * cd, td),
+        _expect(X, "X", n * shape.nheads * shape.headdim, td), _expect(B, "B", bc, td), _expect(C, "C", bc, td),
+        _expect(dt, "dt", n * shape.nheads, td), _stream(stream)))
+
+
+def ssd_conv_decode_step(shape, path, conv, xbc, dt_raw, A, D, scales, conv_state, pos, state, Y,
+                         stream=None):
+    """One position of the convolution and the SSD: ``conv_state`` and ``state`` are
+    updated in place, ``pos`` (int32 [B]) is left for the caller to advance."""
+    cd, td, (px, ldx), (pt, ldt) = _conv_inputs(shape, conv, xbc, dt_raw)
+    b, hp = shape.batch, shape.nheads * shape.headdim
+    if b == 0:
+        return
+    _check("ssd_conv_decode_step", LIB.ssd_conv_decode_step(
+        ctypes.byref(shape), path, ctypes.byref(conv.struct), px, ldx, pt, ldt,
+        _expect(A, "A", shape.nheads, torch.float32), _expect(D, "D", shape.nheads, torch.float32),
+        _scales(scales), _expect(conv_state, "conv_state", b * conv.width * cd, td),
+        _expect(pos, "pos", b, torch.int32),
+        _expect(state, "state", b * hp * shape.dstate, torch.int8 if path == SSD_PATH_INT8 else torch.float32),
+        _expect(Y, "Y", b * hp, td), _stream(stream)))
+
+
+def _norm_outputs(rows, cols, dtype, weight, out, q, scale):
+    return (_expect(weight, "weight", cols, torch.float32), _expect(out, "out", rows * cols, dtype),
+            _expect(q, "q", rows * cols, torch.int8), _expect(scale, "scale", rows, torch.float32))
+
+
+def ssd_add_norm(x, residual, residual_out, weight, eps, out=None, q=None, scale=None, stream=None):
+    """r = x + residual, RMSNorm of r's rows; the rows in ``out`` and as codes ``q`` with
+    a step ``scale`` each. ``x`` may be a column slice; ``residual`` and
+    ``residual_out`` share a type, x's or float32 (either may be None)."""
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    if rows == 0:
+        return
+    px, ldx = _rows(x, cols)
+    kept = residual if residual is not None else residual_out
+    rt = x.dtype if kept is None else kept.dtype
+    w, o, pq, ps = _norm_outputs(rows, cols, x.dtype, weight, out, q, scale)
+    _check("ssd_add_norm", LIB.ssd_add_norm(
+        rows, cols, DTYPE_CODE[x.dtype], px, ldx, _expect(residual, "residual", rows * cols, rt),
+        DTYPE_CODE[rt], _expect(residual_out, "residual_out", rows * cols, rt), w, eps, o, pq, ps,
+        _stream(stream)))
+
+
+def ssd_gated_norm(y, z, groups, weight, eps, out=None, q=None, scale=None, stream=None):
+    """RMSNorm over each of ``groups`` runs of channels of y * silu(z); outputs as
+    ``ssd_add_norm``. ``z`` may be a column slice of In Proj's output. The row
+    length is z's last dimension."""
+    cols = z.shape[-1]
+    rows = z.numel() // cols if cols else 0
+    if rows == 0:
+        return
+    pz, ldz = _rows(z, cols)
+    if z.dtype != y.dtype:
+        raise ValueError("y and z share a type")
+    w, o, pq, ps = _norm_outputs(rows, cols, y.dtype, weight, out, q, scale)
+    _check("ssd_gated_norm", LIB.ssd_gated_norm(
+        rows, cols, groups, DTYPE_CODE[y.dtype], _expect(y, "y", rows * cols, y.dtype), pz, ldz, w, eps, o,
+        pq, ps, _stream(stream)))
+
+
+def ssd_matmul_i8_workspace_bytes(m, n, k) -> int:
+    return int(LIB.ssd_matmul_i8_workspace_bytes(m, n, k))
+
+
+def ssd_matmul_i8_workspace(m, n, k, device="cuda"):
+    """A workspace for products of this size on ``device`` (None where none is needed)."""
+    need = ssd_matmul_i8_workspace_bytes(m, n, k)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None):
+    """out = a_scale * w_scale * (a @ w.T) + bias for int8 a [..., K], w [N, K]; bias may
+    be None. ``workspace`` is allocated here if None and needed."""
+    n, k = w.shape
+    if a.shape[-1] != k:
+        raise ValueError("a and w must agree in their last dimension")
+    m = a.numel() // k if k else 0
+    if m == 0:
+        return
+    if workspace is None:
+        workspace = ssd_matmul_i8_workspace(m, n, k, out.device)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("ssd_matmul_i8", LIB.ssd_matmul_i8(
+        m, n, k, _expect(a, "a", m * k, torch.int8), _expect(a_scale, "a_scale", m, torch.float32),
+        _expect(w, "w", n * k, torch.int8), _expect(w_scale, "w_scale", n, torch.float32),
+        _expect(bias, "bias", n, torch.float32), DTYPE_CODE[out.dtype], _expect(out, "out", m * n, out.dtype),
+        _p(workspace), wsb, _stream(stream)))
+
+
+def ssd_pack_weight_i8(w: np.ndarray):
+    """Host call: a float32 weight matrix [N, K] as int8 codes [N, K] and steps [N]."""
+    a = np.ascontiguousarray(w, dtype=np.float32)
+    if a.ndim != 2:
+        raise ValueError("the weight must be a matrix [N, K]")
+    q = np.zeros(a.shape, dtype=np.int8)
+    s = np.zeros(a.shape[0], dtype=np.float32)
+    _check("ssd_pack_weight_i8", LIB.ssd_pack_weight_i8(a.shape[0], a.shape[1], a.ctypes.data, q.ctypes.data,
+                                                        s.ctypes.data))
+    return q, s

@@ -18,8 +18,9 @@ OUT = os.path.join(PKG, "libssd.so")
 OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 
 HIP_SOURCES = ["k_modules.hip", "k_fused.hip", "k_fused_i8.hip", "k_chunked_i8.hip", "k_calib.hip",
-               "k_decode.hip", "k_epilogue.hip", "ssd_noalloc.hip"]
-CPP_SOURCES = ["ssd_api.cpp"]
+               "k_decode.hip", "k_epilogue.hip", "ssd_noalloc.hip", "k_conv.hip", "k_conv_decode.hip", "k_norm.hip",
+               "k_matmul_i8.hip"]
+CPP_SOURCES = ["ssd_api.cpp", "ssd_layer_api.cpp"]
 
 ARCH = "gfx950"
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"-I{os.path.join(ROOT, 'include')}", f"-I{HERE}"]

@@ -1,0 +1,219 @@
+// Causal depthwise convolution, SiLU and softplus between In Proj and the SSD:
+//
+//   u_t[c] = sum_{j<W} w[c,j] xbc_{t-W+1+j}[c] + b[c],   x | B | C = u / (1 + exp(-u))
+//   dt_t[h] = softplus(dt_raw_t[h] + dt_bias[h])
+//
+// The work is one read of x | B | C and one write: memory bound. A thread owns
+// 16 bytes of channels and walks T positions down the sequence with the last
+// W - 1 inputs in registers, so every input is read once but for W - 1 rows at
+// the head of each tile (cache hits: the tile before reads them at its end).
+// Rows are loaded kU ahead of their use. The blocks behind those of the
+// convolution compute dt.
+//
+// The ring of the last W inputs is written by the thread that computes its
+// channels' first tile: it alone reads the history, and it reads it first.
+#include "ssd_conv.hpp"
+#include "ssd_launch.hpp"
+
+namespace ssd {
+namespace {
+
+constexpr int kConvThreads = 256;
+constexpr int kU = 4;  // rows in flight per thread
+
+struct ConvFwdArgs {
+  ConvPtrs cv;
+  const int32_t* lengths;
+  void* X;
+  void* Bo;
+  void* Co;
+  void* dt;
+  int64_t B, L;
+  int H, dX, dBC, Cd;  // heads, H*P, G*N, all channels
+  int nvec;            // vectors of a row
+  int T, ntiles;
+  unsigned conv_blocks;
+  int dt_rows;  // rows of one dt block
+};
+
+template <int DT, int W, bool AL>
+__device__ __forceinline__ void conv_tile(const ConvFwdArgs& a, unsigned id) {
+  constexpr int V = RawVec<DT>::V;
+  const unsigned vec = id % (unsigned)a.nvec, rest = id / (unsigned)a.nvec;
+  const int tile = (int)(rest % (unsigned)a.ntiles);
+  const int64_t b = rest / (unsigned)a.ntiles;
+  if (b >= a.B) return;
+  const int c = (int)vec * V;
+  const int64_t t0 = (int64_t)tile * a.T;
+  const int64_t t1 = min(t0 + a.T, a.L);
+  int64_t end = a.L;
+  if (a.lengths) end = min(max((int64_t)a.lengths[b], (int64_t)0), a.L);
+  const int64_t row0 = b * a.L;
+  const int64_t ld = a.cv.ld_xbc;
+
+  // the destination of this vector: x, B and C are multiples of 16 channels wide
+  void* dst;
+  int64_t o, ldo;
+  if (c < a.dX) {
+    dst = a.X; ldo = a.dX; o = c;
+  } else if (c < a.dX + a.dBC) {
+    dst = a.Bo; ldo = a.dBC; o = c - a.dX;
+  } else {
+    dst = a.Co; ldo = a.dBC; o = c - a.dX - a.dBC;
+  }
+  o += row0 * ldo;
+
+  float w[V][W], bias[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[e][j] = a.cv.weight[(int64_t)(c + e) * W + j];
+    bias[e] = a.cv.bias ? a.cv.bias[c + e] : 0.f;
+  }
+
+  // the W - 1 inputs before the tile
+  float win[W - 1][V];
+  const uint32_t p0 = a.cv.pos ? (uint32_t)max(a.cv.pos[b], 0) : 0u;
+  void* const ring = a.cv.state;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int back = W - 1 - j;
+    RawVec<DT> v;
+    v.zero();
+    if (t0 >= back) {
+      v.template load<AL>(a.cv.xbc, (row0 + t0 - back) * ld + c);
+    } else if (p0 + (uint32_t)t0 >= (uint32_t)back) {  // only where pos is given: the ring is too
+      const uint32_t slot = (p0 + (uint32_t)t0 - (uint32_t)back) % W;
+      v.template load<true>(ring, (b * W + slot) * (int64_t)a.Cd + c);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) win[j][e] = v.get(e);
+  }
+
+  RawVec<DT> cur[kU], nxt[kU];
+  auto load_rows = [&](int64_t t, RawVec<DT>* v) {
+#pragma unroll
+    for (int i = 0; i < kU; ++i)
+      v[i].template load<AL>(a.cv.xbc, (row0 + min(t + i, a.L - 1)) * ld + c);
+  };
+  load_rows(t0, cur);
+  for (int64_t t = t0; t < t1; t += kU) {
+    if (t + kU < t1) load_rows(t + kU, nxt);
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = cur[i].get(e);
+        float u = bias[e];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) u = fmaf(w[e][j], win[j][e], u);
+        u = fmaf(w[e][W - 1], x, u);
+        y[e] = silu(u);
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
+        win[W - 2][e] = x;
+      }
+      RawVec<DT> out;
+      out.set(y);
+      if (t + i >= end) out.zero();
+      if (t + i < t1) out.store(dst, o + (t + i) * ldo);
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) cur[i] = nxt[i];
+  }
+
+  if (tile == 0 && ring) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const int64_t t = end - W + j;
+      if (t >= 0) {
+        RawVec<DT> v;
+        v.template load<AL>(a.cv.xbc, (row0 + t) * ld + c);
+        v.store(ring, (b * W + (uint32_t)(p0 + (uint32_t)t) % W) * (int64_t)a.Cd + c);
+      }
+    }
+  }
+}
+
+template <int DT, int W, bool AL>
+__global__ __launch_bounds__(kConvThreads) void k_conv(ConvFwdArgs a) {
+  typedef typename Store<DT>::T T;
+  if (blockIdx.x < a.conv_blocks) {
+    conv_tile<DT, W, AL>(a, blockIdx.x * kConvThreads + threadIdx.x);
+    return;
+  }
+  const int64_t r0 = (int64_t)(blockIdx.x - a.conv_blocks) * a.dt_rows;
+  const int n = (int)min((int64_t)a.dt_rows, a.B * a.L - r0) * a.H;
+  for (int i = threadIdx.x; i < n; i += kConvThreads) {
+    const int64_t row = r0 + (unsigned)i / (unsigned)a.H;
+    const int h = (int)((unsigned)i % (unsigned)a.H);
+    float v = softplus(ld_f<DT>(a.cv.dt_raw, row * a.cv.ld_dt + h) + (a.cv.dt_bias ? a.cv.dt_bias[h] : 0.f));
+    if (a.lengths) {
+      const int64_t b = row / a.L;
+      if (row - b * a.L >= a.lengths[b]) v = 0.f;
+    }
+    ((T*)a.dt)[row * a.H + h] = to_store<DT>(v);
+  }
+}
+
+template <int DT, int W>
+hipError_t launch_w(const ConvFwdArgs& a, bool al, unsigned blocks, hipStream_t st) {
+  if (al)
+    hipLaunchKernelGGL((k_conv<DT, W, true>), dim3(blocks), dim3(kConvThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_conv<DT, W, false>), dim3(blocks), dim3(kConvThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const ConvFwdArgs& a, bool al, unsigned blocks, hipStream_t st) {
+  switch (a.cv.width) {
+    case 2: return launch_w<DT, 2>(a, al, blocks, st);
+    case 3: return launch_w<DT, 3>(a, al, blocks, st);
+    case 4: return launch_w<DT, 4>(a, al, blocks, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_conv_forward(const Dims& d, int dtype, const ConvPtrs& cv, const int32_t* lengths,
+                               void* X, void* B, void* C, void* dt, hipStream_t st) {
+  ConvFwdArgs a{};
+  a.cv = cv;
+  a.lengths = lengths;
+  a.X = X; a.Bo = B; a.Co = C; a.dt = dt;
+  a.B = d.B; a.L = d.L;
+  a.H = d.H;
+  a.dX = d.H * d.P;
+  a.dBC = d.G * d.N;
+  a.Cd = a.dX + 2 * a.dBC;
+  const int esize = dtype == DT_F32 ? 4 : 2;
+  a.nvec = a.Cd / (16 / esize);
+  // Positions per thread: long tiles spread the weights' loads and the window's
+  // head over more rows, short ones give enough threads to fill the chip (16
+  // waves on each of its CUs); never below kU, the rows in flight.
+  const int64_t want = (int64_t)(cu_count() > 0 ? cu_count() : 256) * 16 * kWave;
+  int64_t T = kU;
+  while (T < 32 && d.B * ((d.L + 2 * T - 1) / (2 * T)) * a.nvec >= want) T *= 2;
+  // thread indexes fit 31 bits
+  while (d.B * ((d.L + T - 1) / T) * a.nvec >= (int64_t)1 << 31 && T < d.L) T *= 2;
+  a.T = (int)T;
+  a.ntiles = (int)((d.L + T - 1) / T);
+  a.conv_blocks = (unsigned)((d.B * a.ntiles * (int64_t)a.nvec + kConvThreads - 1) / kConvThreads);
+  const int64_t rows = d.B * d.L;
+  int64_t dt_rows = max((int64_t)1, (int64_t)1024 / d.H);
+  while ((rows + dt_rows - 1) / dt_rows >= (int64_t)1 << 22) dt_rows *= 2;
+  a.dt_rows = (int)dt_rows;
+  const unsigned blocks = a.conv_blocks + (unsigned)((rows + dt_rows - 1) / dt_rows);
+  const bool al = (uintptr_t)cv.xbc % 16 == 0 && cv.ld_xbc * esize % 16 == 0;
+  switch (dtype) {
+    case DT_F32: return launch_dt<DT_F32>(a, al, blocks, st);
+    case DT_F16: return launch_dt<DT_F16>(a, al, blocks, st);
+    case DT_BF16: return launch_dt<DT_BF16>(a, al, blocks, st);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace ssd

@@ -40,40 +40,12 @@ struct DecodeArgs {
   int H, G, hpg;
 };
 
-// Value of lane (L xor M) within each group of 32 lanes (ds_swizzle bit mode).
-template <int M>
-__device__ __forceinline__ int swz(int v) {
-  return __builtin_amdgcn_ds_swizzle(v, (M << 10) | 0x1f);
-}
-
-// Sum over aligned groups of R consecutive lanes (R a power of two <= 32).
-template <int R>
-__device__ __forceinline__ int lane_sum_i(int v) {
-  if constexpr (R >= 2) v += swz<1>(v);
-  if constexpr (R >= 4) v += swz<2>(v);
-  if constexpr (R >= 8) v += swz<4>(v);
-  if constexpr (R >= 16) v += swz<8>(v);
-  if constexpr (R >= 32) v += swz<16>(v);
-  return v;
-}
-template <int R>
-__device__ __forceinline__ float lane_sum_f(float v) {
-  if constexpr (R >= 2) v += __int_as_float(swz<1>(__float_as_int(v)));
-  if constexpr (R >= 4) v += __int_as_float(swz<2>(__float_as_int(v)));
-  if constexpr (R >= 8) v += __int_as_float(swz<4>(__float_as_int(v)));
-  if constexpr (R >= 16) v += __int_as_float(swz<8>(__float_as_int(v)));
-  if constexpr (R >= 32) v += __int_as_float(swz<16>(__float_as_int(v)));
-  return v;
-}
-
 // Low bytes of a, b, c, d packed into one dword (three byte permutes).
 __device__ __forceinline__ uint32_t perm_pack4(int a, int b, int c, int d) {
   const uint32_t lo = __builtin_amdgcn_perm((uint32_t)b, (uint32_t)a, 0x0c0c0400u);
   const uint32_t hi = __builtin_amdgcn_perm((uint32_t)d, (uint32_t)c, 0x0c0c0400u);
   return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
-
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 // LDS of one wave: the per-position vectors of its head.
 template <int P, int NS>

@@ -1,0 +1,62 @@
+// Device helpers of the causal convolution (k_conv.hip, k_conv_decode.hip) and
+// of the row norms (k_norm.hip).
+#pragma once
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+
+// u / (1 + exp(-u)): hardware exp2 and reciprocal, each within one unit in the
+// last place of fp32. exp overflows to infinity below u = -88, where the
+// reciprocal gives the limit 0.
+__device__ __forceinline__ float silu(float u) {
+  return u * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+}
+
+// log(1 + exp(v)) as max(v, 0) + log1p(exp(-|v|)): step sizes of 1e-3 keep
+// their relative precision (log(1 + x) of a small x would lose it).
+__device__ __forceinline__ float softplus(float v) {
+  return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+}
+
+// 16 bytes of consecutive elements as loaded: one access where the rows are
+// 16-byte aligned (AL), element by element otherwise.
+template <int DT>
+struct RawVec {
+  static constexpr int V = DT == DT_F32 ? 4 : 8;
+  typedef uint32_t v4 __attribute__((ext_vector_type(4)));
+  v4 w;
+  __device__ __forceinline__ void zero() { w = (v4){0, 0, 0, 0}; }
+  template <bool AL>
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if constexpr (AL) {
+      w = *(const v4*)((const typename Store<DT>::T*)p + i);
+    } else if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = ((const uint32_t*)p)[i + e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (uint32_t)((const u16*)p)[i + 2 * e] | ((uint32_t)((const u16*)p)[i + 2 * e + 1] << 16);
+    }
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    *(v4*)((typename Store<DT>::T*)p + i) = w;
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (DT == DT_F32) return __uint_as_float(w[e]);
+    else if constexpr (DT == DT_BF16) return __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
+    else return (float)__builtin_bit_cast(_Float16, (u16)((e & 1) ? (w[e >> 1] >> 16) : (w[e >> 1] & 0xffffu)));
+  }
+  __device__ __forceinline__ void set(const float* v) {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = pack2<DT>(v[2 * e], v[2 * e + 1]);
+    }
+  }
+};
+
+}  // namespace ssd

@@ -19,6 +19,7 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint16_t u16;
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 enum { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2 };
 
@@ -309,6 +310,32 @@ __device__ __forceinline__ void glb_frag8(const void* p, int64_t i, FragF<DT>& f
 #pragma unroll
     for (int e = 0; e < 8; ++e) f.v[e] = t[e];
   }
+}
+
+// Value of lane (L xor M) within each group of 32 lanes (ds_swizzle bit mode).
+template <int M>
+__device__ __forceinline__ int swz(int v) {
+  return __builtin_amdgcn_ds_swizzle(v, (M << 10) | 0x1f);
+}
+
+// Sum over aligned groups of R consecutive lanes (R a power of two <= 32).
+template <int R>
+__device__ __forceinline__ int lane_sum_i(int v) {
+  if constexpr (R >= 2) v += swz<1>(v);
+  if constexpr (R >= 4) v += swz<2>(v);
+  if constexpr (R >= 8) v += swz<4>(v);
+  if constexpr (R >= 16) v += swz<8>(v);
+  if constexpr (R >= 32) v += swz<16>(v);
+  return v;
+}
+template <int R>
+__device__ __forceinline__ float lane_sum_f(float v) {
+  if constexpr (R >= 2) v += __int_as_float(swz<1>(__float_as_int(v)));
+  if constexpr (R >= 4) v += __int_as_float(swz<2>(__float_as_int(v)));
+  if constexpr (R >= 8) v += __int_as_float(swz<4>(__float_as_int(v)));
+  if constexpr (R >= 16) v += __int_as_float(swz<8>(__float_as_int(v)));
+  if constexpr (R >= 32) v += __int_as_float(swz<16>(__float_as_int(v)));
+  return v;
 }
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }

@@ -105,6 +105,58 @@ hipError_t launch_epilogue(const Dims& d, int dtype, const void* Y, const float*
 hipError_t launch_mean_correction(const Dims& d, int dtype, const void* Yr, const void* Yq, float* c,
                                   hipStream_t st);
 
+// Causal convolution of the mixer's input (k_conv.hip, k_conv_decode.hip).
+struct ConvPtrs {
+  const float* weight;   // [Cd, width]
+  const float* bias;     // [Cd] or null
+  const float* dt_bias;  // [H] or null
+  int width;
+  const void* xbc;  // rows ld_xbc elements apart
+  int64_t ld_xbc;
+  const void* dt_raw;  // rows ld_dt elements apart
+  int64_t ld_dt;
+  const int32_t* pos;  // [B] or null
+  void* state;         // [B, width, Cd] or null
+};
+hipError_t launch_conv_forward(const Dims& d, int dtype, const ConvPtrs& cv, const int32_t* lengths,
+                               void* X, void* B, void* C, void* dt, hipStream_t st);
+hipError_t launch_conv_decode_step(const Dims& d, int dtype, bool int8, const ConvPtrs& cv,
+                                   const float* A, const float* D, const ScalePtrs& sc, void* state,
+                                   void* Y, hipStream_t st);
+
+// Row norms with 8-bit rows (k_norm.hip). res_dtype is read where residual or
+// residual_out is given; z (gated form) and residual exclude each other.
+struct NormArgs {
+  int64_t rows;
+  int cols, groups;
+  const void* x;
+  int64_t ld_x;
+  const void* z;
+  int64_t ld_z;
+  const void* residual;
+  void* residual_out;
+  const float* weight;
+  float eps;
+  void* out;
+  int8_t* q;
+  float* scale;
+};
+hipError_t launch_norm(int dtype, int res_dtype, const NormArgs& a, hipStream_t st);
+
+// Matrix product in 8-bit integers (k_matmul_i8.hip).
+struct MatmulI8Args {
+  int64_t M, N, K;
+  const int8_t* a;
+  const float* a_scale;
+  const int8_t* w;
+  const float* w_scale;
+  const float* bias;
+  void* out;
+  int32_t* ws;
+};
+size_t matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_matmul_i8(int out_dtype, const MatmulI8Args& a, hipStream_t st);
+
 // Zero fill of a device buffer by a kernel (so that a captured graph holds no
 // memset node); bytes is a multiple of 16 and p 16-byte aligned.
 hipError_t launch_zero_fill(void* p, size_t bytes, hipStream_t st);

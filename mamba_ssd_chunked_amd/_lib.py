@@ -371,42 +371,61 @@ def calibrate(shape_of, seqs, A, device="cuda") -> ScalePack:
 # ---------------------------------------------------------------------------
 
 class ConvParams:
-    """The causal convolution's parameters on the device: weight [Cd, width] (or
+    """The causal convolution's parameters on a GPU: weight [Cd, width] (or
     [Cd, 1, width]), bias [Cd] and dt_bias [H] (either may be None), float32."""
 
     def __init__(self, weight, bias=None, dt_bias=None):
         self.weight = weight.reshape(weight.shape[0], -1)
         self.bias, self.dt_bias = bias, dt_bias
-        for t in (self.weight, bias, dt_bias):
-            if t is not None and t.dtype != torch.float32:
-                raise ValueError("convolution parameters are float32")
+        self.channels, self.width = self.weight.shape
+        self.heads = None if dt_bias is None else dt_bias.numel()
         if bias is not None and bias.numel() != self.channels:
             raise ValueError("bias must hold one value for each channel")
+        for t in (self.weight, bias, dt_bias):
+            if t is not None and (t.dtype is not torch.float32 or not t.is_cuda or t.device != weight.device):
+                raise ValueError("convolution parameters are float32 tensors on one GPU")
+        self.device_index = weight.get_device()
         self.struct = SsdConv(_p(self.weight), _p(bias), _p(dt_bias), self.width)
 
-    @property
-    def channels(self) -> int:
-        return self.weight.shape[0]
 
-    @property
-    def width(self) -> int:
-        return self.weight.shape[1]
-
-
-def _on_gpu(t, name):
-    """Kernels are launched on the current device: a tensor elsewhere is refused."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current GPU, got {t.device}")
+def _current_device() -> int:
+    """The device that kernels are launched on. The checks below run once per call and
+    tensor, in front of launches of a few microseconds: they use the cheap queries."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError) as e:
+        raise ValueError(f"the buffers must be on a GPU: {e}") from None
 
 
-def _rows(t, n):
+def _stream_on(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _dense(t, name, numel, dtype, dev):
+    """Address of a dense buffer of a given size and type on device ``dev`` (None passes:
+    the C call decides)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} values on the current GPU, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows(t, name, n, dtype, dev):
     """Address and row distance of a tensor whose rows of n values lie at equal
     distances (a contiguous tensor, or a slice of the columns of one)."""
-    st, sh = t.stride(), t.shape
-    if sh[-1] != n:
-        raise ValueError(f"rows of {n} values expected, got {sh[-1]}")
+    sh = t.shape
+    if sh[-1] != n or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must hold rows of {n} values of {dtype} on the current GPU, got {tuple(sh)} "
+                         f"{t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), n
+    st = t.stride()
     if n > 1 and st[-1] != 1:
-        raise ValueError("the values of a row must be consecutive")
+        raise ValueError(f"{name}: the values of a row must be consecutive")
     ld, rows = None, 1
     for size, step in zip(reversed(sh[:-1]), reversed(st[:-1])):
         if size == 1:
@@ -414,110 +433,107 @@ def _rows(t, n):
         if ld is None:
             ld = step
         elif step != ld * rows:
-            raise ValueError("rows must lie at equal distances")
+            raise ValueError(f"{name}: rows must lie at equal distances")
         rows *= size
-    _on_gpu(t, "the rows")
-    return t.data_ptr(), n if ld is None else ld
-
-
-def _expect(t, name, numel, dtype):
-    """A dense buffer of a given size and type (None passes: the C call decides)."""
-    if t is None:
-        return None
-    if t.numel() != numel or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor of {numel} values, got {tuple(t.shape)} {t.dtype}")
-    _on_gpu(t, name)
-    return _p(t)
+    # a row on its own, or rows that overlap (an expanded tensor), have no distance of their own
+    if ld is None:
+        ld = n
+    elif ld < n:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), ld
 
 
 _TORCH_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
 
 
-def _conv_inputs(shape, conv, xbc, dt_raw):
+def _conv_dims(shape, conv, xbc, dt_raw):
+    """Channels, type and rows of the convolution's inputs, which must fit the shape."""
     cd = shape.nheads * shape.headdim + 2 * shape.ngroups * shape.dstate
-    td = _TORCH_DTYPE.get(shape.dtype)
-    if conv.channels != cd or (conv.dt_bias is not None and conv.dt_bias.numel() != shape.nheads):
-        raise ValueError(f"the shape has {cd} channels and {shape.nheads} heads, the parameters {conv.channels}")
     n = shape.batch * shape.seqlen
-    if xbc.dtype != td or dt_raw.dtype != td or xbc.numel() != n * cd or dt_raw.numel() != n * shape.nheads:
-        raise ValueError("xbc and dt_raw must hold batch * seqlen rows in the shape's type")
-    if n == 0:
-        return cd, td, (None, cd), (None, shape.nheads)
-    return cd, td, _rows(xbc, cd), _rows(dt_raw, shape.nheads)
+    if conv.channels != cd or (conv.heads is not None and conv.heads != shape.nheads):
+        raise ValueError(f"the shape has {cd} channels and {shape.nheads} heads, the parameters {conv.channels} and "
+                         f"{conv.heads}")
+    if xbc.numel() != n * cd or dt_raw.numel() != n * shape.nheads:
+        raise ValueError(f"xbc and dt_raw must hold {n} rows, got {tuple(xbc.shape)} and {tuple(dt_raw.shape)}")
+    return cd, _TORCH_DTYPE.get(shape.dtype), n
 
 
 def ssd_conv_forward(shape, conv, xbc, dt_raw, X, B, C, dt, conv_state=None, pos=None, lengths=None,
                      stream=None):
     """Causal convolution, SiLU and softplus of prompts. ``xbc`` and ``dt_raw`` may be
     column slices of In Proj's output; ``pos`` and ``lengths`` are int32 [B]."""
-    cd, td, (px, ldx), (pt, ldt) = _conv_inputs(shape, conv, xbc, dt_raw)
-    b, n = shape.batch, shape.batch * shape.seqlen
+    cd, td, n = _conv_dims(shape, conv, xbc, dt_raw)
     if n == 0:
         return  # empty tensors have no addresses
-    bc = n * shape.ngroups * shape.dstate
+    dev = _current_device()
+    if conv.device_index != dev:
+        raise ValueError("the convolution's parameters must be on the current GPU")
+    px, ldx = _rows(xbc, "xbc", cd, td, dev)
+    pt, ldt = _rows(dt_raw, "dt_raw", shape.nheads, td, dev)
+    b, bc = shape.batch, n * shape.ngroups * shape.dstate
     _check("ssd_conv_forward", LIB.ssd_conv_forward(
         ctypes.byref(shape), ctypes.byref(conv.struct), px, ldx, pt, ldt,
-        _expect(lengths, "lengths", b, torch.int32), _expect(pos, "pos", b, torch.int32),
-        _expect(conv_state, "conv_state", b * conv.width * cd, td),
-        _expect(X, "X", n * shape.nheads * shape.headdim, td), _expect(B, "B", bc, td), _expect(C, "C", bc, td),
-        _expect(dt, "dt", n * shape.nheads, td), _stream(stream)))
+        _dense(lengths, "lengths", b, torch.int32, dev), _dense(pos, "pos", b, torch.int32, dev),
+        _dense(conv_state, "conv_state", b * conv.width * cd, td, dev),
+        _dense(X, "X", n * shape.nheads * shape.headdim, td, dev), _dense(B, "B", bc, td, dev),
+        _dense(C, "C", bc, td, dev), _dense(dt, "dt", n * shape.nheads, td, dev), _stream_on(stream, dev)))
 
 
 def ssd_conv_decode_step(shape, path, conv, xbc, dt_raw, A, D, scales, conv_state, pos, state, Y,
                          stream=None):
     """One position of the convolution and the SSD: ``conv_state`` and ``state`` are
     updated in place, ``pos`` (int32 [B]) is left for the caller to advance."""
-    cd, td, (px, ldx), (pt, ldt) = _conv_inputs(shape, conv, xbc, dt_raw)
-    b, hp = shape.batch, shape.nheads * shape.headdim
+    cd, td, b = _conv_dims(shape, conv, xbc, dt_raw)
     if b == 0:
         return
+    dev = _current_device()
+    if conv.device_index != dev:
+        raise ValueError("the convolution's parameters must be on the current GPU")
+    h = shape.nheads
+    px, ldx = _rows(xbc, "xbc", cd, td, dev)
+    pt, ldt = _rows(dt_raw, "dt_raw", h, td, dev)
+    hp = b * h * shape.headdim
     _check("ssd_conv_decode_step", LIB.ssd_conv_decode_step(
         ctypes.byref(shape), path, ctypes.byref(conv.struct), px, ldx, pt, ldt,
-        _expect(A, "A", shape.nheads, torch.float32), _expect(D, "D", shape.nheads, torch.float32),
-        _scales(scales), _expect(conv_state, "conv_state", b * conv.width * cd, td),
-        _expect(pos, "pos", b, torch.int32),
-        _expect(state, "state", b * hp * shape.dstate, torch.int8 if path == SSD_PATH_INT8 else torch.float32),
-        _expect(Y, "Y", b * hp, td), _stream(stream)))
-
-
-def _norm_outputs(rows, cols, dtype, weight, out, q, scale):
-    return (_expect(weight, "weight", cols, torch.float32), _expect(out, "out", rows * cols, dtype),
-            _expect(q, "q", rows * cols, torch.int8), _expect(scale, "scale", rows, torch.float32))
+        _dense(A, "A", h, torch.float32, dev), _dense(D, "D", h, torch.float32, dev), _scales(scales),
+        _dense(conv_state, "conv_state", b * conv.width * cd, td, dev), _dense(pos, "pos", b, torch.int32, dev),
+        _dense(state, "state", hp * shape.dstate, torch.int8 if path == SSD_PATH_INT8 else torch.float32, dev),
+        _dense(Y, "Y", hp, td, dev), _stream_on(stream, dev)))
 
 
 def ssd_add_norm(x, residual, residual_out, weight, eps, out=None, q=None, scale=None, stream=None):
     """r = x + residual, RMSNorm of r's rows; the rows in ``out`` and as codes ``q`` with
     a step ``scale`` each. ``x`` may be a column slice; ``residual`` and
     ``residual_out`` share a type, x's or float32 (either may be None)."""
-    cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
-    if rows == 0:
+    cols, td, n = x.shape[-1], x.dtype, x.numel()
+    if n == 0:
         return
-    px, ldx = _rows(x, cols)
-    kept = residual if residual is not None else residual_out
-    rt = x.dtype if kept is None else kept.dtype
-    w, o, pq, ps = _norm_outputs(rows, cols, x.dtype, weight, out, q, scale)
+    dev = _current_device()
+    rows = n // cols
+    px, ldx = _rows(x, "x", cols, td, dev)
+    rt = td if residual is None and residual_out is None else (residual_out if residual is None else residual).dtype
     _check("ssd_add_norm", LIB.ssd_add_norm(
-        rows, cols, DTYPE_CODE[x.dtype], px, ldx, _expect(residual, "residual", rows * cols, rt),
-        DTYPE_CODE[rt], _expect(residual_out, "residual_out", rows * cols, rt), w, eps, o, pq, ps,
-        _stream(stream)))
+        rows, cols, DTYPE_CODE[td], px, ldx, _dense(residual, "residual", n, rt, dev), DTYPE_CODE[rt],
+        _dense(residual_out, "residual_out", n, rt, dev), _dense(weight, "weight", cols, torch.float32, dev), eps,
+        _dense(out, "out", n, td, dev), _dense(q, "q", n, torch.int8, dev),
+        _dense(scale, "scale", rows, torch.float32, dev), _stream_on(stream, dev)))
 
 
 def ssd_gated_norm(y, z, groups, weight, eps, out=None, q=None, scale=None, stream=None):
     """RMSNorm over each of ``groups`` runs of channels of y * silu(z); outputs as
     ``ssd_add_norm``. ``z`` may be a column slice of In Proj's output. The row
     length is z's last dimension."""
-    cols = z.shape[-1]
-    rows = z.numel() // cols if cols else 0
-    if rows == 0:
+    cols, td, n = z.shape[-1], y.dtype, z.numel()
+    if n == 0:
         return
-    pz, ldz = _rows(z, cols)
-    if z.dtype != y.dtype:
-        raise ValueError("y and z share a type")
-    w, o, pq, ps = _norm_outputs(rows, cols, y.dtype, weight, out, q, scale)
+    dev = _current_device()
+    rows = n // cols
+    pz, ldz = _rows(z, "z", cols, td, dev)
     _check("ssd_gated_norm", LIB.ssd_gated_norm(
-        rows, cols, groups, DTYPE_CODE[y.dtype], _expect(y, "y", rows * cols, y.dtype), pz, ldz, w, eps, o,
-        pq, ps, _stream(stream)))
+        rows, cols, groups, DTYPE_CODE[td], _dense(y, "y", n, td, dev), pz, ldz,
+        _dense(weight, "weight", cols, torch.float32, dev), eps, _dense(out, "out", n, td, dev),
+        _dense(q, "q", n, torch.int8, dev), _dense(scale, "scale", rows, torch.float32, dev),
+        _stream_on(stream, dev)))
 
 
 def ssd_matmul_i8_workspace_bytes(m, n, k) -> int:
@@ -539,14 +555,16 @@ def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None
     m = a.numel() // k if k else 0
     if m == 0:
         return
+    dev = _current_device()
     if workspace is None:
-        workspace = ssd_matmul_i8_workspace(m, n, k, out.device)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        workspace = ssd_matmul_i8_workspace(m, n, k, a.device)
+    wsb = 0 if workspace is None else workspace.numel()
+    pw = _dense(workspace, "workspace", wsb, torch.uint8, dev)
     _check("ssd_matmul_i8", LIB.ssd_matmul_i8(
-        m, n, k, _expect(a, "a", m * k, torch.int8), _expect(a_scale, "a_scale", m, torch.float32),
-        _expect(w, "w", n * k, torch.int8), _expect(w_scale, "w_scale", n, torch.float32),
-        _expect(bias, "bias", n, torch.float32), DTYPE_CODE[out.dtype], _expect(out, "out", m * n, out.dtype),
-        _p(workspace), wsb, _stream(stream)))
+        m, n, k, _dense(a, "a", m * k, torch.int8, dev), _dense(a_scale, "a_scale", m, torch.float32, dev),
+        _dense(w, "w", n * k, torch.int8, dev), _dense(w_scale, "w_scale", n, torch.float32, dev),
+        _dense(bias, "bias", n, torch.float32, dev), DTYPE_CODE[out.dtype],
+        _dense(out, "out", m * n, out.dtype, dev), pw, wsb, _stream_on(stream, dev)))
 
 
 def ssd_pack_weight_i8(w: np.ndarray):

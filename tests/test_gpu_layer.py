@@ -470,7 +470,8 @@ def test_norms_in_place_and_empty(gpu_lib):
 MM = [(1, 1, 16), (1, 17, 64), (2, 64, 48), (7, 100, 5120), (8, 2560, 5120), (15, 33, 144), (16, 256, 2560),
       (17, 300, 272), (33, 129, 1040), (63, 64, 64), (65, 1000, 128), (100, 80, 8192), (128, 512, 4096),
       (130, 2568, 2560), (256, 256, 640), (257, 259, 656), (333, 8512, 2048), (1000, 777, 1024), (2048, 10576, 272),
-      (3001, 130, 2560), (4096, 2560, 5120)]
+      (3001, 130, 2560), (4096, 2560, 5120), (4100, 2061, 400),
+      (4096, 2048, 48), (3001, 4000, 656)]
 
 
 @pytest.mark.parametrize("M,N,K", MM)

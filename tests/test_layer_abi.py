@@ -185,20 +185,30 @@ def test_pack_weight():
 
 
 def test_binding_refuses_what_the_library_cannot_see():
-    """Host tensors, wrong sizes and types, and rows at unequal distances."""
+    """Host tensors, wrong sizes and types, rows at unequal distances or that overlap.
+    (-1 stands for a host tensor's device, so that the other checks are met here.)"""
     x = torch.zeros(4, 64, dtype=torch.float16)
     w = torch.ones(64)
     with pytest.raises(ValueError):
         L.ssd_add_norm(x, None, None, w, 1e-5, torch.zeros_like(x))  # not on a GPU
-    with pytest.raises(ValueError):
-        L._rows(torch.zeros(4, 64).t(), 4)
-    with pytest.raises(ValueError):
-        L._rows(torch.zeros(4, 6, 64, device="meta")[:, :5], 64)
-    with pytest.raises(ValueError):
-        L._rows(torch.zeros(4, 64, device="meta"), 63)
-    with pytest.raises(ValueError):
-        L._expect(torch.zeros(63, device="meta"), "w", 64, torch.float32)
-    with pytest.raises(ValueError):
-        L._expect(torch.zeros(64, device="meta", dtype=torch.float16), "w", 64, torch.float32)
-    with pytest.raises(ValueError):
-        L.ConvParams(torch.zeros(96, 4, dtype=torch.float16))
+    f = torch.float32
+    assert L._rows(w.view(1, 64), "x", 64, f, -1) == (w.data_ptr(), 64)
+    wide = torch.zeros(4, 6, 100)
+    assert L._rows(wide[:, :, 3:67], "x", 64, f, -1) == (wide.data_ptr() + 12, 100)
+    assert L._rows(wide[:, 0, 3:67], "x", 64, f, -1) == (wide.data_ptr() + 12, 600)
+    assert L._rows(wide[2:3, 1:2, 3:67], "x", 64, f, -1) == (wide[2, 1, 3:].data_ptr(), 64)
+    for t, n, dt, dev, words in ((torch.zeros(4, 64).t(), 4, f, -1, "consecutive"),
+                                 (wide[:, :5, 3:67], 64, f, -1, "equal distances"),
+                                 (w.expand(4, 64), 64, f, -1, "overlap"),
+                                 (wide, 64, f, -1, "rows of 64"), (wide, 100, torch.float16, -1, "float16"),
+                                 (wide, 100, f, 0, "current GPU")):
+        with pytest.raises(ValueError, match=words):
+            L._rows(t, "x", n, dt, dev)
+    assert L._dense(None, "w", 64, f, -1) is None
+    assert L._dense(w, "w", 64, f, -1) == w.data_ptr()
+    for t, n, dt, dev in ((w, 63, f, -1), (w, 64, torch.int8, -1), (w, 64, f, 0), (wide.transpose(0, 1), 2400, f, -1)):
+        with pytest.raises(ValueError, match="contiguous"):
+            L._dense(t, "w", n, dt, dev)
+    for bad in (torch.zeros(96, 4, dtype=torch.float16), torch.zeros(96, 4)):
+        with pytest.raises(ValueError, match="float32 tensors on one GPU"):
+            L.ConvParams(bad)

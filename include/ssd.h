@@ -418,7 +418,7 @@ int ssd_gated_norm(int64_t rows, int64_t cols, int64_t groups, int dtype, const 
  * each row (output channel), bias [N] fp32 (may be NULL; at Out Proj it carries
  * the mean correction of "Key design 4"), out [M, N] in out_dtype. K is a
  * multiple of 16 (SSD_E_UNSUPPORTED) and at most 131056 (so that the sums of any
- * codes fit), M, N <= 2^31 - 1; M == 0 is a valid empty problem. workspace: device memory
+ * codes fit), M, N < 2^26 and M * N < 2^40; M == 0 is a valid empty problem. workspace: device memory
  * of at least ssd_matmul_i8_workspace_bytes(M, N, K) bytes (may be NULL when
  * that is 0); calls that may overlap need one each. */
 int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float* a_scale,

@@ -144,7 +144,9 @@ int ssd_gated_norm(int64_t rows, int64_t cols, int64_t groups, int dtype, const 
 // M, N, K of the 8-bit product. The largest sum, K products of -128 * -128,
 // fits an int32 up to K = 131056.
 static int check_matmul(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > 131056) return SSD_E_SHAPE;
+  constexpr int64_t kMost = (int64_t)1 << 26;  // rows: tile indexes and offsets in a tile's rows fit 32 bits
+  if (M < 0 || N <= 0 || K <= 0 || M >= kMost || N >= kMost || K > 131056) return SSD_E_SHAPE;
+  if (M * N >= (int64_t)1 << 40) return SSD_E_SHAPE;
   if (K % 16 != 0) return SSD_E_UNSUPPORTED;
   return SSD_OK;
 }

@@ -141,8 +141,9 @@ def mm(m=0, n=16, k=64, a=A16, sa=A16, w=A16, sw=A16, bias=None, dtype=1, out=A1
 
 def test_matmul_refusals():
     assert mm() == L.SSD_OK and mm(bias=MIS) == L.SSD_OK
-    assert mm(m=-1) == L.SSD_E_SHAPE and mm(m=1 << 31) == L.SSD_E_SHAPE
-    assert mm(n=0) == L.SSD_E_SHAPE and mm(n=1 << 31) == L.SSD_E_SHAPE
+    assert mm(m=-1) == L.SSD_E_SHAPE and mm(m=1 << 26) == L.SSD_E_SHAPE
+    assert mm(n=0) == L.SSD_E_SHAPE and mm(n=1 << 26) == L.SSD_E_SHAPE
+    assert mm(m=1 << 20, n=1 << 20) == L.SSD_E_SHAPE
     assert mm(k=0) == L.SSD_E_SHAPE and mm(k=131072) == L.SSD_E_SHAPE and mm(k=131056) == L.SSD_OK
     for k in (1, 8, 24, 100):
         assert mm(k=k) == L.SSD_E_UNSUPPORTED

@@ -9,13 +9,16 @@
 // group share in the caches), so a large batch is bound by HBM and a small one
 // by the latency of one pass.
 //
-// A workgroup of four waves per (batch, head). Its 16-byte slices of the state
-// are requested first; then each thread computes the convolution of one or two
-// of the P + 2 N channels that the head needs, into LDS. All W slots of the
-// ring are loaded, and matched with their weights once pos has arrived, so the
-// prologue costs one memory round trip, not two. The slot pos % W is written
-// by the head itself for its x channels and by the first head of a group for
-// B and C; nobody reads that slot's value, so heads need no order.
+// A workgroup of four waves takes HB heads of a group: one where heads are few
+// or large, up to 8 small ones otherwise (32 KB of state), so that the
+// convolution of B and C is done for all of them and no workgroup is over
+// before it has begun. Its 16-byte slices of the state are requested first; then
+// each thread computes the convolution of one or two of the HB P + 2 N channels
+// that the heads need, into LDS. All W slots of the ring are loaded, and matched
+// with their weights once pos has arrived, so the prologue costs one memory
+// round trip, not two. The slot pos % W is written by the head itself for its x
+// channels and by the first heads of a group for B and C; nobody reads that
+// slot's value, so workgroups need no order.
 #include "ssd_conv.hpp"
 #include "ssd_launch.hpp"
 
@@ -32,35 +35,48 @@ struct StepArgs {
   void* state;
   void* Y;
   int H, G, hpg, Cd;
+  int blocks;  // workgroups of a group of a sequence
 };
 
-// The head's vectors after the convolution.
-template <int P, int NS>
+// A state row's numbers after the convolution.
+struct RowF {
+  float decay, dx, Dx, unused;  // exp(dt A), dt x, D x
+};
+struct RowI8 {
+  float qx, M, f, g;  // float(Q(Xs)), M_req, exp(dt A) s_C s_S, s_C s_B dt x
+  float Dx;
+  int qd;             // Q(Decay)
+  float unused[2];
+};
+template <bool I8>
+struct RowOf { typedef RowF T; };
+template <>
+struct RowOf<true> { typedef RowI8 T; };
+
+template <bool I8, int ROWS, int NS>
 struct StepLds {
-  float x[P];
-  float bc[2 * NS];     // B, then C
-  float4 rv[P];         // INT8, per state row: float(Q(Xs)), M_req, x, exp(dt A) s_C s_S
-  float qb[NS];         // INT8: float(Q(B))
-  int8_t qc[NS];        // INT8: Q(C)
-  int cb[4];            // INT8: Q(B) . Q(C), a part of each wave
+  typename RowOf<I8>::T row[ROWS];
+  float b[NS], c[NS];  // B, C (INT8: float(Q(B)))
+  int8_t qc[NS];       // INT8: Q(C)
 };
 
 // One channel's convolution: the new input, the ring's W slots and the weights,
-// loaded before any of them is used.
+// loaded as they lie (no load is conditional and none is converted here, so that
+// none is waited for before all of them are under way).
 template <int DT>
 struct ConvLane {
-  float slot[4], w[4], bias, x;
-  typename Store<DT>::T raw;
+  typedef typename Store<DT>::T T;
+  T raw, slot[4];
+  float w[4], bias;
   __device__ __forceinline__ void load(const StepArgs& a, int64_t b, int c, int W) {
-    raw = ((const typename Store<DT>::T*)a.cv.xbc)[b * a.cv.ld_xbc + c];
+    raw = ((const T*)a.cv.xbc)[b * a.cv.ld_xbc + c];
     const int64_t r = b * W * (int64_t)a.Cd + c;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      slot[s] = s < W ? ld_f<DT>(a.cv.state, r + (int64_t)s * a.Cd) : 0.f;
-      w[s] = s < W ? a.cv.weight[(int64_t)c * W + s] : 0.f;
+    for (int s = 0; s < 4; ++s) {  // W of them; the rest repeat the last
+      slot[s] = ((const T*)a.cv.state)[r + (int64_t)min(s, W - 1) * a.Cd];
+      w[s] = a.cv.weight[(int64_t)c * W + min(s, W - 1)];
     }
     bias = a.cv.bias ? a.cv.bias[c] : 0.f;
-    x = Store<DT>::to_f(raw);
   }
   // cur = pos % W; slots of positions before the sequence's start count as zero
   __device__ __forceinline__ float value(int W, uint32_t pos, int cur) const {
@@ -69,81 +85,113 @@ struct ConvLane {
     for (int back = 3; back >= 1; --back) {
       if (back < W) {
         const int s = cur >= back ? cur - back : cur - back + W;
-        const float v = s == 0 ? slot[0] : s == 1 ? slot[1] : s == 2 ? slot[2] : slot[3];
+        const float v = Store<DT>::to_f(s == 0 ? slot[0] : s == 1 ? slot[1] : s == 2 ? slot[2] : slot[3]);
         const float wt = W == 4 ? w[3 - back] : W == 3 ? w[(2 - back) & 3] : w[(1 - back) & 3];
         if (pos >= (uint32_t)back) u = fmaf(wt, v, u);
       }
     }
     const float wt = W == 4 ? w[3] : W == 3 ? w[2] : w[1];
-    return silu(fmaf(wt, x, u));
+    return silu(fmaf(wt, Store<DT>::to_f(raw), u));
   }
 };
 
-template <bool I8, int DT, int P, int NS>
+// Q(Decay) = min(128, RHAZ(128 exp(dt A))), decided in float64: float32 settles
+// it unless it lies within 1e-3 of a border between two codes (its error is
+// below 1e-4 for every decay up to 1).
+__device__ __forceinline__ int quant_decay(float dt, float A) {
+  const float v = 128.f * __expf(dt * A), n = floorf(v + 0.5f);
+  if (fabsf(fabsf(v - n) - 0.5f) > 1e-3f && v < 128.25f) return (int)fminf(n, 128.f);
+  return (int)fmin(round(exp((double)dt * (double)A) * 128.0), 128.0);
+}
+
+template <bool I8, int DT, int P, int NS, int HB>
 __global__ __launch_bounds__(kStepThreads) void k_conv_decode(StepArgs a) {
   typedef typename Store<DT>::T T;
   constexpr int R = NS / (I8 ? 16 : 4);                             // 16-byte slices of a state row
-  constexpr int SLOTS = P * R;                                      // of the head
+  constexpr int ROWS = HB * P;                                      // state rows of the workgroup
+  constexpr int SLOTS = ROWS * R;
   constexpr int ITER = (SLOTS + kStepThreads - 1) / kStepThreads;   // of a thread
-  constexpr int NCH = P + 2 * NS;
+  constexpr int NCH = ROWS + 2 * NS;
   constexpr int CIT = (NCH + kStepThreads - 1) / kStepThreads;
-  __shared__ __attribute__((aligned(16))) StepLds<P, NS> L;
+  __shared__ __attribute__((aligned(16))) StepLds<I8, ROWS, NS> L;
 
   const int tid = threadIdx.x;
-  const int64_t unit = blockIdx.x;
-  const int64_t b = unit / a.H;
-  const int h = (int)(unit % a.H);
-  const int g = h / a.hpg;
-  v4u* const st = (v4u*)a.state + unit * (int64_t)SLOTS;
+  // (batch, group, block of heads)
+  const unsigned bg = blockIdx.x / (unsigned)a.blocks, blk = blockIdx.x % (unsigned)a.blocks;
+  const int64_t b = bg / (unsigned)a.G;
+  const int g = (int)(bg % (unsigned)a.G);
+  const int h0 = g * a.hpg + (int)blk * HB;
+  const int rows = HB == 1 ? ROWS : min(HB, a.hpg - (int)blk * HB) * P;
+  const int slots = HB == 1 ? SLOTS : rows * R;
+  const int64_t row0 = (b * a.H + h0) * P;  // of the state and of Y
+  const int x0 = h0 * P;                    // the first x channel
+  v4u* const st = (v4u*)a.state + row0 * R;
 
   v4u hv[ITER];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    const int s = tid + i * kStepThreads;
-    if (SLOTS % kStepThreads == 0 || s < SLOTS) hv[i] = __builtin_nontemporal_load(&st[s]);
+    // behind the last slot: the last one's value, used by nobody (no branch)
+    hv[i] = __builtin_nontemporal_load(&st[min(tid + i * kStepThreads, slots - 1)]);
   }
 
+  // channels of B, C, then x; everything they need is requested here
   const int W = a.cv.width;
   const int dX = a.H * P, dBC = a.G * NS;
+  const int nch = 2 * NS + rows;
   ConvLane<DT> cl[CIT];
+  typename Store<DT>::T dtr[CIT];
+  float dtb[CIT], Av[CIT], Dv[CIT], k0[CIT], k1[CIT], k2[CIT];
   int ch[CIT];
+  float sC = 0.f, sB = 0.f;
+  if constexpr (I8) {
+    sC = a.sc.s_C[g];
+    sB = a.sc.s_B[g];
+  }
 #pragma unroll
   for (int i = 0; i < CIT; ++i) {
-    const int k = tid + i * kStepThreads;  // B, C, then x
-    ch[i] = k < NS ? dX + g * NS + k : k < 2 * NS ? dX + dBC + g * NS + (k - NS) : h * P + (k - 2 * NS);
-    if (k < NCH) cl[i].load(a, b, ch[i], W);
+    // threads behind the last channel, and those of B and C in the x part, load
+    // what a neighbour does
+    const int k = min(tid + i * kStepThreads, nch - 1), xr = max(k - 2 * NS, 0);
+    ch[i] = k < NS ? dX + g * NS + k : k < 2 * NS ? dX + dBC + g * NS + (k - NS) : x0 + xr;
+    cl[i].load(a, b, ch[i], W);
+    const int h = HB == 1 ? h0 : h0 + xr / P;
+    dtr[i] = ((const T*)a.cv.dt_raw)[b * a.cv.ld_dt + h];
+    dtb[i] = a.cv.dt_bias ? a.cv.dt_bias[h] : 0.f;
+    Av[i] = a.A[h];
+    Dv[i] = a.D[h];
+    if constexpr (I8) {
+      k0[i] = *(k < NS ? a.sc.inv_B + g : k < 2 * NS ? a.sc.inv_C + g : a.sc.inv_X + x0 + xr);
+      k1[i] = a.sc.M_req[x0 + xr];
+      k2[i] = a.sc.s_S[x0 + xr];
+    }
   }
   const uint32_t pos = (uint32_t)max(a.cv.pos[b], 0);
   const int cur = (int)(pos % (uint32_t)W);
-  const float Ah = a.A[h], Dh = a.D[h];
-  const float dtv = softplus(ld_f<DT>(a.cv.dt_raw, b * a.cv.ld_dt + h) + (a.cv.dt_bias ? a.cv.dt_bias[h] : 0.f));
-  const float decay = __expf(dtv * Ah);
-  float sC = 0.f;
-  if constexpr (I8) sC = a.sc.s_C[g];
 
 #pragma unroll
   for (int i = 0; i < CIT; ++i) {
     const int k = tid + i * kStepThreads;
-    if (k < NCH) {
+    if (k < nch) {
       const float v = cl[i].value(W, pos, cur);
       if (k < 2 * NS) {
         if constexpr (I8) {
-          if (k < NS) L.qb[k] = (float)q8(__fmul_rn(v, a.sc.inv_B[g]));
-          else L.qc[k - NS] = (int8_t)q8(__fmul_rn(v, a.sc.inv_C[g]));
+          const int q = q8(__fmul_rn(v, k0[i]));
+          if (k < NS) L.b[k] = (float)q;
+          else L.qc[k - NS] = (int8_t)q;
         } else {
-          L.bc[k] = v;
+          if (k < NS) L.b[k] = v;
+          else L.c[k - NS] = v;
         }
       } else {
-        const int p = k - 2 * NS;
-        if constexpr (I8) {
-          const int hp = h * P + p;
-          const float qx = (float)q8(__fmul_rn(__fmul_rn(dtv, v), a.sc.inv_X[hp]));
-          L.rv[p] = make_float4(qx, a.sc.M_req[hp], v, decay * sC * a.sc.s_S[hp]);
-        } else {
-          L.x[p] = v;
-        }
+        const float dt = softplus(Store<DT>::to_f(dtr[i]) + dtb[i]);
+        const float decay = __expf(dt * Av[i]);
+        if constexpr (I8)
+          L.row[k - 2 * NS] = RowI8{(float)q8(__fmul_rn(__fmul_rn(dt, v), k0[i])), k1[i], decay * sC * k2[i],
+                                    sC * sB * dt * v, Dv[i] * v, quant_decay(dt, Av[i]), {0.f, 0.f}};
+        else
+          L.row[k - 2 * NS] = RowF{decay, dt * v, Dv[i] * v, 0.f};
       }
-      if (k >= 2 * NS || h % a.hpg == 0) ((T*)a.cv.state)[(b * W + cur) * (int64_t)a.Cd + ch[i]] = cl[i].raw;
+      if (k >= 2 * NS || blk == 0) ((T*)a.cv.state)[(b * W + cur) * (int64_t)a.Cd + ch[i]] = cl[i].raw;
     }
   }
   __syncthreads();
@@ -155,27 +203,25 @@ __global__ __launch_bounds__(kStepThreads) void k_conv_decode(StepArgs a) {
 #pragma unroll
     for (int n = 0; n < (NS + kWave - 1) / kWave; ++n) {
       const int k = lane_id() + n * kWave;
-      if (NS % kWave == 0 || k < NS) cb += (int)L.qb[k] * (int)L.qc[k];
+      if (NS % kWave == 0 || k < NS) cb += (int)L.b[k] * (int)L.qc[k];
     }
     cb = lane_sum_i<32>(cb);
     cb += __shfl_xor(cb, 32);
-    const int qd = (int)fmin(round(exp((double)dtv * (double)Ah) * 128.0), 128.0);
     float fb[16];
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
-      const float4 v = *(const float4*)&L.qb[16 * col + e];
+      const float4 v = *(const float4*)&L.b[16 * col + e];
       fb[e] = v.x; fb[e + 1] = v.y; fb[e + 2] = v.z; fb[e + 3] = v.w;
     }
     const uint4 qcv = *(const uint4*)&L.qc[16 * col];
     const uint32_t qcw[4] = {qcv.x, qcv.y, qcv.z, qcv.w};
-    const float ydiag = (float)cb * sC * a.sc.s_B[g] * dtv;
-    const v2s qd2 = {(short)qd, (short)qd};
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int s = tid + i * kStepThreads;
-      const bool ok = SLOTS % kStepThreads == 0 || s < SLOTS;
+      const bool ok = s < slots;
       const int row = ok ? s / R : 0;
-      const float4 rv = L.rv[row];
+      const RowI8 rv = L.row[row];
+      const v2s qd2 = {(short)rv.qd, (short)rv.qd};
       uint32_t nw[4];
       int acc = 0;
 #pragma unroll
@@ -183,7 +229,7 @@ __global__ __launch_bounds__(kStepThreads) void k_conv_decode(StepArgs a) {
         const uint32_t hw = hv[i][j];
         float c[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = q8_pre(__fmul_rn(__fmul_rn(rv.x, fb[4 * j + e]), rv.y));
+        for (int e = 0; e < 4; ++e) c[e] = q8_pre(__fmul_rn(__fmul_rn(rv.qx, fb[4 * j + e]), rv.M));
         const v2s s01 = cvt_pair(c[0], c[1]), s23 = cvt_pair(c[2], c[3]);
         const v2s r01 = rsh7_pair(qd2, unpack_pair(hw, 0x010c000cu));
         const v2s r23 = rsh7_pair(qd2, unpack_pair(hw, 0x030c020cu));
@@ -193,56 +239,70 @@ __global__ __launch_bounds__(kStepThreads) void k_conv_decode(StepArgs a) {
       if (ok) __builtin_nontemporal_store((v4u){nw[0], nw[1], nw[2], nw[3]}, &st[s]);
       acc = lane_sum_i<R>(acc);
       if (ok && col == 0)
-        ((T*)a.Y)[unit * P + row] = to_store<DT>((float)acc * rv.w + ydiag * rv.z + Dh * rv.z);
+        ((T*)a.Y)[row0 + row] = to_store<DT>((float)acc * rv.f + (float)cb * rv.g + rv.Dx);
     }
   } else {
-    const float4 bv = *(const float4*)&L.bc[4 * col];
-    const float4 cv = *(const float4*)&L.bc[NS + 4 * col];
+    const float4 bv = *(const float4*)&L.b[4 * col];
+    const float4 cv = *(const float4*)&L.c[4 * col];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int s = tid + i * kStepThreads;
-      const bool ok = SLOTS % kStepThreads == 0 || s < SLOTS;
+      const bool ok = s < slots;
       const int row = ok ? s / R : 0;
-      const float xv = L.x[row], dx = dtv * xv;
+      const RowF rv = L.row[row];
       const v4f o = __builtin_bit_cast(v4f, hv[i]);
       v4f n;
-      n[0] = fmaf(decay, o[0], dx * bv.x);
-      n[1] = fmaf(decay, o[1], dx * bv.y);
-      n[2] = fmaf(decay, o[2], dx * bv.z);
-      n[3] = fmaf(decay, o[3], dx * bv.w);
+      n[0] = fmaf(rv.decay, o[0], rv.dx * bv.x);
+      n[1] = fmaf(rv.decay, o[1], rv.dx * bv.y);
+      n[2] = fmaf(rv.decay, o[2], rv.dx * bv.z);
+      n[3] = fmaf(rv.decay, o[3], rv.dx * bv.w);
       if (ok) __builtin_nontemporal_store(__builtin_bit_cast(v4u, n), &st[s]);
       const float acc = lane_sum_f<R>(cv.x * n[0] + cv.y * n[1] + cv.z * n[2] + cv.w * n[3]);
-      if (ok && col == 0) ((T*)a.Y)[unit * P + row] = to_store<DT>(acc + Dh * xv);
+      if (ok && col == 0) ((T*)a.Y)[row0 + row] = to_store<DT>(acc + rv.Dx);
     }
   }
 }
 
-template <int DT, int P, int NS>
-hipError_t launch_n(bool int8, const StepArgs& a, unsigned units, hipStream_t st) {
-  if (int8)
-    hipLaunchKernelGGL((k_conv_decode<true, DT, P, NS>), dim3(units), dim3(kStepThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_conv_decode<false, DT, P, NS>), dim3(units), dim3(kStepThreads), 0, st, a);
+template <bool I8, int DT, int P, int NS, int HB>
+hipError_t launch_hb(StepArgs& a, int64_t bg, hipStream_t st) {
+  a.blocks = (a.hpg + HB - 1) / HB;
+  hipLaunchKernelGGL((k_conv_decode<I8, DT, P, NS, HB>), dim3((unsigned)(bg * a.blocks)), dim3(kStepThreads), 0, st, a);
   return hipGetLastError();
 }
 
+// A workgroup takes a head; where the heads are more than 6 on each CU, as many
+// as make 32 KB of state. Measured, one head against several: 114 heads of
+// 16 x 32 fp32 at batch 256 97 and 31 us, at batch 4 (1.8 heads on each CU) 4.3
+// and 4.3; 108 heads of 32 x 32 fp32 at batch 256 103 and 55 us, at batch 4 4.3
+// and 6.8. (A part of a head for each workgroup, where heads are fewer than CUs,
+// gained nothing at 64 x 128.)
+template <bool I8, int DT, int P, int NS>
+hipError_t launch_n(StepArgs& a, int64_t B, hipStream_t st) {
+  constexpr int kMost = 2048 / (P * NS / (I8 ? 16 : 4));
+  constexpr int HB = kMost < 1 ? 1 : kMost > 8 ? 8 : kMost;
+  const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
+  if constexpr (HB > 1)
+    if (B * a.H > 6 * ncu && a.hpg > 1) return launch_hb<I8, DT, P, NS, HB>(a, B * a.G, st);
+  return launch_hb<I8, DT, P, NS, 1>(a, B * a.G, st);
+}
+
 template <int DT, int P>
-hipError_t dispatch_n(bool int8, int N, const StepArgs& a, unsigned units, hipStream_t st) {
+hipError_t dispatch_n(bool int8, int N, StepArgs& a, int64_t B, hipStream_t st) {
   switch (N) {
-    case 16: return launch_n<DT, P, 16>(int8, a, units, st);
-    case 32: return launch_n<DT, P, 32>(int8, a, units, st);
-    case 64: return launch_n<DT, P, 64>(int8, a, units, st);
-    case 128: return launch_n<DT, P, 128>(int8, a, units, st);
+    case 16: return int8 ? launch_n<true, DT, P, 16>(a, B, st) : launch_n<false, DT, P, 16>(a, B, st);
+    case 32: return int8 ? launch_n<true, DT, P, 32>(a, B, st) : launch_n<false, DT, P, 32>(a, B, st);
+    case 64: return int8 ? launch_n<true, DT, P, 64>(a, B, st) : launch_n<false, DT, P, 64>(a, B, st);
+    case 128: return int8 ? launch_n<true, DT, P, 128>(a, B, st) : launch_n<false, DT, P, 128>(a, B, st);
     default: return hipErrorInvalidValue;
   }
 }
 
 template <int DT>
-hipError_t dispatch_p(bool int8, int P, int N, const StepArgs& a, unsigned units, hipStream_t st) {
+hipError_t dispatch_p(bool int8, int P, int N, StepArgs& a, int64_t B, hipStream_t st) {
   switch (P) {
-    case 16: return dispatch_n<DT, 16>(int8, N, a, units, st);
-    case 32: return dispatch_n<DT, 32>(int8, N, a, units, st);
-    case 64: return dispatch_n<DT, 64>(int8, N, a, units, st);
+    case 16: return dispatch_n<DT, 16>(int8, N, a, B, st);
+    case 32: return dispatch_n<DT, 32>(int8, N, a, B, st);
+    case 64: return dispatch_n<DT, 64>(int8, N, a, B, st);
     default: return hipErrorInvalidValue;
   }
 }
@@ -252,12 +312,11 @@ hipError_t dispatch_p(bool int8, int P, int N, const StepArgs& a, unsigned units
 hipError_t launch_conv_decode_step(const Dims& d, int dtype, bool int8, const ConvPtrs& cv, const float* A,
                                    const float* D, const ScalePtrs& sc, void* state, void* Y,
                                    hipStream_t st) {
-  StepArgs a{cv, A, D, sc, state, Y, d.H, d.G, d.hpg, d.H * d.P + 2 * d.G * d.N};
-  const unsigned units = (unsigned)(d.B * d.H);
+  StepArgs a{cv, A, D, sc, state, Y, d.H, d.G, d.hpg, d.H * d.P + 2 * d.G * d.N, 0};
   switch (dtype) {
-    case DT_F32: return dispatch_p<DT_F32>(int8, d.P, d.N, a, units, st);
-    case DT_F16: return dispatch_p<DT_F16>(int8, d.P, d.N, a, units, st);
-    case DT_BF16: return dispatch_p<DT_BF16>(int8, d.P, d.N, a, units, st);
+    case DT_F32: return dispatch_p<DT_F32>(int8, d.P, d.N, a, d.B, st);
+    case DT_F16: return dispatch_p<DT_F16>(int8, d.P, d.N, a, d.B, st);
+    case DT_BF16: return dispatch_p<DT_BF16>(int8, d.P, d.N, a, d.B, st);
     default: return hipErrorInvalidValue;
   }
 }

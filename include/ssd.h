@@ -368,7 +368,7 @@ typedef struct ssd_conv {
  * position 0, count as zero and need nothing in conv_state. On return
  * conv_state holds the last width inputs up to the sequence's end; slots of
  * older positions stay as they were. The caller then adds the lengths to pos.
- * B * Cd < 2^32 (SSD_E_SHAPE otherwise). */
+ * B * Cd < 2^32, ld_xbc and ld_dt < 2^28 (SSD_E_SHAPE otherwise). */
 int ssd_conv_forward(const ssd_shape* shape, const ssd_conv* conv, const void* xbc,
                      int64_t ld_xbc, const void* dt_raw, int64_t ld_dt, const int32_t* lengths,
                      const int32_t* pos, void* conv_state, void* X, void* B, void* C, void* dt,

@@ -6,9 +6,17 @@
 //
 // Memory bound: every input is read once and every output written once, a row
 // stays in fp32 registers in between. A workgroup computes one row; thread i
-// holds the row's pieces i, i + blockDim, ... (8 consecutive channels, or one
-// channel where the rows are not a multiple of 8 long). Two reductions over
-// the row (the sum of squares, the largest magnitude) cross the waves in LDS.
+// holds the row's pieces i, i + blockDim, ... of 8 consecutive channels. Rows
+// that are not aligned, or not a multiple of 8 long, take the same pieces with
+// unaligned accesses, the last one channel by channel (G runs of channels that
+// are no multiple of 8 long: single channels instead of pieces). Two reductions
+// over the row (the sum of squares, the largest magnitude) cross the waves in
+// LDS. Rows leave past the caches (2 to 10 % faster; loads that do are slower).
+// Measured: 16384 rows of 2560 bf16 with an fp32 residual, codes and values
+// 98 us, 5.5 TB/s of 545 MB; 16384 of 5120 fp16, gated, 111 us, 5.3 TB/s (139 us
+// while the loads waited for one another and the codes took 3 more operations:
+// 63 % of the VALU's cycles were busy); 8 rows of 2560 3.3 us, a launch and two
+// memory round trips.
 //
 // The largest magnitude is found on bit patterns (unsigned order), in which
 // NaN is above infinity and infinity above every number: a row that holds
@@ -21,33 +29,87 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 
-template <int DT, int VEC, bool AL>
-__device__ __forceinline__ void ld_piece(const void* p, int64_t i, float* v) {
-  if constexpr (VEC == 1) {
-    v[0] = ld_f<DT>(p, i);
-  } else {
-    constexpr int V = RawVec<DT>::V;
+// A piece of a row as loaded: VEC channels, of which the last piece of a row that
+// is no multiple of 8 long has fewer (n; the rest are zeros, and are not written).
+template <int DT, int VEC>
+struct RawPiece {
+  static constexpr int V = RawVec<DT>::V;
+  RawVec<DT> v[VEC / V];
+  template <bool AL>
+  __device__ __forceinline__ void load(const void* p, int64_t i, int n) {
+    if (AL || n >= VEC) {
 #pragma unroll
-    for (int k = 0; k < VEC / V; ++k) {
-      RawVec<DT> r;
-      r.template load<AL>(p, i + k * V);
+      for (int k = 0; k < VEC / V; ++k) v[k].template load<AL>(p, i + k * V);
+    } else {
+      float f[VEC];
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[k * V + e] = r.get(e);
+      for (int e = 0; e < VEC; ++e) f[e] = e < n ? ld_f<DT>(p, i + e) : 0.f;
+#pragma unroll
+      for (int k = 0; k < VEC / V; ++k) v[k].set(f + k * V);
     }
   }
+  __device__ __forceinline__ float get(int e) const { return v[e / V].get(e % V); }
+};
+template <int DT>
+struct RawPiece<DT, 1> {
+  typename Store<DT>::T v;
+  template <bool AL>
+  __device__ __forceinline__ void load(const void* p, int64_t i, int) { v = ((const typename Store<DT>::T*)p)[i]; }
+  __device__ __forceinline__ float get(int) const { return Store<DT>::to_f(v); }
+};
+
+// Four whole numbers of [-127, 127] as bytes: the conversions write their low
+// bytes straight into place.
+__device__ __forceinline__ uint32_t pack4_codes(const float* v) {
+  uint32_t d = (uint32_t)(int)v[0];
+  asm("v_cvt_i32_f32_sdwa %0, %1 dst_sel:BYTE_1 dst_unused:UNUSED_PRESERVE src0_sel:DWORD" : "+v"(d) : "v"(v[1]));
+  asm("v_cvt_i32_f32_sdwa %0, %1 dst_sel:BYTE_2 dst_unused:UNUSED_PRESERVE src0_sel:DWORD" : "+v"(d) : "v"(v[2]));
+  asm("v_cvt_i32_f32_sdwa %0, %1 dst_sel:BYTE_3 dst_unused:UNUSED_PRESERVE src0_sel:DWORD" : "+v"(d) : "v"(v[3]));
+  return d;
 }
 
-template <int DT, int VEC>
-__device__ __forceinline__ void st_piece(void* p, int64_t i, const float* v) {
+template <int DT, int VEC, bool AL>
+__device__ __forceinline__ void st_piece(void* p, int64_t i, int n, const float* v) {
   if constexpr (VEC == 1) {
     ((typename Store<DT>::T*)p)[i] = to_store<DT>(v[0]);
   } else {
     constexpr int V = RawVec<DT>::V;
+    if (AL || n >= VEC) {
 #pragma unroll
-    for (int k = 0; k < VEC / V; ++k) {
-      RawVec<DT> r;
-      r.set(v + k * V);
-      r.store(p, i + k * V);
+      for (int k = 0; k < VEC / V; ++k) {
+        RawVec<DT> r;
+        r.set(v + k * V);
+        r.template store_nt<AL>(p, i + k * V);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < n) ((typename Store<DT>::T*)p)[i + e] = to_store<DT>(v[e]);
+    }
+  }
+}
+
+// The codes of VEC values v in steps: v + copysign(0.5 - 2^-25, v), truncated,
+// is v rounded half away from zero; |v| is at most 127 (1 + 2^-21), so there is
+// nothing to clamp. On return v holds the codes.
+template <int VEC, bool AL>
+__device__ __forceinline__ void st_codes(int8_t* p, int n, float* v) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = truncf(v[e] + __builtin_copysignf(0.49999997f, v[e]));
+  if constexpr (VEC == 1) {
+    p[0] = (int8_t)(int)v[0];
+  } else {
+    typedef uint32_t v2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t v2_any __attribute__((ext_vector_type(2), aligned(1)));
+    const uint32_t lo = pack4_codes(v), hi = pack4_codes(v + 4);
+    if constexpr (AL) {
+      __builtin_nontemporal_store((v2){lo, hi}, (v2*)p);
+    } else if (n >= VEC) {
+      __builtin_nontemporal_store((v2_any){lo, hi}, (v2_any*)p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e < n) p[e] = (int8_t)(int)v[e];
     }
   }
 }
@@ -63,81 +125,52 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return v;
 }
 
-// Codes of values n in steps of most / 127. inv = 127 / most overflows for rows
-// below 2^-120; such rows are scaled up by 2^100 first (exactly).
-struct Coder {
-  float scale, inv, up;
-  __device__ __forceinline__ explicit Coder(uint32_t most_bits) {
-    const float most = __uint_as_float(most_bits);
-    scale = most_bits == 0 ? 1.f : most / 127.f;
-    up = most < 0x1p-100f ? 0x1p100f : 1.f;
-    inv = most_bits == 0 ? 0.f : 127.f / (most * up);
-  }
-  __device__ __forceinline__ float code(float n) const { return truncf(q8_pre((n * up) * inv)); }
-};
-
-template <int DT, int RT, bool GATED, int VEC, int V, bool AL>
+// One row for each workgroup (of the first 2^20, then on). PARTS: the mean is over
+// groups of a row, otherwise over the row.
+template <int DT, int RT, bool GATED, bool PARTS, int VEC, int V, bool AL>
 __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
-  extern __shared__ float s_part[];  // groups > 1: the sum of squares of each piece, then 1/rms of each group
+  extern __shared__ float s_part[];  // PARTS: the sum of squares of each piece, then 1/rms of each group
   __shared__ float s_sum[kMaxWaves];
   __shared__ uint32_t s_max[kMaxWaves];
   const int nt = blockDim.x, nw = nt / kWave;
-  const int np = a.cols / VEC;  // pieces of the row
+  const int np = (a.cols + VEC - 1) / VEC;  // pieces of the row
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const int64_t base = row * (int64_t)a.cols;
+    const bool add = !GATED && a.residual;
 
-    float r[V][VEC];
+    // everything is requested before anything is used; threads behind the last
+    // piece load it too (no load is conditional on the lane)
+    RawPiece<DT, VEC> xr[V], zr[V];
+    RawPiece<RT, VEC> rr[V];
+    RawPiece<DT_F32, VEC> wr[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int p = min((int)threadIdx.x + i * nt, np - 1), c = p * VEC, n = a.cols - c;
+      xr[i].template load<AL>(a.x, row * (GATED ? (int64_t)a.cols : a.ld_x) + c, n);
+      if constexpr (GATED) zr[i].template load<AL>(a.z, row * a.ld_z + c, n);
+      else rr[i].template load<AL>(add ? a.residual : (const void*)a.weight, add ? base + c : 0, add ? n : a.cols);
+      wr[i].template load<AL>(a.weight, c, n);
+    }
+    float r[V][VEC], ss[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int p = threadIdx.x + i * nt;
-      if (p < np) ld_piece<DT, VEC, GATED || AL>(a.x, row * (GATED ? (int64_t)a.cols : a.ld_x) + p * VEC, r[i]);
-    }
-    if constexpr (GATED) {
+      ss[i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int p = threadIdx.x + i * nt;
-        if (p < np) {
-          float z[VEC];
-          ld_piece<DT, VEC, AL>(a.z, row * a.ld_z + p * VEC, z);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) r[i][e] *= silu(z[e]);
-        }
+      for (int e = 0; e < VEC; ++e) {
+        r[i][e] = xr[i].get(e);
+        if constexpr (GATED) r[i][e] *= silu(zr[i].get(e));
+        else if (add) r[i][e] += rr[i].get(e);
+        ss[i] = fmaf(r[i][e], r[i][e], ss[i]);
       }
-    } else {
-      if (a.residual) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int p = threadIdx.x + i * nt;
-          if (p < np) {
-            float o[VEC];
-            ld_piece<RT, VEC, true>(a.residual, base + p * VEC, o);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) r[i][e] += o[e];
-          }
-        }
-      }
-      if (a.residual_out) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int p = threadIdx.x + i * nt;
-          if (p < np) st_piece<RT, VEC>(a.residual_out, base + p * VEC, r[i]);
-        }
-      }
+      if (p >= np) ss[i] = 0.f;
+      if constexpr (!GATED)
+        if (a.residual_out && p < np) st_piece<RT, VEC, AL>(a.residual_out, base + p * VEC, a.cols - p * VEC, r[i]);
     }
 
-    // sums of squares
-    float ss[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      ss[i] = 0.f;
-      if ((int)threadIdx.x + i * nt < np) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) ss[i] = fmaf(r[i][e], r[i][e], ss[i]);
-      }
-    }
-    const int gp = np / a.groups;  // pieces of a group
     float rs0 = 0.f;
-    if (!GATED || a.groups == 1) {
+    const int gp = PARTS ? np / a.groups : np;  // pieces of a group
+    if constexpr (!PARTS) {
       float t = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) t += ss[i];
@@ -164,19 +197,15 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
       __syncthreads();
     }
 
+    // the normalised rows; the threads behind the last piece repeat its values
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int p = threadIdx.x + i * nt;
-      if (p < np) {
-        float w[VEC];
-        ld_piece<DT_F32, VEC, true>(a.weight, p * VEC, w);
-        const float rs = (!GATED || a.groups == 1) ? rs0 : s_part[np + p / gp];
+      const float rs = PARTS ? s_part[np + min((int)threadIdx.x + i * nt, np - 1) / gp] : rs0;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          r[i][e] = r[i][e] * rs * w[e];
-          most = max(most, __float_as_uint(r[i][e]) & 0x7fffffffu);
-        }
+      for (int e = 0; e < VEC; ++e) {
+        r[i][e] = r[i][e] * rs * wr[i].get(e);
+        most = max(most, __float_as_uint(r[i][e]) & 0x7fffffffu);
       }
     }
     if (a.q) {
@@ -185,33 +214,34 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
       __syncthreads();
       most = 0;
       for (int i = 0; i < nw; ++i) most = max(most, s_max[i]);
-      const Coder cd(most);
+      // steps of most / 127; 127 / most overflows for rows below 2^-120: those
+      // are scaled up by 2^100 first (exactly)
+      const float top = __uint_as_float(most);
+      const bool tiny = top < 0x1p-100f;
+      const float scale = most == 0 ? 1.f : top / 127.f;
+      const float inv = most == 0 ? 0.f : 127.f / (tiny ? top * 0x1p100f : top);
+      if (tiny) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) r[i][e] *= 0x1p100f;
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int p = threadIdx.x + i * nt;
-        if (p < np) {
-          float c[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            c[e] = cd.code(r[i][e]);
-            r[i][e] = c[e] * cd.scale;
-          }
-          if constexpr (VEC == 1) {
-            a.q[base + p] = (int8_t)(int)c[0];
-          } else {
-            const uint2 v = make_uint2(pack4((int)c[0], (int)c[1], (int)c[2], (int)c[3]),
-                                       pack4((int)c[4], (int)c[5], (int)c[6], (int)c[7]));
-            *(uint2*)(a.q + base + p * VEC) = v;
-          }
-        }
+        for (int e = 0; e < VEC; ++e) r[i][e] *= inv;
+        if (p < np) st_codes<VEC, AL>(a.q + base + p * VEC, a.cols - p * VEC, r[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r[i][e] *= scale;
       }
-      if (threadIdx.x == 0) a.scale[row] = cd.scale;
+      if (threadIdx.x == 0) a.scale[row] = scale;
     }
     if (a.out) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int p = threadIdx.x + i * nt;
-        if (p < np) st_piece<DT, VEC>(a.out, base + p * VEC, r[i]);
+        if (p < np) st_piece<DT, VEC, AL>(a.out, base + p * VEC, a.cols - p * VEC, r[i]);
       }
     }
     // the next row's sums overwrite this one's: with codes, the barrier of the
@@ -220,44 +250,50 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
   }
 }
 
-template <int DT, int RT, bool GATED, int VEC, int V, bool AL>
-hipError_t go(const NormArgs& a, int nt, hipStream_t st) {
-  const size_t lds = GATED && a.groups > 1 ? (size_t)(a.cols / VEC + a.groups) * sizeof(float) : 0;
-  hipLaunchKernelGGL((k_norm<DT, RT, GATED, VEC, V, AL>), dim3((unsigned)min(a.rows, (int64_t)1 << 20)),
-                     dim3(nt), lds, st, a);
+template <int DT, int RT, bool GATED, bool PARTS, int VEC, int V, bool AL>
+hipError_t go(const NormArgs& a, int waves, hipStream_t st) {
+  const size_t lds = PARTS ? (size_t)(a.cols / VEC + a.groups) * sizeof(float) : 0;
+  hipLaunchKernelGGL((k_norm<DT, RT, GATED, PARTS, VEC, V, AL>), dim3((unsigned)min(a.rows, (int64_t)1 << 20)),
+                     dim3(waves * kWave), lds, st, a);
   return hipGetLastError();
+}
+
+template <int DT, int RT, bool GATED, bool PARTS, bool AL>
+hipError_t pick_pieces(const NormArgs& a, hipStream_t st) {
+  // at most 8 waves a row: more meet at its two barriers more slowly (16384 rows
+  // of 5120, gated: 10 waves 174 us, 5 waves 139; 8192 of 8192: 16 waves 120, 8
+  // waves 100), fewer hold more registers (2560 columns: 5 waves 101 us, 3 waves
+  // 106, 1 wave 116)
+  const int wp = ((a.cols + 7) / 8 + kWave - 1) / kWave;  // pieces of a row, in waves
+  const int v = (wp + 7) / 8, waves = (wp + v - 1) / v;
+  switch (v) {
+    case 1: return go<DT, RT, GATED, PARTS, 8, 1, AL>(a, waves, st);
+    case 2: return go<DT, RT, GATED, PARTS, 8, 2, AL>(a, waves, st);
+    case 3: return go<DT, RT, GATED, PARTS, 8, 3, AL>(a, waves, st);
+    default: return go<DT, RT, GATED, PARTS, 8, 4, AL>(a, waves, st);
+  }
 }
 
 template <int DT, int RT, bool GATED>
 hipError_t pick(const NormArgs& a, hipStream_t st) {
-  constexpr int esize = DT == DT_F32 ? 4 : 2;
-  const int group = a.cols / a.groups;
-  if (group % 8 == 0) {
-    const int np = a.cols / 8;
-    const int v = (np + 511) / 512;  // pieces of a thread, 1 .. 4
-    const int nt = ((np + v - 1) / v + kWave - 1) / kWave * kWave;
-    const bool al = GATED ? (uintptr_t)a.z % 16 == 0 && a.ld_z * esize % 16 == 0
-                          : (uintptr_t)a.x % 16 == 0 && a.ld_x * esize % 16 == 0;
-#define GO_(V_) return al ? go<DT, RT, GATED, 8, V_, true>(a, nt, st) : go<DT, RT, GATED, 8, V_, false>(a, nt, st)
-    switch (v) {
-      case 1: GO_(1);
-      case 2: GO_(2);
-      case 3: GO_(3);
-      default: GO_(4);
-    }
-#undef GO_
+  constexpr int64_t esize = DT == DT_F32 ? 4 : 2;
+  if (a.groups == 1 || a.cols / a.groups % 8 == 0) {
+    const void* const p = GATED ? a.z : a.x;
+    const int64_t ld = GATED ? a.ld_z : a.ld_x;
+    const bool al = a.cols % 8 == 0 && (uintptr_t)p % 16 == 0 && ld * esize % 16 == 0;
+    if constexpr (GATED)
+      if (a.groups > 1)
+        return al ? pick_pieces<DT, RT, true, true, true>(a, st) : pick_pieces<DT, RT, true, true, false>(a, st);
+    return al ? pick_pieces<DT, RT, GATED, false, true>(a, st) : pick_pieces<DT, RT, GATED, false, false>(a, st);
   }
-  // single channels, 1 .. 16 of a thread in powers of two
-  int v = 1;
-  while (a.cols > v * 1024) v *= 2;
-  const int nt = ((a.cols + v - 1) / v + kWave - 1) / kWave * kWave;
-  switch (v) {
-    case 1: return go<DT, RT, GATED, 1, 1, false>(a, nt, st);
-    case 2: return go<DT, RT, GATED, 1, 2, false>(a, nt, st);
-    case 4: return go<DT, RT, GATED, 1, 4, false>(a, nt, st);
-    case 8: return go<DT, RT, GATED, 1, 8, false>(a, nt, st);
-    default: return go<DT, RT, GATED, 1, 16, false>(a, nt, st);
+  if constexpr (GATED) {  // single channels, 1, 4 or 16 of a thread
+    const int v = a.cols <= 1024 ? 1 : a.cols <= 4096 ? 4 : 16;
+    const int waves = ((a.cols + v - 1) / v + kWave - 1) / kWave;
+    if (v == 1) return go<DT, RT, true, true, 1, 1, false>(a, waves, st);
+    if (v == 4) return go<DT, RT, true, true, 1, 4, false>(a, waves, st);
+    return go<DT, RT, true, true, 1, 16, false>(a, waves, st);
   }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace

@@ -19,29 +19,30 @@ __device__ __forceinline__ float softplus(float v) {
   return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
 }
 
-// 16 bytes of consecutive elements as loaded: one access where the rows are
-// 16-byte aligned (AL), element by element otherwise.
+// 16 bytes of consecutive elements as loaded, at a 16-byte aligned address (AL)
+// or at any element's: the memory pipe takes both in one access.
 template <int DT>
 struct RawVec {
   static constexpr int V = DT == DT_F32 ? 4 : 8;
   typedef uint32_t v4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t v4_any __attribute__((ext_vector_type(4), aligned(2)));
   v4 w;
   __device__ __forceinline__ void zero() { w = (v4){0, 0, 0, 0}; }
   template <bool AL>
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    if constexpr (AL) {
-      w = *(const v4*)((const typename Store<DT>::T*)p + i);
-    } else if constexpr (DT == DT_F32) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = ((const uint32_t*)p)[i + e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = (uint32_t)((const u16*)p)[i + 2 * e] | ((uint32_t)((const u16*)p)[i + 2 * e + 1] << 16);
-    }
+    const typename Store<DT>::T* const q = (const typename Store<DT>::T*)p + i;
+    if constexpr (AL) w = *(const v4*)q;
+    else w = *(const v4_any*)q;
   }
   __device__ __forceinline__ void store(void* p, int64_t i) const {
     *(v4*)((typename Store<DT>::T*)p + i) = w;
+  }
+  // past the caches' reach: written once and read, if at all, by a later kernel
+  template <bool AL>
+  __device__ __forceinline__ void store_nt(void* p, int64_t i) const {
+    typename Store<DT>::T* const q = (typename Store<DT>::T*)p + i;
+    if constexpr (AL) __builtin_nontemporal_store(w, (v4*)q);
+    else __builtin_nontemporal_store(w, (v4_any*)q);
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (DT == DT_F32) return __uint_as_float(w[e]);

@@ -31,7 +31,8 @@ int check_conv(const Dims& d, int dtype, const ssd_conv* cv, const void* xbc, in
   if (!aligned_to(xbc, elem_bytes(dtype)) || !aligned_to(dt_raw, elem_bytes(dtype)) || !aligned_to(pos, 4))
     return SSD_E_ALIGN;
   const int64_t cd = (int64_t)d.H * d.P + 2 * (int64_t)d.G * d.N;
-  if (ld_xbc < cd || ld_dt < d.H) return SSD_E_SHAPE;
+  constexpr int64_t kMostLd = (int64_t)1 << 28;  // a row's bytes fit 32 bits
+  if (ld_xbc < cd || ld_dt < d.H || ld_xbc >= kMostLd || ld_dt >= kMostLd) return SSD_E_SHAPE;
   int64_t t;
   if (!mul_ok(d.B, cd, &t) || t >= (int64_t)1 << 32) return SSD_E_SHAPE;
   if (!mul_ok(d.B, d.L, &t)) return SSD_E_SHAPE;

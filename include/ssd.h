@@ -334,6 +334,7 @@ int ssd_scales_from_amax(int64_t ngroups, int64_t nheads, int64_t headdim,
  *   Out Proj             ssd_matmul_i8
  *
  * and, for single tokens, ssd_conv_decode_step in the place of Conv and SSD.
+ * No output may overlap an input or another output, but where a call says so.
  * Unlike the dense buffers above, inputs that are parts of In Proj's rows are
  * read in place: "ld" is the distance between rows in elements, and such a
  * pointer need only be aligned to its element (16-byte aligned rows are read
@@ -377,7 +378,7 @@ int ssd_conv_forward(const ssd_shape* shape, const ssd_conv* conv, const void* x
 /* One position of Conv and SSD in one launch: ssd_conv_forward's arithmetic on
  * one row per sequence, then ssd_decode_step's on its results, which stay in
  * fp32 (they are not rounded to shape->dtype in between). shape->seqlen must
- * be 1 (or batch 0), batch * nheads <= 2^24.
+ * be 1 (or batch 0), batch * nheads < 2^24.
  * xbc [B rows, Cd] and dt_raw [B rows, H] with row distances; conv_state
  * [B, width, Cd] and pos [B] as above, both required; the call writes slot
  * pos % width and reads the width - 1 others. It does not change pos: the
@@ -418,9 +419,9 @@ int ssd_gated_norm(int64_t rows, int64_t cols, int64_t groups, int dtype, const 
  * each row (output channel), bias [N] fp32 (may be NULL; at Out Proj it carries
  * the mean correction of "Key design 4"), out [M, N] in out_dtype. K is a
  * multiple of 16 (SSD_E_UNSUPPORTED) and at most 131056 (so that the sums of any
- * codes fit), M, N < 2^26 and M * N < 2^40; M == 0 is a valid empty problem. workspace: device memory
- * of at least ssd_matmul_i8_workspace_bytes(M, N, K) bytes (may be NULL when
- * that is 0); calls that may overlap need one each. */
+ * codes fit), M, N < 2^26 and M * N < 2^40; M == 0 is a valid empty problem.
+ * workspace: device memory of at least ssd_matmul_i8_workspace_bytes(M, N, K)
+ * bytes (may be NULL when that is 0); calls that may overlap need one each. */
 int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float* a_scale,
                   const int8_t* w, const float* w_scale, const float* bias, int out_dtype,
                   void* out, void* workspace, size_t workspace_bytes, void* stream);

@@ -403,6 +403,13 @@ def _stream_on(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _code(dtype):
+    try:
+        return DTYPE_CODE[dtype]
+    except KeyError:
+        raise ValueError(f"no such type here: {dtype}") from None
+
+
 def _dense(t, name, numel, dtype, dev):
     """Address of a dense buffer of a given size and type on device ``dev`` (None passes:
     the C call decides)."""
@@ -513,7 +520,7 @@ def ssd_add_norm(x, residual, residual_out, weight, eps, out=None, q=None, scale
     px, ldx = _rows(x, "x", cols, td, dev)
     rt = td if residual is None and residual_out is None else (residual_out if residual is None else residual).dtype
     _check("ssd_add_norm", LIB.ssd_add_norm(
-        rows, cols, DTYPE_CODE[td], px, ldx, _dense(residual, "residual", n, rt, dev), DTYPE_CODE[rt],
+        rows, cols, _code(td), px, ldx, _dense(residual, "residual", n, rt, dev), _code(rt),
         _dense(residual_out, "residual_out", n, rt, dev), _dense(weight, "weight", cols, torch.float32, dev), eps,
         _dense(out, "out", n, td, dev), _dense(q, "q", n, torch.int8, dev),
         _dense(scale, "scale", rows, torch.float32, dev), _stream_on(stream, dev)))
@@ -530,7 +537,7 @@ def ssd_gated_norm(y, z, groups, weight, eps, out=None, q=None, scale=None, stre
     rows = n // cols
     pz, ldz = _rows(z, "z", cols, td, dev)
     _check("ssd_gated_norm", LIB.ssd_gated_norm(
-        rows, cols, groups, DTYPE_CODE[td], _dense(y, "y", n, td, dev), pz, ldz,
+        rows, cols, groups, _code(td), _dense(y, "y", n, td, dev), pz, ldz,
         _dense(weight, "weight", cols, torch.float32, dev), eps, _dense(out, "out", n, td, dev),
         _dense(q, "q", n, torch.int8, dev), _dense(scale, "scale", rows, torch.float32, dev),
         _stream_on(stream, dev)))
@@ -563,7 +570,7 @@ def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None
     _check("ssd_matmul_i8", LIB.ssd_matmul_i8(
         m, n, k, _dense(a, "a", m * k, torch.int8, dev), _dense(a_scale, "a_scale", m, torch.float32, dev),
         _dense(w, "w", n * k, torch.int8, dev), _dense(w_scale, "w_scale", n, torch.float32, dev),
-        _dense(bias, "bias", n, torch.float32, dev), DTYPE_CODE[out.dtype],
+        _dense(bias, "bias", n, torch.float32, dev), _code(out.dtype),
         _dense(out, "out", m * n, out.dtype, dev), pw, wsb, _stream_on(stream, dev)))
 
 

@@ -197,16 +197,21 @@ __global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
       __syncthreads();
     }
 
-    // the normalised rows; the threads behind the last piece repeat its values
+    // The normalised rows. What threads behind the last piece hold counts for
+    // nothing: where residual_out is residual itself, another wave may have
+    // written the last piece before they loaded it.
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float rs = PARTS ? s_part[np + min((int)threadIdx.x + i * nt, np - 1) / gp] : rs0;
+      const int p = threadIdx.x + i * nt;
+      const float rs = PARTS ? s_part[np + min(p, np - 1) / gp] : rs0;
+      uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         r[i][e] = r[i][e] * rs * wr[i].get(e);
-        most = max(most, __float_as_uint(r[i][e]) & 0x7fffffffu);
+        m = max(m, __float_as_uint(r[i][e]) & 0x7fffffffu);
       }
+      if (p < np) most = max(most, m);
     }
     if (a.q) {
       most = wave_max(most);

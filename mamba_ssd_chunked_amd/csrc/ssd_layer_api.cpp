@@ -99,7 +99,7 @@ int ssd_conv_decode_step(const ssd_shape* shape, int path, const ssd_conv* conv,
   if ((rc = check_path(path))) return rc;
   if (d.B > 0 && d.L != 1) return SSD_E_SHAPE;
   // a workgroup per (batch, head): keep the grid's thread count below 2^32
-  if (d.B * (int64_t)d.H > (int64_t)1 << 24) return SSD_E_SHAPE;
+  if (d.B * (int64_t)d.H >= (int64_t)1 << 24) return SSD_E_SHAPE;
   const bool i8 = path == SSD_PATH_INT8;
   if ((rc = check_conv(d, shape->dtype, conv, xbc, ld_xbc, dt_raw, ld_dt, pos))) return rc;
   if (!pos) return SSD_E_NULL;

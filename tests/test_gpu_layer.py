@@ -463,6 +463,31 @@ def test_norms_in_place_and_empty(gpu_lib):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("cols", [4104, 4360, 8200, 12296])
+def test_add_norm_over_the_residual_where_a_wave_has_no_piece(gpu_lib, cols):
+    """Rows whose last wave lies behind the last piece: the codes do not depend on
+    whether residual_out is the residual itself."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    rows = 2000
+    x = torch.randn(rows, cols, generator=g, device="cuda").half()
+    r = torch.randn(rows, cols, generator=g, device="cuda")
+    r[:, -8:] += 40 * torch.sign(x[:, -8:].float())  # the last piece decides the scale
+    x[:, -8:] *= 20
+    w = torch.ones(cols, device="cuda")
+
+    def run(res, res_out):
+        q = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+        s = torch.empty(rows, device="cuda")
+        L.ssd_add_norm(x, res, res_out, w, EPS, None, q, s)
+        return q, s, res_out
+
+    a, b = run(r, torch.empty_like(r)), run(r2 := r.clone(), r2)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
 # ---------------------------------------------------------------------------
 # product
 # ---------------------------------------------------------------------------
@@ -688,3 +713,93 @@ def test_layer_step_replayed_from_a_graph(gpu_lib):
         assert torch.equal(H.bits(out), H.bits(eager[t])), t
         _ = (out.float() * 2).sum().item()
     assert torch.equal(H.bits(h), H.bits(h2)) and torch.equal(H.bits(ring), H.bits(ring2)) and torch.equal(pos, pos2)
+
+
+def test_layer_with_padding_that_is_not_finite(gpu_lib):
+    """What lies behind a sequence's end, NaN or infinity, reaches neither its
+    outputs nor its states."""
+    import torch
+    L = gpu_lib
+    ly = _Layer(L, torch, dtype="fp16", seed=5)
+    g = torch.Generator(device="cuda").manual_seed(16)
+    B, n = 3, 130
+    ends = [130, 64, 0]
+    x = torch.randn(B, n, ly.model, generator=g, device="cuda").half()
+    lengths = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    got = []
+    for pad in (0.0, float("nan"), float("inf")):
+        xs = x.clone()
+        for b, e in enumerate(ends):
+            xs[b, e:] = pad
+        ring = torch.zeros((B, ly.W, ly.cd), dtype=ly.td, device="cuda")
+        h = torch.ones((B, ly.H, ly.P, ly.N), device="cuda")
+        pos = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+        out = ly.prompt(xs, torch.zeros(B * n, ly.model, device="cuda"), ring, pos, lengths, h)
+        got.append([ring, h] + [out[b, :e].clone() for b, e in enumerate(ends)])
+    for other in got[1:]:
+        for u, v in zip(got[0], other):
+            assert torch.isfinite(v).all() and torch.equal(u, v)
+    assert torch.equal(got[0][1][2], torch.ones_like(got[0][1][2]))  # a sequence of no positions
+
+
+def test_layer_steps_on_streams_and_in_two_graphs(gpu_lib):
+    """Two layers at once: eagerly on two streams, and as two graphs that replay by
+    turns and side by side, each as alone. A batch of 300 takes other kernels of the
+    product than one of 4."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(18)
+    steps, sizes = 4, (4, 300)
+    layers = [_Layer(L, torch, dtype=d, seed=k) for k, d in ((7, "fp16"), (8, "bf16"))]
+    xs = [torch.randn(steps, b, ly.model, generator=g, device="cuda").to(ly.td) for b, ly in zip(sizes, layers)]
+
+    def fresh(i):
+        ly, b = layers[i], sizes[i]
+        return (torch.zeros(b, ly.model, device="cuda"), torch.zeros((b, ly.W, ly.cd), dtype=ly.td, device="cuda"),
+                torch.zeros(b, dtype=torch.int32, device="cuda"), torch.zeros((b, ly.H, ly.P, ly.N), device="cuda"))
+
+    alone = []
+    for i, ly in enumerate(layers):
+        res, ring, pos, h = fresh(i)
+        outs = []
+        for t in range(steps):
+            outs.append(ly.step(xs[i][t], res, ring, pos, h))
+            pos += 1
+        alone.append(outs)
+    torch.cuda.synchronize()
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    state = [fresh(0), fresh(1)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for t in range(steps):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(layers[i].step(xs[i][t], *state[i]))
+                state[i][2].add_(1)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for t in range(steps):
+            assert torch.equal(H.bits(outs[i][t]), H.bits(alone[i][t])), (i, t)
+
+    state, x_in = [fresh(0), fresh(1)], [xs[0][0].clone(), xs[1][0].clone()]
+    torch.cuda.synchronize()
+    graphs, out = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            out.append(layers[i].step(x_in[i], *state[i]))
+            state[i][2].add_(1)
+    for t in range(steps):
+        for i in range(2):
+            x_in[i].copy_(xs[i][t])
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            if t % 2:  # side by side
+                with torch.cuda.stream(s):
+                    graphs[i].replay()
+            else:
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(H.bits(out[i]), H.bits(alone[i][t])), (i, t)

@@ -62,6 +62,9 @@ def test_conv_forward_refusals():
     assert conv_fwd(ldt=3) == L.SSD_E_SHAPE
     assert conv_fwd(sh=shape(), ldx=BIG) == L.SSD_E_SHAPE
     assert conv_fwd(sh=shape(), ldt=BIG) == L.SSD_E_SHAPE
+    # a row's bytes are counted in 32 bits
+    assert conv_fwd(ldx=1 << 28) == L.SSD_E_SHAPE and conv_fwd(ldt=1 << 28) == L.SSD_E_SHAPE
+    assert conv_fwd(ldx=(1 << 28) - 1, ldt=(1 << 28) - 1) == L.SSD_OK
     assert conv_fwd(sh=shape(seqlen=0, batch=65535, nheads=4096), ldx=1 << 20, ldt=4096) == L.SSD_E_SHAPE
     assert conv_fwd(pos=A16) == L.SSD_E_NULL  # a position without the ring it speaks of
     assert conv_fwd(pos=A16, ring=A16) == L.SSD_OK
@@ -87,6 +90,8 @@ def test_conv_decode_step_refusals():
     assert step(sh=shape(seqlen=2)) == L.SSD_E_SHAPE
     assert step(sh=shape(seqlen=0)) == L.SSD_E_SHAPE
     assert step(sh=shape(seqlen=1, batch=65535, nheads=512), ldx=1 << 20, ldt=512) == L.SSD_E_SHAPE
+    # 2^24 workgroups of 256 threads are one more than a grid holds
+    assert step(sh=shape(seqlen=1, batch=32768, nheads=512), ldx=1 << 20, ldt=512) == L.SSD_E_SHAPE
     for k in ("xbc", "raw", "A", "D", "ring", "pos", "state", "Y"):
         assert step(**{k: None}) == L.SSD_E_NULL, k
         assert step(**{k: ODD}) == L.SSD_E_ALIGN, k
@@ -210,6 +215,10 @@ def test_binding_refuses_what_the_library_cannot_see():
     for t, n, dt, dev in ((w, 63, f, -1), (w, 64, torch.int8, -1), (w, 64, f, 0), (wide.transpose(0, 1), 2400, f, -1)):
         with pytest.raises(ValueError, match="contiguous"):
             L._dense(t, "w", n, dt, dev)
+    assert L._code(torch.bfloat16) == L.DTYPE_CODE[torch.bfloat16]
+    for dt in (torch.float64, torch.int32):
+        with pytest.raises(ValueError, match=str(dt)):
+            L._code(dt)
     for bad in (torch.zeros(96, 4, dtype=torch.float16), torch.zeros(96, 4)):
         with pytest.raises(ValueError, match="float32 tensors on one GPU"):
             L.ConvParams(bad)

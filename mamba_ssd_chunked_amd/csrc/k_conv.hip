@@ -216,9 +216,12 @@ hipError_t launch_conv_forward(const Dims& d, int dtype, const ConvPtrs& cv, con
   const int esize = dtype == DT_F32 ? 4 : 2;
   a.nvec = a.Cd / (16 / esize);
   // Positions per thread: long tiles spread the weights' loads and the window's
-  // head over more rows, short ones give enough threads to fill the chip (16
-  // waves on each of its CUs); never below kU, the rows in flight.
-  const int64_t want = (int64_t)(cu_count() > 0 ? cu_count() : 256) * 16 * kWave;
+  // head over more rows, short ones give every CU something to do. Three waves on
+  // each CU are enough, as a wave has 8 rows under way (16-bit types, us at 1, 2,
+  // 3, 4 and 16 waves: 4 x 791 x 1552 channels 15.8, 12.1, 12.5, 12.4, 14.1;
+  // 3 x 701 x 10240 22 and, at 16, 27; 5 x 2954 x 1024, at 4 and 16, 16 and 24).
+  // Never below kU, the rows of a set.
+  const int64_t want = (int64_t)(cu_count() > 0 ? cu_count() : 256) * 3 * kWave;
   int64_t T = kU;
   while (T < 32 && d.B * ((d.L + 2 * T - 1) / (2 * T)) * a.nvec >= want) T *= 2;
   // thread indexes fit 31 bits

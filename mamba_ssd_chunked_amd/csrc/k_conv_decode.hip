@@ -270,11 +270,12 @@ hipError_t launch_hb(StepArgs& a, int64_t bg, hipStream_t st) {
   return hipGetLastError();
 }
 
-// A workgroup takes a head; where the heads are more than 6 on each CU, as many
+// A workgroup takes a head; where the heads are more than 3 on each CU, as many
 // as make 32 KB of state. Measured, one head against several: 114 heads of
 // 16 x 32 fp32 at batch 256 97 and 31 us, at batch 4 (1.8 heads on each CU) 4.3
 // and 4.3; 108 heads of 32 x 32 fp32 at batch 256 103 and 55 us, at batch 4 4.3
-// and 6.8. (A part of a head for each workgroup, where heads are fewer than CUs,
+// and 6.8; 25 heads of 16 x 128 fp32 at batch 32 (3.1) 9.6 and 7.7; 3 of 64 x 32
+// at batch 173 (2.0) 5.5 and 6.5. (A part of a head for each workgroup, where heads are fewer than CUs,
 // gained nothing at 64 x 128.)
 template <bool I8, int DT, int P, int NS>
 hipError_t launch_n(StepArgs& a, int64_t B, hipStream_t st) {
@@ -282,7 +283,7 @@ hipError_t launch_n(StepArgs& a, int64_t B, hipStream_t st) {
   constexpr int HB = kMost < 1 ? 1 : kMost > 8 ? 8 : kMost;
   const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
   if constexpr (HB > 1)
-    if (B * a.H > 6 * ncu && a.hpg > 1) return launch_hb<I8, DT, P, NS, HB>(a, B * a.G, st);
+    if (B * a.H > 3 * ncu && a.hpg > 1) return launch_hb<I8, DT, P, NS, HB>(a, B * a.G, st);
   return launch_hb<I8, DT, P, NS, 1>(a, B * a.G, st);
 }
 

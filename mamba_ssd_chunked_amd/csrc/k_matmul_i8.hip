@@ -10,6 +10,9 @@ namespace ssd {
 namespace {
 
 typedef int v16i __attribute__((ext_vector_type(16)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));  // at any 16-bit element's address
+typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // 16 bytes per lane from global memory straight into LDS: lane i's bytes land
 // at l + 16 i (l is uniform over the wave).
@@ -175,7 +178,6 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
   constexpr int U = DT == DT_F32 ? 1 : 2;  // 32-column blocks of a piece
   constexpr int E = 16 / sizeof(T);        // outputs of a 16-byte chunk
   const int lane = lane_id(), hi = lane >> 5;
-  const bool wide = g.N % E == 0;
   const int row = lane & 31, swz = (row >> 1) & 7;
   const unsigned lane_at = ((lane >> 3) * (unsigned)g.N + (lane & 7) * E) * sizeof(T);
   // The columns' steps come through the scalar cache (they are the same for all
@@ -232,15 +234,8 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
         const v4u v = *(const v4u*)(st + orow * 128 + ((lane & 7) ^ ((orow >> 1) & 7)) * 16);
         // the rows' address is uniform, the lane's place in them fits 32 bits
         T* const o = (T*)(const_cast<int8_t*>(uniform_ptr((const int8_t*)g.out + ((int64_t)(m0 + wm + 32 * j + 8 * r) * g.N + nu) * sizeof(T))) + lane_at);
-        if (wide) {
-          *(v4u*)o = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if constexpr (DT == DT_F32) ((uint32_t*)o)[e] = v[e];
-            else ((u16*)o)[e] = (u16)(v[e >> 1] >> (16 * (e & 1)));
-          }
-        }
+        // rows that are not 16-byte aligned take the same stores
+        *(v4u_any*)o = v;
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -349,11 +344,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_matmul_i8_tile(MatmulI8Args
 // registers are 64 bytes of sixteen rows in each load, at which a CU took in
 // 41 GB/s instead of the copies' 107.)
 template <int DT>
-__device__ __forceinline__ void store4(void* out, int64_t at, const float (&y)[4], int n, bool wide) {
+__device__ __forceinline__ void store4(void* out, int64_t at, const float (&y)[4], int n) {
   typename Store<DT>::T* const o = (typename Store<DT>::T*)out + at;
-  if (wide) {
-    if constexpr (DT == DT_F32) *(v4f*)o = (v4f){y[0], y[1], y[2], y[3]};
-    else *(uint2*)o = make_uint2(pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3]));
+  if (n >= 4) {
+    if constexpr (DT == DT_F32) *(v4f_any*)o = (v4f_any){y[0], y[1], y[2], y[3]};
+    else *(v2u_any*)o = (v2u_any){pack2<DT>(y[0], y[1]), pack2<DT>(y[2], y[3])};
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -491,11 +486,10 @@ __global__ __launch_bounds__(64 * NW) void k_matmul_i8_rows(MatmulI8Args g, int 
     for (int e = 0; e < 4; ++e) y[e] = fmaf((float)sum[e], as * ws[e], bias[e]);
     const int64_t o = (int64_t)m * g.N + n;
     const int left = (int)g.N - n;
-    const bool wide = g.N % 4 == 0;
     switch (dtype) {
-      case DT_F32: store4<DT_F32>(g.out, o, y, left, wide); break;
-      case DT_F16: store4<DT_F16>(g.out, o, y, left, wide); break;
-      default: store4<DT_BF16>(g.out, o, y, left, wide); break;
+      case DT_F32: store4<DT_F32>(g.out, o, y, left); break;
+      case DT_F16: store4<DT_F16>(g.out, o, y, left); break;
+      default: store4<DT_BF16>(g.out, o, y, left); break;
     }
   }
 }

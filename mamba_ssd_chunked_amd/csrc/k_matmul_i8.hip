@@ -46,13 +46,13 @@ constexpr int kBK = 128;
 template <int NW>
 struct Tile {
   static constexpr int kSide = 32 * NW, kBytesA = kSide * kBK, kBytes = 2 * kBytesA;
-  static constexpr int kSteps = NW == 8 ? 2 : 4;  // steps in LDS at a time: 128 KB
-  // Whether a step's copies are issued in quarters among products. Three steps
-  // ahead (NW = 4) that is 5 % faster; one step ahead the copies' latency is
-  // what counts, and at once is 5 % faster.
-  static constexpr bool kSpread = NW == 4;
   static constexpr int TI = NW / 2;  // 32 x 32 blocks of a wave in n; 2 in m
 };
+// S steps are in LDS at a time. Three steps ahead (S = 4) a step's copies are
+// issued in quarters among products, which is 5 % faster; one step ahead the
+// copies' latency is what counts, and at once is 5 % faster.
+template <int S>
+constexpr bool kSpread = S > 2;
 constexpr int kStage = 32 * 128;  // a wave's part of the epilogue's staging: 32 rows of 128 bytes
 
 // The rows of both operands this lane copies, and their LDS homes. A tile row
@@ -133,7 +133,7 @@ struct TileFrags {
 // once and the others among the next step's products (here: the rest of `sp`'s
 // into `prv`), so that no wave stands in front of a full memory pipe with
 // products to issue.
-template <int NW, bool TAIL>
+template <int NW, int S, bool TAIL>
 __device__ __forceinline__ void tile_step(int8_t* prv, const TileFrom& sp, int8_t* cur, const TileFrom& sn,
                                           const int8_t* nxt, const TileCopy<NW, TAIL>& cp, int K, int wm, int wn,
                                           TileFrags<NW> (&f)[2], v16i (&acc)[Tile<NW>::TI][2]) {
@@ -141,13 +141,13 @@ __device__ __forceinline__ void tile_step(int8_t* prv, const TileFrom& sp, int8_
 #pragma unroll
   for (int ks = 0; ks < 3; ++ks) {
     f[(ks + 1) & 1].load(cur, ks + 1, wm, wn);
-    if constexpr (Tile<NW>::kSpread) copy_quarter<NW, TAIL>(cp, ks + 1, sp, K, prv);
+    if constexpr (kSpread<S>) copy_quarter<NW, TAIL>(cp, ks + 1, sp, K, prv);
     f[ks & 1].multiply(acc);
 #pragma unroll
     for (int q = 0; q < TI + 2; ++q) {  // a read, a product, ...
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (Tile<NW>::kSpread && (q == 1 || q == 3)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (kSpread<S> && (q == 1 || q == 3)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     if constexpr (TI > 2) __builtin_amdgcn_sched_group_barrier(0x008, TI - 2, 0);
   }
@@ -155,13 +155,13 @@ __device__ __forceinline__ void tile_step(int8_t* prv, const TileFrom& sp, int8_
   asm volatile("" ::: "memory");
   // This wave's copies into nxt have arrived (only those of the steps behind it,
   // 8 each, may still be on their way), its reads of cur have too (lgkmcnt 0).
-  constexpr int kBehind = 8 * (Tile<NW>::kSteps - 2);
+  constexpr int kBehind = 8 * (S - 2);
   __builtin_amdgcn_s_waitcnt(0x0070 | (kBehind & 15) | ((kBehind >> 4) << 14));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
   f[0].load(nxt, 0, wm, wn);
-  if constexpr (Tile<NW>::kSpread) copy_quarter<NW, TAIL>(cp, 0, sn, K, cur);
+  if constexpr (kSpread<S>) copy_quarter<NW, TAIL>(cp, 0, sn, K, cur);
   else copy_step<NW, TAIL>(cp, sn, K, cur);
   f[1].multiply(acc);
   __builtin_amdgcn_sched_barrier(0);
@@ -244,17 +244,20 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
   }
 }
 
+// Workgroups on a CU: their LDS (S steps and the stages) fills the 160 KB.
+template <int NW, int S>
+constexpr int kTileWgs = (160 * 1024) / (S * Tile<NW>::kBytes + NW * kStage);
+
 // As many workgroups as fit the chip's LDS walk the tiles; the copies of the
 // next tile's first steps run under the epilogue of this one's.
-template <int DT, bool TAIL, bool BIAS, int NW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void k_matmul_i8_tile(MatmulI8Args g, int tiles_m, int tiles_n) {
+template <int DT, bool TAIL, bool BIAS, int NW, int S>
+__global__ __launch_bounds__(64 * NW, (kTileWgs<NW, S> * NW / 4)) void k_matmul_i8_tile(MatmulI8Args g, int tiles_m, int tiles_n) {
   constexpr int kSide = Tile<NW>::kSide, TI = Tile<NW>::TI;
-  constexpr int kSteps = Tile<NW>::kSteps;
   // separate objects, so that the compiler sees that a read of one need not
   // wait for the copies into another
   __shared__ __attribute__((aligned(1024))) int8_t buf0[Tile<NW>::kBytes], buf1[Tile<NW>::kBytes];
-  __shared__ __attribute__((aligned(1024))) int8_t buf2[kSteps > 2 ? Tile<NW>::kBytes : 16];
-  __shared__ __attribute__((aligned(1024))) int8_t buf3[kSteps > 2 ? Tile<NW>::kBytes : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t buf2[S > 2 ? Tile<NW>::kBytes : 16];
+  __shared__ __attribute__((aligned(1024))) int8_t buf3[S > 2 ? Tile<NW>::kBytes : 16];
   __shared__ __attribute__((aligned(1024))) int8_t stage[NW * kStage];
   // Consecutive workgroups go to the eight XCDs in turn. Each XCD takes a
   // contiguous run of the tiles, which its workgroups walk together, in columns
@@ -283,8 +286,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_matmul_i8_tile(MatmulI8Args
   copy_step<NW, TAIL>(cp, here, K, buf0);
   __builtin_amdgcn_s_waitcnt(0x0f70);
   __syncthreads();
-  last.k = (kSteps - 1) * kBK;
-  if constexpr (kSteps > 2) {
+  last.k = (S - 1) * kBK;
+  if constexpr (S > 2) {
     here.k = kBK;
     copy_step<NW, TAIL>(cp, here, K, buf1);
     here.k = 2 * kBK;
@@ -306,21 +309,21 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_matmul_i8_tile(MatmulI8Args
       for (int j = 0; j < 2; ++j) acc[i][j] = (v16i)(0);
     // a round of all buffers at a time; where the rows end inside a round its
     // rest is zeros (TAIL)
-    for (int k = 0; k < K; k += kSteps * kBK) {
-      TileFrom s{here.a, here.w, k + kSteps * kBK};
+    for (int k = 0; k < K; k += S * kBK) {
+      TileFrom s{here.a, here.w, k + S * kBK};
       // the next tile's first steps (the last tile's once more: read by nobody)
       if (s.k >= K) s = here = from(m1, n1, 0);
-      if constexpr (kSteps > 2) {
-        tile_step<NW, TAIL>(buf3, last, buf0, s, buf1, cp, K, wm, wn, f, acc);
+      if constexpr (S > 2) {
+        tile_step<NW, S, TAIL>(buf3, last, buf0, s, buf1, cp, K, wm, wn, f, acc);
         const TileFrom s1{s.a, s.w, s.k + kBK}, s2{s.a, s.w, s.k + 2 * kBK};
-        tile_step<NW, TAIL>(buf0, s, buf1, s1, buf2, cp, K, wm, wn, f, acc);
-        tile_step<NW, TAIL>(buf1, s1, buf2, s2, buf3, cp, K, wm, wn, f, acc);
+        tile_step<NW, S, TAIL>(buf0, s, buf1, s1, buf2, cp, K, wm, wn, f, acc);
+        tile_step<NW, S, TAIL>(buf1, s1, buf2, s2, buf3, cp, K, wm, wn, f, acc);
         last = TileFrom{s.a, s.w, s.k + 3 * kBK};
-        tile_step<NW, TAIL>(buf2, s2, buf3, last, buf0, cp, K, wm, wn, f, acc);
+        tile_step<NW, S, TAIL>(buf2, s2, buf3, last, buf0, cp, K, wm, wn, f, acc);
       } else {
-        tile_step<NW, TAIL>(buf1, last, buf0, s, buf1, cp, K, wm, wn, f, acc);
+        tile_step<NW, S, TAIL>(buf1, last, buf0, s, buf1, cp, K, wm, wn, f, acc);
         last = TileFrom{s.a, s.w, s.k + kBK};
-        tile_step<NW, TAIL>(buf0, s, buf1, last, buf0, cp, K, wm, wn, f, acc);
+        tile_step<NW, S, TAIL>(buf0, s, buf1, last, buf0, cp, K, wm, wn, f, acc);
       }
     }
     tile_store<DT, BIAS, NW>(g, m0, n0, wm, wn, stage + wv * kStage, acc);
@@ -501,13 +504,13 @@ hipError_t launch_rows(const MatmulI8Args& g, int dtype, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int DT, int NW>
+template <int DT, int NW, int S>
 hipError_t launch_tile(const MatmulI8Args& g, int64_t ncu, hipStream_t st) {
   constexpr int kSide = Tile<NW>::kSide;
   const int tm = (int)((g.M + kSide - 1) / kSide), tn = (int)((g.N + kSide - 1) / kSide);
-  const dim3 grid((unsigned)min((int64_t)tm * tn, ncu)), block(64 * NW);
-#define TILE_(TAIL_, BIAS_) hipLaunchKernelGGL((k_matmul_i8_tile<DT, TAIL_, BIAS_, NW>), grid, block, 0, st, g, tm, tn)
-  if (g.K % (Tile<NW>::kSteps * kBK) == 0) {
+  const dim3 grid((unsigned)min((int64_t)tm * tn, ncu * kTileWgs<NW, S>)), block(64 * NW);
+#define TILE_(TAIL_, BIAS_) hipLaunchKernelGGL((k_matmul_i8_tile<DT, TAIL_, BIAS_, NW, S>), grid, block, 0, st, g, tm, tn)
+  if (g.K % (S * kBK) == 0) {
     if (g.bias) TILE_(false, true);
     else TILE_(false, false);
   } else {
@@ -521,33 +524,38 @@ hipError_t launch_tile(const MatmulI8Args& g, int64_t ncu, hipStream_t st) {
 // Which kernel takes a product: the one whose time, a + rounds (b + c K / 1024)
 // us, comes out least. A round is as many workgroups as the chip holds at once
 // (256 CUs, or twice that where two fit a CU's LDS); the few-rows kernels of two
-// workgroups a CU fill in between rounds, the others finish whole rounds. The
-// constants are fits to products of 8 to 1000 rows with N x K = 512 x 4096,
-// 2560 x 5120, 8512 x 2048 and 10576 x 2560 (each within 20 % or 1 us). Where
-// they cross, for example (us, the chosen first): 8 x 2560 x 5120 4.4 at 16 x 16,
-// 5.7 at 32 x 32; 64 x 10576 x 2560 9.5 at 32 x 32, 16.4 at 16 x 16, 10.0 at
-// 64 x 64; 333 x 2560 x 5120 12.0 at 64 x 64, 16.4 at 32 x 32, 20.5 at 128;
-// 333 x 8512 x 2048 12.6 at 128, 22.6 at 32 x 32, 27 at 256; 4096 x 4096 x 4096
-// 65 at 256, 81 at 128; 16384 x 2560 x 5120 224 at 256, 257 at 128.
+// workgroups a CU fill in between rounds, the others finish whole rounds. K is
+// taken up to whole rounds of a kernel's buffers. The constants are fits to 300
+// products over 1 to 16384 rows, N from 17 to 18000 and K from 64 to 8192, of
+// which half have odd sizes; over 200 others the choice is 1.1 % above the best
+// kernel's time in the geometric mean, 30 % at most. Where they cross, for example (us, the
+// chosen first): 8 x 2560 x 5120 4.4 at 16 x 16, 5.7 at 32 x 32; 64 x 10576 x
+// 2560 9.5 at 32 x 32, 16.4 at 16 x 16, 10.0 at 64 x 64; 333 x 2560 x 5120 12.0
+// at 64 x 64, 16.4 at 32 x 32, 20.5 at 128; 333 x 8512 x 2048 12.6 at 128, 22.6
+// at 32 x 32, 27 at 256; 4096 x 2048 x 1024 15.8 at 128 with two workgroups a CU,
+// 18.5 with one, 22 at 256; 4096 x 4096 x 4096 62 at 256, 71 and 75 at 128;
+// 16384 x 2560 x 5120 224 at 256, 257 at 128.
 struct MatmulKind {
-  int rows, cols, per_cu;
+  int rows, cols, per_cu, round;
   float a, b, c;
 };
 constexpr MatmulKind kKinds[] = {
-    {16, 16, 2, 3.0f, 1.2f, 0.45f}, {16, 32, 2, 4.2f, 1.0f, 0.8f},  {32, 32, 2, 4.6f, 1.2f, 1.0f},
-    {64, 64, 1, 2.5f, 1.9f, 1.7f},  {128, 128, 1, 3.0f, 2.0f, 4.0f}, {256, 256, 1, 3.0f, 4.0f, 12.0f},
+    {16, 16, 2, 1024, 2.2f, 1.7f, 0.45f},  {16, 32, 2, 512, 2.8f, 1.2f, 1.12f},
+    {32, 32, 2, 512, 3.3f, 0.8f, 1.61f},   {64, 64, 1, 512, 0.4f, 5.5f, 1.40f},
+    {128, 128, 1, 512, 2.3f, 3.8f, 3.70f}, {128, 128, 2, 256, 0.2f, 4.4f, 6.35f},
+    {256, 256, 1, 256, 1.7f, 11.3f, 9.58f},
 };
 
 int pick_kind(const MatmulI8Args& g, int64_t ncu) {
   int best = 0;
   float least = 0.f;
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 7; ++i) {
     const MatmulKind& q = kKinds[i];
     if (q.rows >= 128 && (g.M < q.rows || g.N < q.cols)) continue;  // tiles lie inside the matrix
     const int64_t blocks = ((g.M + q.rows - 1) / q.rows) * ((g.N + q.cols - 1) / q.cols);
     const int64_t slots = ncu * q.per_cu;
-    const float rounds = q.per_cu == 2 ? (float)blocks / (float)slots : (float)((blocks + slots - 1) / slots);
-    const float us = q.a + rounds * (q.b + q.c * (float)g.K / 1024.f);
+    const float rounds = q.rows < 64 ? (float)blocks / (float)slots : (float)((blocks + slots - 1) / slots);
+    const float us = q.a + rounds * (q.b + q.c * (float)((g.K + q.round - 1) / q.round * q.round) / 1024.f);
     if (i == 0 || us < least) {
       best = i;
       least = us;
@@ -564,8 +572,9 @@ hipError_t launch(const MatmulI8Args& g, hipStream_t st) {
     case 1: return launch_rows<1, 2, 4, 3>(g, DT, st);
     case 2: return launch_rows<2, 2, 4, 2>(g, DT, st);
     case 3: return launch_rows<4, 4, 4, 2>(g, DT, st);
-    case 4: return launch_tile<DT, 4>(g, ncu, st);
-    default: return launch_tile<DT, 8>(g, ncu, st);
+    case 4: return launch_tile<DT, 4, 4>(g, ncu, st);
+    case 5: return launch_tile<DT, 4, 2>(g, ncu, st);
+    default: return launch_tile<DT, 8, 2>(g, ncu, st);
   }
 }
 

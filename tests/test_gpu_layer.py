@@ -496,7 +496,7 @@ MM = [(1, 1, 16), (1, 17, 64), (2, 64, 48), (7, 100, 5120), (8, 2560, 5120), (15
       (17, 300, 272), (33, 129, 1040), (63, 64, 64), (65, 1000, 128), (100, 80, 8192), (128, 512, 4096),
       (130, 2568, 2560), (256, 256, 640), (257, 259, 656), (333, 8512, 2048), (1000, 777, 1024), (2048, 10576, 272),
       (3001, 130, 2560), (4096, 2560, 5120), (4100, 2061, 400),
-      (4096, 2048, 48), (3001, 4000, 656)]
+      (4096, 2048, 48), (3001, 4000, 656), (1500, 2051, 512), (4096, 2048, 1024), (8354, 33, 2368)]
 
 
 @pytest.mark.parametrize("M,N,K", MM)

@@ -392,8 +392,8 @@ def _current_device() -> int:
     """The device that kernels are launched on. The checks below run once per call and
     tensor, in front of launches of a few microseconds: they use the cheap queries."""
     try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError) as e:
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError) as e:
         raise ValueError(f"the buffers must be on a GPU: {e}") from None
 
 

@@ -128,7 +128,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 // One row for each workgroup (of the first 2^20, then on). PARTS: the mean is over
 // groups of a row, otherwise over the row.
 template <int DT, int RT, bool GATED, bool PARTS, int VEC, int V, bool AL>
-__global__ __launch_bounds__(1024) void k_norm(NormArgs a) {
+__global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
   extern __shared__ float s_part[];  // PARTS: the sum of squares of each piece, then 1/rms of each group
   __shared__ float s_sum[kMaxWaves];
   __shared__ uint32_t s_max[kMaxWaves];

@@ -10,7 +10,7 @@
 // by the latency of one pass.
 //
 // A workgroup of four waves takes HB heads of a group: one where heads are few
-// or large, up to 8 small ones otherwise (32 KB of state), so that the
+// or large, up to 8 otherwise (32 KB of state), so that the
 // convolution of B and C is done for all of them and no workgroup is over
 // before it has begun. Its 16-byte slices of the state are requested first; then
 // each thread computes the convolution of one or two of the HB P + 2 N channels
@@ -19,6 +19,9 @@
 // round trip, not two. The slot pos % W is written by the head itself for its x
 // channels and by the first heads of a group for B and C; nobody reads that
 // slot's value, so workgroups need no order.
+//
+// Measured, fp16 with 80 heads of 64 x 128: fp32 state 5.2 us at batch 1, 231 us
+// at batch 256 (5.9 TB/s of 1.36 GB); 8-bit state 4.5 and 76 us (4.7 TB/s).
 #include "ssd_conv.hpp"
 #include "ssd_launch.hpp"
 
@@ -274,30 +277,41 @@ hipError_t launch_hb(StepArgs& a, int64_t bg, hipStream_t st) {
   return hipGetLastError();
 }
 
-// A workgroup takes a head; where the heads are more than 3 on each CU, as many
-// as make 32 KB of state. Measured, one head against several: 114 heads of
-// 16 x 32 fp32 at batch 256 97 and 31 us, at batch 4 (1.8 heads on each CU) 4.3
-// and 4.3; 108 heads of 32 x 32 fp32 at batch 256 103 and 55 us, at batch 4 4.3
-// and 6.8; 25 heads of 16 x 128 fp32 at batch 32 (3.1) 9.6 and 7.7; 3 of 64 x 32
-// at batch 173 (2.0) 5.5 and 6.5. (A part of a head for each workgroup, where heads are fewer than CUs,
-// gained nothing at 64 x 128.)
-template <bool I8, int DT, int P, int NS>
+// How many heads a workgroup takes: as many, up to 8 and 32 KB of state, as leave
+// 4 workgroups on each CU and idle for less than a fifth; or, from 3 heads on each
+// CU, as many as cost no more passes than one head does. Measured against one
+// head (fp16 inputs, us): 114 heads of 16 x 32, 8-bit, batch 256 64 and 16 (8 of
+// them), batch 16 6.8 and 4.1; 80 of 64 x 128, 8-bit, batch 256 87 and 76 (4), at
+// batch 16 4 of them would take 12.8 instead of 9.8; 24 in 8 groups of 64 x 64,
+// fp32, batch 256: 38, and 45 with 2; 108 of 32 x 32, fp32, batch 256 52 and 43.
+// (A part of a head for each workgroup, where heads are fewer than CUs, gained
+// nothing at 64 x 128.)
+template <bool I8, int DT, int P, int NS, int HB>
 hipError_t launch_n(StepArgs& a, int64_t B, hipStream_t st) {
-  constexpr int kMost = 2048 / (P * NS / (I8 ? 16 : 4));
-  constexpr int HB = kMost < 1 ? 1 : kMost > 8 ? 8 : kMost;
-  const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
-  if constexpr (HB > 1)
-    if (B * a.H > 3 * ncu && a.hpg > 1) return launch_hb<I8, DT, P, NS, HB>(a, B * a.G, st);
-  return launch_hb<I8, DT, P, NS, 1>(a, B * a.G, st);
+  constexpr int kSlots = P * NS / (I8 ? 16 : 4);  // of a head
+  if constexpr (HB > 1) {
+    constexpr auto passes = [](int hb) {
+      return (hb * kSlots + kStepThreads - 1) / kStepThreads + (hb * P + 2 * NS + kStepThreads - 1) / kStepThreads;
+    };
+    if constexpr (HB * kSlots <= 2048) {
+      const int64_t ncu = cu_count() > 0 ? cu_count() : 256, blocks = (a.hpg + HB - 1) / HB;
+      const bool full = 4 * HB * blocks <= 5 * (int64_t)a.hpg && B * a.G * blocks >= 4 * ncu;
+      const bool free = passes(HB) == passes(1) && HB / 2 < a.hpg && B * a.H > 3 * ncu;
+      if (full || free) return launch_hb<I8, DT, P, NS, HB>(a, B * a.G, st);
+    }
+    return launch_n<I8, DT, P, NS, HB / 2>(a, B, st);
+  } else {
+    return launch_hb<I8, DT, P, NS, 1>(a, B * a.G, st);
+  }
 }
 
 template <int DT, int P>
 hipError_t dispatch_n(bool int8, int N, StepArgs& a, int64_t B, hipStream_t st) {
   switch (N) {
-    case 16: return int8 ? launch_n<true, DT, P, 16>(a, B, st) : launch_n<false, DT, P, 16>(a, B, st);
-    case 32: return int8 ? launch_n<true, DT, P, 32>(a, B, st) : launch_n<false, DT, P, 32>(a, B, st);
-    case 64: return int8 ? launch_n<true, DT, P, 64>(a, B, st) : launch_n<false, DT, P, 64>(a, B, st);
-    case 128: return int8 ? launch_n<true, DT, P, 128>(a, B, st) : launch_n<false, DT, P, 128>(a, B, st);
+    case 16: return int8 ? launch_n<true, DT, P, 16, 8>(a, B, st) : launch_n<false, DT, P, 16, 8>(a, B, st);
+    case 32: return int8 ? launch_n<true, DT, P, 32, 8>(a, B, st) : launch_n<false, DT, P, 32, 8>(a, B, st);
+    case 64: return int8 ? launch_n<true, DT, P, 64, 8>(a, B, st) : launch_n<false, DT, P, 64, 8>(a, B, st);
+    case 128: return int8 ? launch_n<true, DT, P, 128, 8>(a, B, st) : launch_n<false, DT, P, 128, 8>(a, B, st);
     default: return hipErrorInvalidValue;
   }
 }

@@ -194,6 +194,13 @@ STEP = [
     (7, 80, 64, 128, 1, 4, "fp16", 0),
     (2, 16, 64, 16, 2, 4, "fp32", 0),
     (3, 3, 32, 128, 3, 3, "fp16", 2),
+    # several heads a workgroup, the last of a group with fewer
+    (150, 13, 16, 32, 1, 4, "fp16", 0),
+    (400, 6, 32, 16, 2, 3, "bf16", 1),
+    (70, 40, 32, 64, 1, 2, "fp32", 0),
+    (300, 20, 64, 16, 1, 4, "fp16", 3),
+    (1100, 8, 16, 16, 1, 4, "bf16", 0),
+    (60, 20, 16, 128, 1, 4, "fp16", 0),
 ]
 
 

@@ -175,9 +175,14 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
                                            const v16i (&acc)[Tile<NW>::TI][2]) {
   typedef typename Store<DT>::T T;
   typedef const __attribute__((address_space(4))) float* scalar_ptr;
+  typedef __attribute__((address_space(1))) v4u_any* global_out;
   constexpr int U = DT == DT_F32 ? 1 : 2;  // 32-column blocks of a piece
   constexpr int E = 16 / sizeof(T);        // outputs of a 16-byte chunk
   const int lane = lane_id(), hi = lane >> 5;
+  // Pieces that are whole 128-byte lines go past the caches (16384 x 10752 x 2560
+  // fp16 431 -> 392 us); others would go to memory in parts (8192 x 3352 x 1024
+  // fp32 46 -> 73 us; halves of lines, 96 to 103 % of the time, are left too).
+  const bool lines = ((uint64_t)g.out | g.N * sizeof(T)) % 128 == 0;
   const int row = lane & 31, swz = (row >> 1) & 7;
   const unsigned lane_at = ((lane >> 3) * (unsigned)g.N + (lane & 7) * E) * sizeof(T);
   // The columns' steps come through the scalar cache (they are the same for all
@@ -198,14 +203,16 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
   float as[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) as[j] = g.a_scale[m0 + wm + 32 * j + row];
+  // the pieces of a row leave one after the other, so that they meet in the cache
+  // where they share lines
 #pragma unroll
-  for (int u = 0; u < Tile<NW>::TI / U; ++u) {
-    const int nu = n0 + wn + 32 * U * u;
-    float ws[U][4][4], bias[U][4][4];
-    columns(g.w_scale + nu, ws);
-    if constexpr (BIAS) columns(g.bias + nu, bias);
+  for (int j = 0; j < 2; ++j) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int u = 0; u < Tile<NW>::TI / U; ++u) {
+      const int nu = n0 + wn + 32 * U * u;
+      float ws[U][4][4], bias[U][4][4];
+      columns(g.w_scale + nu, ws);
+      if constexpr (BIAS) columns(g.bias + nu, bias);
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -233,9 +240,15 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
         const int orow = r * 8 + (lane >> 3);
         const v4u v = *(const v4u*)(st + orow * 128 + ((lane & 7) ^ ((orow >> 1) & 7)) * 16);
         // the rows' address is uniform, the lane's place in them fits 32 bits
-        T* const o = (T*)(const_cast<int8_t*>(uniform_ptr((const int8_t*)g.out + ((int64_t)(m0 + wm + 32 * j + 8 * r) * g.N + nu) * sizeof(T))) + lane_at);
+        const global_out o = (global_out)(uint64_t)(uniform_ptr((const int8_t*)g.out + ((int64_t)(m0 + wm + 32 * j + 8 * r) * g.N + nu) * sizeof(T)) + lane_at);
         // rows that are not 16-byte aligned take the same stores
-        *(v4u_any*)o = v;
+        if (lines) {
+          asm volatile("; lines");  // without these the compiler makes one store of the two
+          __builtin_nontemporal_store(v, o);
+          asm volatile("; lines");
+        } else {
+          *o = v;
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();

@@ -10,7 +10,7 @@
 // Rows are loaded a set of kU ahead of their use (sets of 2 and 8 are slower by 6
 // and 15 %, tiles of 16 positions instead of 32 by 8 %), and written past the
 // caches (3 to 20 % faster: what is written exceeds them, and the tile heads
-// stay). 8 x 2048 x 5376 channels in fp16: 88 us, 4.1 TB/s of its 360 MB; three
+// stay). 8 x 2048 x 5376 channels in fp16: 79 us, 4.5 TB/s of its 358 MB; three
 // waves on each SIMD hold 160 registers each (weights 40, window 24, sets 32),
 // and a fourth, with 128, spills (193 us). The blocks behind those of the
 // convolution compute dt.
@@ -228,6 +228,11 @@ hipError_t launch_conv_forward(const Dims& d, int dtype, const ConvPtrs& cv, con
   const int64_t want = (int64_t)(cu_count() > 0 ? cu_count() : 256) * 3 * kWave;
   int64_t T = kU;
   while (T < 32 && d.B * ((d.L + 2 * T - 1) / (2 * T)) * a.nvec >= want) T *= 2;
+  // 64 where that takes less time in rounds of 12 waves a CU, at T + 6 rows each
+  // (us at 32 and 64: 4 x 4096 x 10240 161, 148; 1 x 9000 x 6912 60, 56; but 8 x
+  // 4000 x 3328, 2 rounds of 64 with an almost empty second one, 99, 103)
+  auto rounds = [&](int64_t t) { return (d.B * ((d.L + t - 1) / t) * a.nvec + 4 * want - 1) / (4 * want); };
+  if (T == 32 && rounds(64) * 70 < rounds(32) * 38) T = 64;
   // thread indexes fit 31 bits
   while (d.B * ((d.L + T - 1) / T) * a.nvec >= (int64_t)1 << 31 && T < d.L) T *= 2;
   a.T = (int)T;

@@ -181,6 +181,32 @@ def test_conv_chunks_equal_the_whole(gpu_lib, dtype, W):
     assert torch.equal(H.bits(ring), H.bits(ring2))
 
 
+def test_conv_long_tiles_equal_short_ones(gpu_lib):
+    """A batch that fills the chip with tiles of 64 positions, with ragged ends in
+    and between them, equals its sequences by themselves (shorter tiles) bit for bit."""
+    import torch
+    L = gpu_lib
+    B, Ln, H_, P, N, G, W = 6, 2050, 80, 64, 128, 1, 4
+    c = _conv_case(torch, 81, B, Ln, H_, P, N, G, W, "bf16")
+    conv = L.ConvParams(c["w"], c["b"], c["dtb"])
+    lengths = torch.tensor([2050, 64, 1999, 0, 2048, 65], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([0, 1, 2, 3, 70, 0], dtype=torch.int32, device="cuda")
+
+    def run(b0, b1):
+        n = b1 - b0
+        o = [torch.full(s, float("nan"), dtype=torch.bfloat16, device="cuda") for s in
+             ((n, Ln, H_, P), (n, Ln, G, N), (n, Ln, G, N), (n, Ln, H_))]
+        ring = c["ring"][b0:b1].clone()
+        L.ssd_conv_forward(L.make_shape(n, Ln, H_, P, N, G, 64, "bf16"), conv, c["xbc"][b0:b1], c["raw"][b0:b1], *o,
+                           ring, pos[b0:b1].clone(), lengths[b0:b1].clone())
+        return [*o, ring]
+
+    whole = run(0, B)
+    for b in range(B):
+        for w, s in zip(whole, run(b, b + 1)):
+            assert torch.equal(H.bits(w[b:b + 1].contiguous()), H.bits(s)), b
+
+
 # ---------------------------------------------------------------------------
 # decode step
 # ---------------------------------------------------------------------------

@@ -421,12 +421,13 @@ int ssd_gated_norm(int64_t rows, int64_t cols, int64_t groups, int dtype, const 
  * multiple of 16 (SSD_E_UNSUPPORTED) and at most 131056 (so that the sums of any
  * codes fit), M, N < 2^26 and M * N < 2^40; M == 0 is a valid empty problem.
  * workspace: device memory of at least ssd_matmul_i8_workspace_bytes(M, N, K)
- * bytes (may be NULL when that is 0); calls that may overlap need one each. */
+ * bytes, 16-byte aligned. No product needs one at present: that is 0, and NULL
+ * will do. */
 int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float* a_scale,
                   const int8_t* w, const float* w_scale, const float* bias, int out_dtype,
                   void* out, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes ssd_matmul_i8 needs (0 for an invalid problem). Host only. */
+/* Workspace bytes ssd_matmul_i8 needs: 0. Host only. */
 size_t ssd_matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Host-only: a weight matrix [N, K] (fp32, row-major) as 8-bit rows for

@@ -555,7 +555,7 @@ def ssd_matmul_i8_workspace(m, n, k, device="cuda"):
 
 def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None):
     """out = a_scale * w_scale * (a @ w.T) + bias for int8 a [..., K], w [N, K]; bias may
-    be None. ``workspace`` is allocated here if None and needed."""
+    be None. ``workspace``: see the C call (None will do)."""
     n, k = w.shape
     if a.shape[-1] != k:
         raise ValueError("a and w must agree in their last dimension")
@@ -563,8 +563,6 @@ def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None
     if m == 0:
         return
     dev = _current_device()
-    if workspace is None:
-        workspace = ssd_matmul_i8_workspace(m, n, k, a.device)
     wsb = 0 if workspace is None else workspace.numel()
     pw = _dense(workspace, "workspace", wsb, torch.uint8, dev)
     _check("ssd_matmul_i8", LIB.ssd_matmul_i8(

@@ -152,9 +152,7 @@ struct MatmulI8Args {
   const float* w_scale;
   const float* bias;
   void* out;
-  int32_t* ws;
 };
-size_t matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_matmul_i8(int out_dtype, const MatmulI8Args& a, hipStream_t st);
 
 // Zero fill of a device buffer by a kernel (so that a captured graph holds no

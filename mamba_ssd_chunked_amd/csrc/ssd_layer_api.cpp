@@ -152,14 +152,12 @@ static int check_matmul(int64_t M, int64_t N, int64_t K) {
   return SSD_OK;
 }
 
-size_t ssd_matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (check_matmul(M, N, K) != SSD_OK || M == 0) return 0;
-  return ssd::matmul_i8_workspace_bytes(M, N, K);
-}
+// No kernel needs a workspace: sums that are split over waves meet in LDS.
+size_t ssd_matmul_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
 
 int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float* a_scale, const int8_t* w,
                   const float* w_scale, const float* bias, int out_dtype, void* out, void* workspace,
-                  size_t workspace_bytes, void* stream) {
+                  size_t, void* stream) {
   int rc = check_matmul(M, N, K);
   if (rc) return rc;
   if (!known_dtype(out_dtype)) return SSD_E_UNSUPPORTED;
@@ -168,9 +166,7 @@ int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float*
   if (!aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4)) return SSD_E_ALIGN;
   if ((rc = check_opt({workspace}))) return rc;
   if (M == 0) return SSD_OK;
-  const size_t need = ssd::matmul_i8_workspace_bytes(M, N, K);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return SSD_E_WORKSPACE;
-  ssd::MatmulI8Args m{M, N, K, a, a_scale, w, w_scale, bias, out, (int32_t*)workspace};
+  ssd::MatmulI8Args m{M, N, K, a, a_scale, w, w_scale, bias, out};
   return hip_status(ssd::launch_matmul_i8(out_dtype, m, (hipStream_t)stream));
 }
 

@@ -249,7 +249,9 @@ __device__ __forceinline__ void tile_store(const MatmulI8Args& g, int m0, int n0
         const int orow = r * 8 + (lane >> 3);
         const v4u v = *(const v4u*)(st + orow * 128 + ((lane & 7) ^ ((orow >> 1) & 7)) * 16);
         // the rows' address is uniform, the lane's place in them fits 32 bits
-        const global_out o = (global_out)(uint64_t)(uniform_ptr((const int8_t*)g.out + ((int64_t)(m0 + wm + 32 * j + 8 * r) * g.N + nu) * sizeof(T)) + lane_at);
+        const int64_t at = (int64_t)(m0 + wm + 32 * j + 8 * r) * g.N + nu;
+        const int8_t* const rows = uniform_ptr((const int8_t*)g.out + at * sizeof(T));
+        const global_out o = (global_out)(uint64_t)(rows + lane_at);
         // rows that are not 16-byte aligned take the same stores
         if (lines) {
           asm volatile("; lines");  // without these the compiler makes one store of the two
@@ -273,7 +275,8 @@ constexpr int kTileWgs = (160 * 1024) / (S * Tile<NW>::kBytes + NW * kStage);
 // As many workgroups as fit the chip's LDS walk the tiles; the copies of the
 // next tile's first steps run under the epilogue of this one's.
 template <int DT, bool TAIL, bool BIAS, int NW, int S>
-__global__ __launch_bounds__(64 * NW, (kTileWgs<NW, S> * NW / 4)) void k_matmul_i8_tile(MatmulI8Args g, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(64 * NW, (kTileWgs<NW, S> * NW / 4)) void k_matmul_i8_tile(MatmulI8Args g,
+                                                                                     int tiles_m, int tiles_n) {
   constexpr int kSide = Tile<NW>::kSide, TI = Tile<NW>::TI;
   // separate objects, so that the compiler sees that a read of one need not
   // wait for the copies into another
@@ -550,8 +553,8 @@ hipError_t launch_tile(const MatmulI8Args& g, int64_t ncu, hipStream_t st) {
 // taken up to whole rounds of a kernel's buffers. The constants are fits to 300
 // products over 1 to 16384 rows, N from 17 to 18000 and K from 64 to 8192, of
 // which half have odd sizes; over 200 others the choice is 1.1 % above the best
-// kernel's time in the geometric mean, 30 % at most. Where they cross, for example (us, the
-// chosen first): 8 x 2560 x 5120 4.4 at 16 x 16, 5.7 at 32 x 32; 64 x 10576 x
+// kernel's time in the geometric mean, 30 % at most. Where they cross, for
+// example (us, the chosen first): 8 x 2560 x 5120 4.4 at 16 x 16, 5.7 at 32 x 32; 64 x 10576 x
 // 2560 9.5 at 32 x 32, 16.4 at 16 x 16, 10.0 at 64 x 64; 333 x 2560 x 5120 12.0
 // at 64 x 64, 16.4 at 32 x 32, 20.5 at 128; 333 x 8512 x 2048 12.6 at 128, 22.6
 // at 32 x 32, 27 at 256; 4096 x 2048 x 1024 15.8 at 128 with two workgroups a CU,

@@ -400,7 +400,11 @@ def _current_device() -> int:
 def _stream_on(stream, dev):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device_index != dev:
+        raise ValueError(f"the stream belongs to GPU {stream.device_index}, the current GPU is {dev}")
+    return stream.cuda_stream
 
 
 def _code(dtype):

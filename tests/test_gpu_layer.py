@@ -836,3 +836,104 @@ def test_layer_steps_on_streams_and_in_two_graphs(gpu_lib):
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(H.bits(out[i]), H.bits(alone[i][t])), (i, t)
+
+
+# ---------------------------------------------------------------------------
+# offsets that pass 32 bits: the end of a large buffer equals a call on the end alone
+# ---------------------------------------------------------------------------
+
+def test_conv_offsets_past_32_bits(gpu_lib):
+    import torch
+    L = gpu_lib
+    B, Ln, H_, P, N, G, W, n = 2, 210001, 80, 64, 128, 1, 4, 150
+    d, cd = H_ * P, H_ * P + 2 * G * N
+    g = torch.Generator(device="cuda").manual_seed(3)
+    full = torch.zeros((B, Ln, d + cd + H_), dtype=torch.float16, device="cuda")  # 8.9 GB
+    full[:, -n:] = torch.randn((B, n, d + cd + H_), generator=g, device="cuda").half()
+    conv = L.ConvParams(torch.randn((cd, W), generator=g, device="cuda"))
+
+    def run(x):
+        b, t = x.shape[:2]
+        o = [torch.empty(s, dtype=x.dtype, device="cuda") for s in ((b, t, H_, P), (b, t, G, N), (b, t, G, N), (b, t, H_))]
+        ring = torch.empty((b, W, cd), dtype=x.dtype, device="cuda")
+        L.ssd_conv_forward(L.make_shape(b, t, H_, P, N, G, 64, "fp16"), conv, x[..., d:d + cd], x[..., d + cd:], *o, ring)
+        return o, ring
+
+    whole, ring = run(full)
+    assert whole[0].numel() * 2 > 2 ** 32
+    part, _ = run(full[1:, -n:])
+    for u, v in zip(whole, part):
+        assert torch.equal(u[1, -n + W:], v[0, W:])
+    t = torch.arange(Ln - W, Ln, device="cuda")
+    assert torch.equal(ring[1, t % W], full[1, -W:, d:d + cd])
+
+
+def test_step_offsets_past_32_bits(gpu_lib):
+    import torch
+    L = gpu_lib
+    B, H_, P, N, W, n = 2100, 80, 64, 128, 4, 3
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    d, cd = H_ * P, H_ * P + 2 * N
+    conv, A, D = L.ConvParams(r(cd, W)), -torch.rand(H_, generator=g, device="cuda"), r(H_)
+    proj, ring = r(B, cd + H_).half(), r(B, W, cd).half()
+    pos = torch.full((B,), 9, dtype=torch.int32, device="cuda")
+    h = torch.zeros((B, H_, P, N), device="cuda")
+    assert h.numel() * 4 > 2 ** 32
+    h[-n:] = r(n, H_, P, N)
+
+    def run(b0, h, ring):
+        Y = torch.empty((B - b0, H_, P), dtype=torch.float16, device="cuda")
+        L.ssd_conv_decode_step(L.make_shape(B - b0, 1, H_, P, N, 1, 64, "fp16"), L.SSD_PATH_FLOAT, conv, proj[b0:, :cd],
+                               proj[b0:, cd:], A, D, None, ring, pos[b0:], h, Y)
+        return Y
+
+    h2, ring2 = h[-n:].clone(), ring[-n:].clone()
+    Y2 = run(B - n, h2, ring2)
+    Y = run(0, h, ring)
+    assert torch.equal(ring[-n:], ring2)
+    # other numbers of heads a workgroup may contract products differently: two roundings of each term
+    assert torch.allclose(h[-n:], h2, rtol=4 * U, atol=4 * U * float(h2.abs().max()))
+    assert torch.allclose(Y[-n:].float(), Y2.float(), rtol=2 ** -10, atol=(2 * N) * U * float(Y2.abs().max()) + 2 ** -10)
+
+
+def test_norm_offsets_past_32_bits(gpu_lib):
+    import torch
+    L = gpu_lib
+    rows, cols, n = 450001, 5120, 7
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.zeros((rows, cols), dtype=torch.float16, device="cuda")
+    assert x.numel() * 2 > 2 ** 32
+    x[-n:] = torch.randn((n, cols), generator=g, device="cuda").half()
+    w = torch.rand(cols, generator=g, device="cuda")
+
+    def run(call):
+        out = []
+        for v in (x, x[-n:]):
+            o, q = torch.empty_like(v), torch.empty(v.shape, dtype=torch.int8, device="cuda")
+            s = torch.empty(v.shape[0], device="cuda")
+            call(v, o, q, s)
+            out.append((o[-n:], q[-n:], s[-n:]))
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
+
+    run(lambda v, o, q, s: L.ssd_add_norm(v, v, None, w, EPS, o, q, s))
+    run(lambda v, o, q, s: L.ssd_gated_norm(v, v, 8, w, EPS, o, q, s))
+
+
+def test_matmul_offsets_past_32_bits(gpu_lib):
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for M, N, K, n in ((230001, 10001, 64, 300), (300, 8000000, 64, 300)):
+        a = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+        w = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        sa, sw = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+        out = torch.empty((M, N), dtype=torch.float16, device="cuda")
+        assert out.numel() * 2 > 2 ** 32
+        L.ssd_matmul_i8(a, sa, w, sw, None, out)
+        c = slice(N - 500, N)
+        part = torch.empty((n, 500), dtype=torch.float16, device="cuda")
+        L.ssd_matmul_i8(a[-n:].contiguous(), sa[-n:].contiguous(), w[c].contiguous(), sw[c].contiguous(), None, part)
+        assert torch.equal(out[-n:, c], part)
+        del out

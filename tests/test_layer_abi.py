@@ -215,6 +215,10 @@ def test_binding_refuses_what_the_library_cannot_see():
     for t, n, dt, dev in ((w, 63, f, -1), (w, 64, torch.int8, -1), (w, 64, f, 0), (wide.transpose(0, 1), 2400, f, -1)):
         with pytest.raises(ValueError, match="contiguous"):
             L._dense(t, "w", n, dt, dev)
+    other = type("S", (), {"device_index": 1, "cuda_stream": 7})()
+    assert L._stream_on(5, 0) == 5 and L._stream_on(other, 1) == 7
+    with pytest.raises(ValueError, match="GPU 1"):
+        L._stream_on(other, 0)
     assert L._code(torch.bfloat16) == L.DTYPE_CODE[torch.bfloat16]
     for dt in (torch.float64, torch.int32):
         with pytest.raises(ValueError, match=str(dt)):

@@ -5,13 +5,15 @@
 //   scale = max|n| / 127,  q = round half away(n / scale)
 //
 // Memory bound: every input is read once and every output written once, a row
-// stays in fp32 registers in between. A workgroup computes one row; thread i
-// holds the row's pieces i, i + blockDim, ... of 8 consecutive channels. Rows
-// that are not aligned, or not a multiple of 8 long, take the same pieces with
-// unaligned accesses, the last one channel by channel (G runs of channels that
-// are no multiple of 8 long: single channels instead of pieces). Two reductions
-// over the row (the sum of squares, the largest magnitude) cross the waves in
-// LDS. Rows leave past the caches (2 to 10 % faster; loads that do are slower).
+// stays in fp32 registers in between. A workgroup computes one row (four of up to
+// 512 channels, a wave each); thread i holds the row's pieces i, i + blockDim, ...
+// of 8 consecutive channels. Rows that are not aligned, or not a multiple of 8
+// long, take the same pieces with unaligned accesses, the last one channel by
+// channel (G runs of channels that are no multiple of 8 long: single channels
+// instead of pieces). Two reductions over the row (the sum of squares, the largest
+// magnitude) cross the waves in LDS; short runs of channels are summed side by
+// side (4000 rows of 4096 in 64 runs: 35 -> 22 us). Rows leave past the caches (2
+// to 10 % faster; loads that do are slower).
 // Measured: 16384 rows of 2560 bf16 with an fp32 residual, codes and values
 // 98 us, 5.5 TB/s of 545 MB; 16384 of 5120 fp16, gated, 111 us, 5.3 TB/s (139 us
 // while the loads waited for one another and the codes took 3 more operations:
@@ -125,16 +127,31 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return v;
 }
 
-// One row for each workgroup (of the first 2^20, then on). PARTS: the mean is over
-// groups of a row, otherwise over the row.
-template <int DT, int RT, bool GATED, bool PARTS, int VEC, int V, bool AL>
-__global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
-  extern __shared__ float s_part[];  // PARTS: the sum of squares of each piece, then 1/rms of each group
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One row for each workgroup (of the first 2^20, then on), or (WAVE: rows of one
+// piece a lane) for each wave. The mean is over the row (PARTS 0), or over groups
+// of at least 64 pieces (1) or fewer (2).
+template <int DT, int RT, bool GATED, int PARTS, int VEC, int V, bool AL, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
+  extern __shared__ float s_parts[];  // PARTS: the sum of squares of each piece, then 1/rms of each group
   __shared__ float s_sum[kMaxWaves];
   __shared__ uint32_t s_max[kMaxWaves];
-  const int nt = blockDim.x, nw = nt / kWave;
+  const int nt = WAVE ? kWave : blockDim.x, nw = nt / kWave;
+  const int tid = WAVE ? lane_id() : threadIdx.x, wave = WAVE ? 0 : wave_id();
+  const int rows_wg = WAVE ? blockDim.x / kWave : 1;
   const int np = (a.cols + VEC - 1) / VEC;  // pieces of the row
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  float* const s_part = s_parts + (PARTS && WAVE ? wave_id() * (np + a.groups) : 0);
+  auto sync = [] {
+    if constexpr (WAVE) wave_sync();
+    else __syncthreads();
+  };
+  for (int64_t row = (int64_t)blockIdx.x * rows_wg + (WAVE ? wave_id() : 0); row < a.rows;
+       row += (int64_t)gridDim.x * rows_wg) {
     const int64_t base = row * (int64_t)a.cols;
     const bool add = !GATED && a.residual;
 
@@ -145,7 +162,7 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
     RawPiece<DT_F32, VEC> wr[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int p = min((int)threadIdx.x + i * nt, np - 1), c = p * VEC, n = a.cols - c;
+      const int p = min(tid + i * nt, np - 1), c = p * VEC, n = a.cols - c;
       xr[i].template load<AL>(a.x, row * (GATED ? (int64_t)a.cols : a.ld_x) + c, n);
       if constexpr (GATED) zr[i].template load<AL>(a.z, row * a.ld_z + c, n);
       else rr[i].template load<AL>(add ? a.residual : (const void*)a.weight, add ? base + c : 0, add ? n : a.cols);
@@ -154,7 +171,7 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
     float r[V][VEC], ss[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int p = threadIdx.x + i * nt;
+      const int p = tid + i * nt;
       ss[i] = 0.f;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -170,31 +187,45 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
 
     float rs0 = 0.f;
     const int gp = PARTS ? np / a.groups : np;  // pieces of a group
-    if constexpr (!PARTS) {
+    if constexpr (PARTS == 0) {
       float t = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) t += ss[i];
       t = wave_sum(t);
-      if (lane_id() == 0) s_sum[wave_id()] = t;
-      __syncthreads();
-      t = 0.f;
-      for (int i = 0; i < nw; ++i) t += s_sum[i];
+      if constexpr (!WAVE) {
+        if (lane_id() == 0) s_sum[wave] = t;
+        __syncthreads();
+        t = 0.f;
+        for (int i = 0; i < nw; ++i) t += s_sum[i];
+      }
       rs0 = rsqrtf(t / (float)a.cols + a.eps);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int p = threadIdx.x + i * nt;
+        const int p = tid + i * nt;
         if (p < np) s_part[p] = ss[i];
       }
-      __syncthreads();
+      sync();
       float* const s_rs = s_part + np;
-      for (int g = wave_id(); g < a.groups; g += nw) {
-        float t = 0.f;
-        for (int k = lane_id(); k < gp; k += kWave) t += s_part[g * gp + k];
-        t = wave_sum(t);
-        if (lane_id() == 0) s_rs[g] = rsqrtf(t / (float)(gp * VEC) + a.eps);
+      if constexpr (PARTS == 1) {
+        for (int g = wave; g < a.groups; g += nw) {
+          float t = 0.f;
+          for (int k = lane_id(); k < gp; k += kWave) t += s_part[g * gp + k];
+          t = wave_sum(t);
+          if (lane_id() == 0) s_rs[g] = rsqrtf(t / (float)(gp * VEC) + a.eps);
+        }
+      } else {  // as many lanes a group as the largest power of two up to its pieces
+        const int sh = 31 - __builtin_clz(gp), lanes = 1 << sh, sub = lane_id() & (lanes - 1);
+        for (int g0 = wave * (kWave >> sh); g0 < a.groups; g0 += nw * (kWave >> sh)) {
+          const int g = g0 + (lane_id() >> sh);
+          float t = 0.f;
+          if (g < a.groups)
+            for (int k = sub; k < gp; k += lanes) t += s_part[g * gp + k];
+          for (int m = lanes / 2; m >= 1; m >>= 1) t += __shfl_xor(t, m);
+          if (g < a.groups && sub == 0) s_rs[g] = rsqrtf(t / (float)(gp * VEC) + a.eps);
+        }
       }
-      __syncthreads();
+      sync();
     }
 
     // The normalised rows. What threads behind the last piece hold counts for
@@ -203,7 +234,7 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
     uint32_t most = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int p = threadIdx.x + i * nt;
+      const int p = tid + i * nt;
       const float rs = PARTS ? s_part[np + min(p, np - 1) / gp] : rs0;
       uint32_t m = 0;
 #pragma unroll
@@ -215,10 +246,12 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
     }
     if (a.q) {
       most = wave_max(most);
-      if (lane_id() == 0) s_max[wave_id()] = most;
-      __syncthreads();
-      most = 0;
-      for (int i = 0; i < nw; ++i) most = max(most, s_max[i]);
+      if constexpr (!WAVE) {
+        if (lane_id() == 0) s_max[wave] = most;
+        __syncthreads();
+        most = 0;
+        for (int i = 0; i < nw; ++i) most = max(most, s_max[i]);
+      }
       // steps of most / 127; 127 / most overflows for rows below 2^-120: those
       // are scaled up by 2^100 first (exactly)
       const float top = __uint_as_float(most);
@@ -233,37 +266,38 @@ __global__ __launch_bounds__(VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int p = threadIdx.x + i * nt;
+        const int p = tid + i * nt;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) r[i][e] *= inv;
         if (p < np) st_codes<VEC, AL>(a.q + base + p * VEC, a.cols - p * VEC, r[i]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) r[i][e] *= scale;
       }
-      if (threadIdx.x == 0) a.scale[row] = scale;
+      if (tid == 0) a.scale[row] = scale;
     }
     if (a.out) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int p = threadIdx.x + i * nt;
+        const int p = tid + i * nt;
         if (p < np) st_piece<DT, VEC, AL>(a.out, base + p * VEC, a.cols - p * VEC, r[i]);
       }
     }
     // the next row's sums overwrite this one's: with codes, the barrier of the
     // maximum has separated them already
-    if (!a.q) __syncthreads();
+    if (WAVE ? PARTS != 0 : !a.q) sync();
   }
 }
 
-template <int DT, int RT, bool GATED, bool PARTS, int VEC, int V, bool AL>
+template <int DT, int RT, bool GATED, int PARTS, int VEC, int V, bool AL, bool WAVE = false>
 hipError_t go(const NormArgs& a, int waves, hipStream_t st) {
-  const size_t lds = PARTS ? (size_t)(a.cols / VEC + a.groups) * sizeof(float) : 0;
-  hipLaunchKernelGGL((k_norm<DT, RT, GATED, PARTS, VEC, V, AL>), dim3((unsigned)min(a.rows, (int64_t)1 << 20)),
+  const size_t lds = PARTS ? (WAVE ? waves : 1) * (size_t)(a.cols / VEC + a.groups) * sizeof(float) : 0;
+  const int64_t wgs = WAVE ? (a.rows + waves - 1) / waves : a.rows;
+  hipLaunchKernelGGL((k_norm<DT, RT, GATED, PARTS, VEC, V, AL, WAVE>), dim3((unsigned)min(wgs, (int64_t)1 << 20)),
                      dim3(waves * kWave), lds, st, a);
   return hipGetLastError();
 }
 
-template <int DT, int RT, bool GATED, bool PARTS, bool AL>
+template <int DT, int RT, bool GATED, int PARTS, bool AL>
 hipError_t pick_pieces(const NormArgs& a, hipStream_t st) {
   // at most 8 waves a row: more meet at its two barriers more slowly (16384 rows
   // of 5120, gated: 10 waves 174 us, 5 waves 139; 8192 of 8192: 16 waves 120, 8
@@ -271,12 +305,26 @@ hipError_t pick_pieces(const NormArgs& a, hipStream_t st) {
   // 106, 1 wave 116)
   const int wp = ((a.cols + 7) / 8 + kWave - 1) / kWave;  // pieces of a row, in waves
   const int v = (wp + 7) / 8, waves = (wp + v - 1) / v;
+  // rows of one wave: four to a workgroup, without barriers (16384 rows of 320 9.2
+  // us, one to a workgroup 10.0; 64 rows 3.0 and 3.2)
+  if constexpr (PARTS != 1)  // (two groups of them have at most 32 pieces each)
+    if (waves == 1) return go<DT, RT, GATED, PARTS, 8, 1, AL, true>(a, 4, st);
   switch (v) {
     case 1: return go<DT, RT, GATED, PARTS, 8, 1, AL>(a, waves, st);
     case 2: return go<DT, RT, GATED, PARTS, 8, 2, AL>(a, waves, st);
     case 3: return go<DT, RT, GATED, PARTS, 8, 3, AL>(a, waves, st);
     default: return go<DT, RT, GATED, PARTS, 8, 4, AL>(a, waves, st);
   }
+}
+
+// Single channels, 1, 4 or 16 of a thread.
+template <int DT, int PARTS>
+hipError_t pick_channels(const NormArgs& a, hipStream_t st) {
+  const int v = a.cols <= 1024 ? 1 : a.cols <= 4096 ? 4 : 16;
+  const int waves = ((a.cols + v - 1) / v + kWave - 1) / kWave;
+  if (v == 1) return go<DT, DT, true, PARTS, 1, 1, false>(a, waves, st);
+  if (v == 4) return go<DT, DT, true, PARTS, 1, 4, false>(a, waves, st);
+  return go<DT, DT, true, PARTS, 1, 16, false>(a, waves, st);
 }
 
 template <int DT, int RT, bool GATED>
@@ -286,18 +334,16 @@ hipError_t pick(const NormArgs& a, hipStream_t st) {
     const void* const p = GATED ? a.z : a.x;
     const int64_t ld = GATED ? a.ld_z : a.ld_x;
     const bool al = a.cols % 8 == 0 && (uintptr_t)p % 16 == 0 && ld * esize % 16 == 0;
-    if constexpr (GATED)
+    if constexpr (GATED) {
+      if (a.groups > 1 && a.cols / 8 / a.groups >= kWave)
+        return al ? pick_pieces<DT, RT, true, 1, true>(a, st) : pick_pieces<DT, RT, true, 1, false>(a, st);
       if (a.groups > 1)
-        return al ? pick_pieces<DT, RT, true, true, true>(a, st) : pick_pieces<DT, RT, true, true, false>(a, st);
-    return al ? pick_pieces<DT, RT, GATED, false, true>(a, st) : pick_pieces<DT, RT, GATED, false, false>(a, st);
+        return al ? pick_pieces<DT, RT, true, 2, true>(a, st) : pick_pieces<DT, RT, true, 2, false>(a, st);
+    }
+    return al ? pick_pieces<DT, RT, GATED, 0, true>(a, st) : pick_pieces<DT, RT, GATED, 0, false>(a, st);
   }
-  if constexpr (GATED) {  // single channels, 1, 4 or 16 of a thread
-    const int v = a.cols <= 1024 ? 1 : a.cols <= 4096 ? 4 : 16;
-    const int waves = ((a.cols + v - 1) / v + kWave - 1) / kWave;
-    if (v == 1) return go<DT, RT, true, true, 1, 1, false>(a, waves, st);
-    if (v == 4) return go<DT, RT, true, true, 1, 4, false>(a, waves, st);
-    return go<DT, RT, true, true, 1, 16, false>(a, waves, st);
-  }
+  if constexpr (GATED)
+    return a.cols / a.groups >= kWave ? pick_channels<DT, 1>(a, st) : pick_channels<DT, 2>(a, st);
   return hipErrorInvalidValue;
 }
 

@@ -372,7 +372,7 @@ def test_decode_steps_follow_a_prompt(gpu_lib):
 # ---------------------------------------------------------------------------
 
 EPS = 1e-5
-NORM = [(1, 1), (3, 5), (2, 8), (5, 64), (2, 777), (7, 1000), (4, 1025), (8, 2560), (3, 4096), (2, 5000), (3, 8200),
+NORM = [(1, 1), (3, 5), (6, 512), (5, 509), (9, 100), (2, 8), (5, 64), (2, 777), (7, 1000), (4, 1025), (8, 2560), (3, 4096), (2, 5000), (3, 8200),
         (2, 16384), (2, 16383)]
 
 
@@ -426,7 +426,9 @@ def test_add_norm(gpu_lib, rows, cols, dtype, res, codes):
 @pytest.mark.parametrize("dtype,codes", [("fp16", True), ("bf16", True), ("fp32", False), ("bf16", False)])
 @pytest.mark.parametrize("rows,cols,groups,cut", [(1, 16, 1, 0), (3, 96, 3, 1), (2, 60, 5, 0), (5, 1024, 8, 0),
                                                   (37, 8192, 8, 0), (4, 5120, 1, 0), (3, 5120, 1, 3), (2, 1536, 128, 0),
-                                                  (2, 9000, 3, 0), (2, 16384, 2, 1), (3, 2001, 1, 0), (2, 2001, 23, 2)])
+                                                  (2, 9000, 3, 0), (2, 16384, 2, 1), (3, 2001, 1, 0), (2, 2001, 23, 2),
+                                                  (6, 96, 4, 0), (5, 480, 20, 1), (9, 512, 2, 0), (3, 960, 20, 0),
+                                                  (2, 4096, 64, 1), (2, 8000, 25, 0), (4, 1400, 100, 0), (3, 1416, 3, 0)])
 def test_gated_norm(gpu_lib, rows, cols, groups, cut, dtype, codes):
     import torch
     L = gpu_lib

@@ -391,8 +391,9 @@ int ssd_conv_decode_step(const ssd_shape* shape, int path, const ssd_conv* conv,
 
 /* The residual's addition and RMSNorm of rows, with the rows in 8 bits:
  *   r = x + residual,   y = r / sqrt(mean(r^2) + eps) * weight
- *   scale = max|y| / 127 (1 for a row of zeros),  q = RHAZ(y / scale)
- * in fp32. x [rows, cols] at row distance ld_x, dtype SSD_DTYPE_*; residual
+ *   scale = max|y| / 127 (1 where that rounds to zero),  q = RHAZ(y / scale)
+ * in fp32, each operation of the second line rounded as IEEE's (codes of rows whose
+ * scale is subnormal end at +-127). x [rows, cols] at row distance ld_x, dtype SSD_DTYPE_*; residual
  * and residual_out [rows, cols] dense in res_dtype (either may be NULL: no
  * residual, and r not kept; they may be the same buffer). weight [cols] fp32.
  * q int8 [rows, cols] and scale [rows] fp32 go together (both NULL: no codes).

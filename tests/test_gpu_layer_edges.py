@@ -1,0 +1,102 @@
+"""The steps around the SSD where a rounding, a size or a choice of kernel decides:
+the norms' codes by their documented rule, rows whose squares leave fp32's range,
+exponentials of large arguments, groups of odd sizes, products for every kernel, the
+INT8 path from prompt to tokens.
+
+Bounds are counted from the roundings made (u = 2^-24, one fp32 rounding).
+"""
+import numpy as np
+import pytest
+
+from oracle import layer_oracle as LO
+from tests.test_gpu_layer import EPS, U, _np, _t
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# codes
+# ---------------------------------------------------------------------------
+
+def _codes_by_rule(y):
+    """q = RHAZ(y / scale), scale = max|y| / 127 (1 where that is zero), each in fp32."""
+    with np.errstate(under="ignore"):
+        scale = (np.abs(y).max(-1) / np.float32(127)).astype(np.float32)
+        scale = np.where(scale > 0, scale, np.float32(1))
+        v = y / scale[:, None]
+    assert v.dtype == np.float32
+    return np.clip(LO.rhaz(v), -127, 127).astype(np.int8), scale
+
+
+def _norm_calls(torch, L, x, r, z, groups, w, eps):
+    """The rows (in x's type) and, from a second call, the codes and their steps."""
+    out, q = torch.empty_like(x), torch.empty(x.shape, dtype=torch.int8, device="cuda")
+    s = torch.empty(x.shape[0], device="cuda")
+    for o, c, p in ((out, None, None), (None, q, s)):
+        if z is None:
+            L.ssd_add_norm(x, r, None, w, eps, o, c, p)
+        else:
+            L.ssd_gated_norm(x, z, groups, w, eps, o, c, p)
+    torch.cuda.synchronize()
+    return out, q, s
+
+
+@pytest.mark.parametrize("rows,cols,groups", [(4000, 2560, 0), (3000, 5120, 1), (3000, 8192, 8), (2000, 4096, 64),
+                                              (1000, 777, 0), (900, 320, 2), (900, 1400, 100), (500, 509, 1)])
+def test_norm_codes_follow_the_documented_rule(gpu_lib, rows, cols, groups):
+    """Codes and steps are what the rows themselves give by q = RHAZ(y / scale), to
+    the bit, from ordinary rows to rows whose step is the smallest subnormal or
+    rounds to zero (groups 0: ssd_add_norm)."""
+    import torch
+    L = gpu_lib
+    print("codes", rows, cols, groups, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    x[::7] *= 1e-37
+    x[3::7] *= torch.logspace(-44.5, -36, len(range(3, rows, 7)), device="cuda")[:, None]
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    z = 2 * torch.randn(rows, cols, generator=g, device="cuda") if groups else None
+    y, q, s = _norm_calls(torch, L, x, None, z, groups, w, 1.0)  # eps 1: tiny rows stay tiny
+    ref, step = _codes_by_rule(y.cpu().numpy())
+    assert np.array_equal(s.cpu().numpy(), step)
+    bad = q.cpu().numpy() != ref
+    assert not bad.any(), f"{bad.sum()} of {bad.size} codes, in {bad.any(-1).sum()} rows"
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(4000, 2560), (3000, 777), (900, 320), (37, 8192)])
+def test_norm_codes_do_not_depend_on_the_type(gpu_lib, rows, cols, dtype):
+    """16-bit rows and the same values in fp32 give the same codes and steps: all that
+    happens before the codes is fp32."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda").to(_t(torch, dtype))
+    r = 3 * torch.randn(rows, cols, generator=g, device="cuda")
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    _, q, s = _norm_calls(torch, L, x, r, None, 0, w, EPS)
+    _, qf, sf = _norm_calls(torch, L, x.float(), r, None, 0, w, EPS)
+    assert torch.equal(s, sf) and torch.equal(q, qf)
+
+
+def test_norm_tiny_rows_have_steps_of_their_own(gpu_lib):
+    """Each row's step against its own largest value (a subnormal step is off by half
+    of 2^-149), its codes by that step, and `out` as the values they stand for."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(6, 320, generator=g, device="cuda")
+    x *= torch.tensor([1.0, 1e-20, 1e-36, 1e-37, 1e-40, 0.0], device="cuda")[:, None]
+    w = torch.ones(320, device="cuda")
+    q, s, out = torch.empty((6, 320), dtype=torch.int8, device="cuda"), torch.empty(6, device="cuda"), torch.empty_like(x)
+    L.ssd_add_norm(x, None, None, w, 1.0, out, q, s)
+    torch.cuda.synchronize()
+    y = LO.rms_rows(_np(x), 1, np.ones(320), 1.0)
+    step = np.abs(y).max(-1) / 127
+    step[5] = 1
+    # the row's 40 roundings and the step's; a subnormal y is off by 2^-150, its step by a 127th of that and 2^-150
+    assert (np.abs(_np(s) - step) <= 64 * U * step + 2.0 ** -149).all()
+    codes, gs = _np(q), _np(s)[:, None]
+    slack = (64 * U * np.abs(y) + 2.0 ** -149) / gs + 2 * U * np.abs(codes)
+    assert (np.abs(codes - np.clip(y / gs, -127, 127)) <= 0.5 + slack).all()
+    assert (np.abs(_np(out) - codes * gs) <= U * np.abs(codes * gs) + 2.0 ** -150).all()

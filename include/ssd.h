@@ -400,9 +400,10 @@ int ssd_conv_decode_step(const ssd_shape* shape, int path, const ssd_conv* conv,
  * out [rows, cols] in dtype (NULL: not wanted; q or out is required): the rows
  * y; where q is given too, the values scale * q that the codes stand for, so
  * that a consumer in floating point sees what one in 8 bits sees.
- * out may be x itself (at ld_x == cols). A row that holds NaN or infinity gets
- * a scale that is not finite. rows <= 2^31 - 1, cols <= 16384 (SSD_E_SHAPE);
- * rows == 0 is a valid empty problem. */
+ * out may be x itself (at ld_x == cols). A row r that holds NaN or infinity gets
+ * a scale that is not finite; finite rows are normalised whatever the size of
+ * their squares, and with eps = 0 a row of zeros stays zeros. rows <= 2^31 - 1,
+ * cols <= 16384 (SSD_E_SHAPE); rows == 0 is a valid empty problem. */
 int ssd_add_norm(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ld_x,
                  const void* residual, int res_dtype, void* residual_out, const float* weight,
                  float eps, void* out, int8_t* q, float* scale, void* stream);

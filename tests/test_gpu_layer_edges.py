@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import layer_oracle as LO
-from tests.test_gpu_layer import EPS, U, _np, _t
+from tests.test_gpu_layer import EPS, U, _check_rows, _np, _t
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,73 @@ def test_norm_tiny_rows_have_steps_of_their_own(gpu_lib):
     slack = (64 * U * np.abs(y) + 2.0 ** -149) / gs + 2 * U * np.abs(codes)
     assert (np.abs(codes - np.clip(y / gs, -127, 127)) <= 0.5 + slack).all()
     assert (np.abs(_np(out) - codes * gs) <= U * np.abs(codes * gs) + 2.0 ** -150).all()
+
+
+# ---------------------------------------------------------------------------
+# squares outside fp32's range
+# ---------------------------------------------------------------------------
+
+SPECIAL = [(320, 0), (512, 2), (2560, 0), (777, 0), (8192, 8), (4096, 64), (5000, 1), (60, 5), (2001, 23), (16384, 0)]
+
+
+@pytest.mark.parametrize("dtype,codes", [("fp32", False), ("fp32", True), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("cols,groups", SPECIAL)
+def test_norm_rows_whose_squares_overflow_or_vanish(gpu_lib, cols, groups, dtype, codes):
+    """Rows that are finite but whose squares or their sum are not, and (eps = 0) rows
+    whose squares fall below fp32, next to ordinary rows: all are normalised."""
+    import torch
+    L = gpu_lib
+    print("squares", cols, groups, dtype, codes, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(cols + groups)
+    td = _t(torch, dtype)
+    n = max(groups, 1)
+    big = torch.tensor([1e20, 1.0, 2e18, 1e36, 1e19], device="cuda")
+    low = torch.tensor([1e-25, 1.0, 1e-30, 1e-22, 3e-19], device="cuda")
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    for sizes, eps in ((big, EPS), (big, 0.0), (low, 0.0), (low, 1e-45)):
+        x = torch.randn(5, cols, generator=g, device="cuda")
+        z = None
+        if groups:  # a group each of its own size, shifted from row to row
+            size = torch.stack([sizes.roll(k).repeat(n // 5 + 1)[:n] for k in range(5)])
+            x = (x.view(5, n, -1) * size[..., None]).view(5, cols)
+            z = (1 + torch.rand(5, cols, generator=g, device="cuda")).to(td)
+        else:
+            x = x * sizes[:, None]
+            x[1, cols // 2] = 3e38 if sizes is big else 1e-30  # one value of its own size
+        x = x.to(td)
+        out = torch.empty_like(x)
+        q = torch.empty(x.shape, dtype=torch.int8, device="cuda") if codes else None
+        s = torch.empty(5, device="cuda") if codes else None
+        if groups:
+            L.ssd_gated_norm(x, z, groups, w, eps, out, q, s)
+        else:
+            L.ssd_add_norm(x, None, None, w, eps, out, q, s)
+        torch.cuda.synchronize()
+        v = _np(x) * (LO.silu(_np(z)) if groups else 1.0)
+        y = LO.rms_rows(v, n, _np(w), np.float64(np.float32(eps)))
+        # a value 2^80 below its row's largest may have been scaled into the subnormals
+        _check_rows(torch, L, y, np.abs(y) * 136 * U + 2.0 ** -126, out, q, s, dtype)
+
+
+@pytest.mark.parametrize("cols,groups", SPECIAL)
+def test_norm_rows_of_zeros_without_eps(gpu_lib, cols, groups):
+    """eps = 0: a row (or group) of zeros gives zeros, with a step of 1 where all of
+    the row is; a row that holds NaN or infinity still shows it in its step."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    n = max(groups, 1)
+    x = torch.randn(4, cols, generator=g, device="cuda")
+    x[0] = 0
+    x[1, :cols // n] = 0
+    x[2, -1], x[3, 0] = float("nan"), float("inf")
+    w, z = torch.ones(cols, device="cuda"), torch.full((4, cols), 3.0, device="cuda")
+    out, q, s = torch.empty_like(x), torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    if groups:
+        L.ssd_gated_norm(x, z, groups, w, 0.0, out, q, s)
+    else:
+        L.ssd_add_norm(x, None, None, w, 0.0, out, q, s)
+    torch.cuda.synchronize()
+    assert s[0] == 1 and not out[0].any() and not q[0].any()
+    assert not out[1, :cols // n].any() and torch.isfinite(s[1]) and (n == 1 or out[1, cols // n:].any())
+    assert not torch.isfinite(s[2:]).any()

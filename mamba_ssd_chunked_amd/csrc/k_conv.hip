@@ -116,7 +116,7 @@ __device__ __forceinline__ void conv_tile(const ConvFwdArgs& a, unsigned id) {
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) u = fmaf(w[e][j], win[j][e], u);
       u = fmaf(w[e][W - 1], x, u);
-      y[e] = silu(u);
+      y[e] = silu_rows<DT>(u);
 #pragma unroll
       for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
       win[W - 2][e] = x;

@@ -3,10 +3,11 @@
 //   u[c] = sum_j w[c,j] (the last W inputs of channel c) + b[c],  x | B | C = silu(u)
 //   dt = softplus(dt_raw + dt_bias),   then the step of k_decode.hip on x, B, C, dt
 //
-// with everything between the two kept in fp32. The state is read and written
-// once and is by far the most of the traffic (at P = 64, N = 128 in fp32 64 KB
-// a head against about 6 KB of the convolution's inputs, which the heads of a
-// group share in the caches), so a large batch is bound by HBM and a small one
+// with everything between the two kept in fp32 (SiLU and exp(dt A) in their exact
+// forms in any storage type: 0.1 us of a step of one sequence). The state is read
+// and written once and is by far the most of the traffic (at P = 64, N = 128 in
+// fp32 64 KB a head against about 6 KB of the convolution's inputs, which the heads
+// of a group share in the caches), so a large batch is bound by HBM and a small one
 // by the latency of one pass.
 //
 // A workgroup of four waves takes HB heads of a group: one where heads are few
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(kStepThreads) void k_conv_decode(StepArgs a) {
         }
       } else {
         const float dt = softplus(Store<DT>::to_f(dtr[i]) + dtb[i]);
-        const float decay = __expf(dt * Av[i]);
+        const float decay = expf(dt * Av[i]);  // to a unit for any argument: the state keeps it
         if constexpr (I8)
           L.row[k - 2 * NS] = RowI8{(float)q8(__fmul_rn(__fmul_rn(dt, v), k0[i])), k1[i], decay * sC * k2[i],
                                     sC * sB * dt * v, Dv[i] * v, quant_decay(dt, Av[i]), {0.f, 0.f}};

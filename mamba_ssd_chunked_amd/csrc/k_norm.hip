@@ -185,7 +185,7 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         r[i][e] = xr[i].get(e);
-        if constexpr (GATED) r[i][e] *= silu(zr[i].get(e));
+        if constexpr (GATED) r[i][e] *= silu_rows<DT>(zr[i].get(e));
         else if (add) r[i][e] += rr[i].get(e);
         ss[i] = fmaf(r[i][e], r[i][e], ss[i]);
       }

@@ -6,11 +6,34 @@
 
 namespace ssd {
 
-// u / (1 + exp(-u)): hardware exp2 and reciprocal, each within one unit in the
-// last place of fp32. exp overflows to infinity below u = -88, where the
-// reciprocal gives the limit 0.
+// u / (1 + exp(-u)) in fp32, to 9 roundings for any u down to -87 (below, where it is
+// less than 2^-119, it may be 0). With t = exp(-|u|) it is u / (1 + t) or u t / (1 + t):
+// nothing overflows. -|u| log2(e) is held to twice fp32's bits, as h + l, because an
+// exponent's absolute error is the power's relative one (rounded once, it would cost
+// |u| roundings); exp2 and the reciprocal are the hardware's, one unit each.
 __device__ __forceinline__ float silu(float u) {
+  const float a = fminf(fabsf(u), 104.f);  // exp(-104) is 0
+  const float h = a * -1.44269502f;
+  const float l = fmaf(a, -1.92596299e-8f, fmaf(a, -1.44269502f, -h));
+  const float t = __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.f);
+  return (u < 0.f ? u * t : u) * __builtin_amdgcn_rcpf(1.f + t);
+}
+
+// The same to about |u| + 8 roundings (2^-17 at u = -87), eight operations fewer: for
+// what is 16 bits wide next, or was before.
+__device__ __forceinline__ float silu_16(float u) {
   return u * __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+}
+
+// Rows in storage type DT. fp32 rows take the exact form, which the memory covers
+// (8192 x 5376 channels fp32 73 us with either; gated norm of 8192 x 5120 fp32 96).
+// 16-bit rows take the short one: a convolution's result is rounded to 16 bits at
+// once (a half step is 2^-12 of it or more), and a gate was read from 16 bits; there
+// the exact form would cost 5 to 19 % (16384 x 5120 gated, rows and codes 107 us
+// and 113, codes only 86 and 103).
+template <int DT>
+__device__ __forceinline__ float silu_rows(float u) {
+  return DT == DT_F32 ? silu(u) : silu_16(u);
 }
 
 // log(1 + exp(v)) as max(v, 0) + log1p(exp(-|v|)): step sizes of 1e-3 keep

@@ -9,7 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import layer_oracle as LO
-from tests.test_gpu_layer import EPS, U, _check_rows, _np, _t
+from tests.test_gpu_layer import EPS, U, _check_rows, _np, _t, _within
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,83 @@ def test_norm_rows_of_zeros_without_eps(gpu_lib, cols, groups):
     assert s[0] == 1 and not out[0].any() and not q[0].any()
     assert not out[1, :cols // n].any() and torch.isfinite(s[1]) and (n == 1 or out[1, cols // n:].any())
     assert not torch.isfinite(s[2:]).any()
+
+
+# ---------------------------------------------------------------------------
+# exponentials of large arguments
+# ---------------------------------------------------------------------------
+
+def test_conv_silu_of_large_arguments(gpu_lib):
+    """fp32 storage: SiLU of values from -87 to 88 (weights of 0 and 1, so that u is
+    the input itself) to 10 roundings, whatever the size of its argument: the
+    exponential 2 and its argument's product 2, the sum 1, the reciprocal 2, the
+    products 3."""
+    import torch
+    L = gpu_lib
+    B, Ln, H_, P, N = 2, 500, 4, 16, 16
+    cd = H_ * P + 2 * N
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = -87 + 175 * torch.rand(B, Ln, cd, generator=g, device="cuda")
+    x[0, :50] /= 50
+    w = torch.tensor([0.0, 1.0], device="cuda").repeat(cd, 1)
+    X, Bo, Co, dt = (torch.empty(s, device="cuda") for s in ((B, Ln, H_, P), (B, Ln, 1, N), (B, Ln, 1, N), (B, Ln, H_)))
+    L.ssd_conv_forward(L.make_shape(B, Ln, H_, P, N, 1, 64, "fp32"), L.ConvParams(w), x,
+                       torch.zeros(B, Ln, H_, device="cuda"), X, Bo, Co, dt)
+    torch.cuda.synchronize()
+    got = np.concatenate([_np(v).reshape(B, Ln, -1) for v in (X, Bo, Co)], -1)
+    ref = LO.silu(_np(x))
+    _within(got, ref, 10 * U * np.abs(ref), "fp32", "silu")
+
+
+@pytest.mark.parametrize("cols,groups", [(512, 1), (4096, 8), (1400, 100)])
+def test_gated_norm_silu_of_large_arguments(gpu_lib, cols, groups):
+    """fp32 rows gated by z from -80 to 8: the gate's 10 roundings, the product's 1, at
+    most 22 of the sum of squares on a path through its tree, halved by the root, and
+    8 behind it."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    z = -80 + 88 * torch.rand(6, cols, generator=g, device="cuda")
+    y = torch.randn(6, cols, generator=g, device="cuda")
+    w, out = torch.ones(cols, device="cuda"), torch.empty_like(y)
+    L.ssd_gated_norm(y, z, groups, w, 0.0, out)
+    torch.cuda.synchronize()
+    ref = LO.rms_rows(_np(y) * LO.silu(_np(z)), groups, np.ones(cols), 0.0)
+    _within(_np(out), ref, 30 * U * np.abs(ref) + 2.0 ** -126, "fp32", "gated")
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_decode_step_exponentials_of_large_arguments(gpu_lib, dtype):
+    """The step's decay and SiLU stay in fp32 in any storage type. With x = 0 the state
+    is decay times what it was (dt A exact: exponential 2 roundings, product 1); with
+    a state of zeros it is dt silu(u) silu(u_B) (10 roundings each and 2)."""
+    import torch
+    L = gpu_lib
+    B, H_, P, N = 3, 80, 16, 16
+    td, cd = _t(torch, dtype), H_ * P + 2 * N
+    g = torch.Generator(device="cuda").manual_seed(7)
+    w = torch.tensor([0.0, 1.0], device="cuda").repeat(cd, 1)
+    A, D = -torch.arange(H_, device="cuda") / 64.0, torch.zeros(H_, device="cuda")
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+
+    def step(x, raw, h):
+        Y = torch.empty((B, H_, P), dtype=td, device="cuda")
+        ring = torch.zeros((B, 2, cd), dtype=td, device="cuda")
+        L.ssd_conv_decode_step(L.make_shape(B, 1, H_, P, N, 1, 64, dtype), L.SSD_PATH_FLOAT, L.ConvParams(w), x, raw, A,
+                               D, None, ring, pos, h, Y)
+        torch.cuda.synchronize()
+
+    raw = torch.full((B, H_), 32.0, dtype=td, device="cuda")  # softplus(32) is 32 in fp32
+    h0 = torch.randn(B, H_, P, N, generator=g, device="cuda")
+    h = h0.clone()
+    step(torch.zeros((B, cd), dtype=td, device="cuda"), raw, h)
+    ref = _np(h0) * np.exp(32 * _np(A))[:, None, None]
+    _within(_np(h), ref, 3 * U * np.abs(ref), "fp32", "decay")
+
+    x = torch.empty(B, cd, device="cuda").uniform_(-60, 8, generator=g).to(td)
+    x[:, H_ * P:] = (1 + 3 * torch.rand(B, 2 * N, generator=g, device="cuda")).to(td)
+    h = torch.zeros((B, H_, P, N), device="cuda")
+    step(x, raw, h)
+    v = LO.silu(_np(x))
+    ref = 32 * v[:, :H_ * P].reshape(B, H_, P, 1) * v[:, None, None, H_ * P:H_ * P + N]
+    _within(_np(h), ref, 22 * U * np.abs(ref), "fp32", "dt x B")

@@ -188,6 +188,7 @@ class ScalePack:
 
     ORDER = ("s_B", "s_C", "inv_B", "inv_C", "s_X", "inv_X", "s_S", "M_req")
     OPTIONAL = ("s_Xq", "inv_Xq")
+    PER_GROUP = ("s_B", "s_C", "inv_B", "inv_C")
 
     def __init__(self, arrays: dict, device="cuda"):
         names = [k for k in self.ORDER if k in arrays] + [k for k in self.OPTIONAL if k in arrays]
@@ -201,6 +202,10 @@ class ScalePack:
             host[o:o + a.size] = a
         self.host = {k: a for k, a in zip(names, flat)}
         self.tensor = torch.from_numpy(host).to(device)
+        self.device_index = self.tensor.get_device()
+        # (G, H*P) that all arrays agree on, or None
+        sizes = [{a.size for k, a in self.host.items() if (k in self.PER_GROUP) == g} for g in (True, False)]
+        self.fits = (sizes[0].pop(), sizes[1].pop()) if all(len(v) == 1 for v in sizes) else None
         base = self.tensor.data_ptr()
         ptr = {k: base + 4 * o for k, o in zip(names, offs)}
         self.struct = SsdScales(*[ptr.get(k) for k in ("s_B", "s_C", "inv_B", "inv_C", "inv_X",
@@ -454,6 +459,20 @@ def _rows(t, name, n, dtype, dev):
     return t.data_ptr(), ld
 
 
+def _pack(scales, shape, dev):
+    """A scale pack for the INT8 step, whose arrays must fit the shape (None and bare
+    structs pass: the C call decides)."""
+    if isinstance(scales, ScalePack):
+        if scales.device_index != dev:
+            raise ValueError(f"the scales must be on the current GPU, they are on {scales.tensor.device}")
+        if scales.fits != (shape.ngroups, shape.nheads * shape.headdim):
+            for k, v in scales.host.items():
+                n = shape.ngroups if k in ScalePack.PER_GROUP else shape.nheads * shape.headdim
+                if v.size != n:
+                    raise ValueError(f"the scales' {k} holds {v.size} values, the shape has {n}")
+    return _scales(scales)
+
+
 _TORCH_DTYPE = {v: k for k, v in DTYPE_CODE.items()}
 
 
@@ -506,7 +525,7 @@ def ssd_conv_decode_step(shape, path, conv, xbc, dt_raw, A, D, scales, conv_stat
     hp = b * h * shape.headdim
     _check("ssd_conv_decode_step", LIB.ssd_conv_decode_step(
         ctypes.byref(shape), path, ctypes.byref(conv.struct), px, ldx, pt, ldt,
-        _dense(A, "A", h, torch.float32, dev), _dense(D, "D", h, torch.float32, dev), _scales(scales),
+        _dense(A, "A", h, torch.float32, dev), _dense(D, "D", h, torch.float32, dev), _pack(scales, shape, dev),
         _dense(conv_state, "conv_state", b * conv.width * cd, td, dev), _dense(pos, "pos", b, torch.int32, dev),
         _dense(state, "state", hp * shape.dstate, torch.int8 if path == SSD_PATH_INT8 else torch.float32, dev),
         _dense(Y, "Y", hp, td, dev), _stream_on(stream, dev)))

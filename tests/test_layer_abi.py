@@ -226,3 +226,19 @@ def test_binding_refuses_what_the_library_cannot_see():
     for bad in (torch.zeros(96, 4, dtype=torch.float16), torch.zeros(96, 4)):
         with pytest.raises(ValueError, match="float32 tensors on one GPU"):
             L.ConvParams(bad)
+
+
+def test_step_refuses_scales_of_another_shape():
+    """The kernel reads G and H*P steps: a pack of fewer would be read behind its end."""
+    def pack(g, hp):
+        return L.ScalePack({k: np.ones(g if k in ("s_B", "s_C", "inv_B", "inv_C") else hp, np.float32)
+                            for k in L.ScalePack.ORDER}, "cpu")
+
+    sh = shape(batch=0, seqlen=1, nheads=4, headdim=16, ngroups=2)
+    assert L._pack(None, sh, -1) is None
+    L._pack(pack(2, 64), sh, -1)
+    for g, hp, name in ((1, 64, "s_B"), (4, 64, "s_B"), (2, 48, "s_X"), (2, 16, "s_X")):
+        with pytest.raises(ValueError, match=name):
+            L._pack(pack(g, hp), sh, -1)
+    with pytest.raises(ValueError, match="current GPU"):
+        L._pack(pack(2, 64), sh, 0)

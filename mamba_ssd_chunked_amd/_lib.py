@@ -536,6 +536,8 @@ def ssd_add_norm(x, residual, residual_out, weight, eps, out=None, q=None, scale
     a step ``scale`` each. ``x`` may be a column slice; ``residual`` and
     ``residual_out`` share a type, x's or float32 (either may be None)."""
     cols, td, n = x.shape[-1], x.dtype, x.numel()
+    if cols == 0:
+        raise ValueError("the rows hold no channels")
     if n == 0:
         return
     dev = _current_device()
@@ -554,6 +556,8 @@ def ssd_gated_norm(y, z, groups, weight, eps, out=None, q=None, scale=None, stre
     ``ssd_add_norm``. ``z`` may be a column slice of In Proj's output. The row
     length is z's last dimension."""
     cols, td, n = z.shape[-1], y.dtype, z.numel()
+    if cols == 0:
+        raise ValueError("the rows hold no channels")
     if n == 0:
         return
     dev = _current_device()
@@ -582,7 +586,9 @@ def ssd_matmul_i8(a, a_scale, w, w_scale, bias, out, workspace=None, stream=None
     n, k = w.shape
     if a.shape[-1] != k:
         raise ValueError("a and w must agree in their last dimension")
-    m = a.numel() // k if k else 0
+    if k == 0:
+        raise ValueError("a and w hold no columns")
+    m = a.numel() // k
     if m == 0:
         return
     dev = _current_device()

@@ -242,3 +242,19 @@ def test_step_refuses_scales_of_another_shape():
             L._pack(pack(g, hp), sh, -1)
     with pytest.raises(ValueError, match="current GPU"):
         L._pack(pack(2, 64), sh, 0)
+
+
+def test_rows_of_no_columns_are_refused():
+    """Sums over nothing are refused, as in the C calls, instead of leaving the outputs
+    as they were; no rows are a valid empty problem."""
+    e = torch.empty
+    w, s, out = torch.ones(0), torch.zeros(4), torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="no columns"):
+        L.ssd_matmul_i8(e(4, 0, dtype=torch.int8), s, e(16, 0, dtype=torch.int8), torch.zeros(16), None, out)
+    with pytest.raises(ValueError, match="no channels"):
+        L.ssd_add_norm(e(4, 0), None, None, w, 1e-5, None, e(4, 0, dtype=torch.int8), s)
+    with pytest.raises(ValueError, match="no channels"):
+        L.ssd_gated_norm(e(4, 0), e(4, 0), 1, w, 1e-5, None, e(4, 0, dtype=torch.int8), s)
+    L.ssd_matmul_i8(e(0, 64, dtype=torch.int8), e(0), e(16, 64, dtype=torch.int8), torch.zeros(16), None, e(0, 16))
+    L.ssd_add_norm(e(0, 64), None, None, torch.ones(64), 1e-5, e(0, 64))
+    L.ssd_gated_norm(e(0, 64), e(0, 64), 1, torch.ones(64), 1e-5, e(0, 64))

@@ -9,8 +9,8 @@
 // 512 channels, a wave each); thread i holds the row's pieces i, i + blockDim, ...
 // of 8 consecutive channels. Rows that are not aligned, or not a multiple of 8
 // long, take the same pieces with unaligned accesses, the last one channel by
-// channel (G runs of channels that are no multiple of 8 long: single channels
-// instead of pieces). Two reductions over the row (the sum of squares, the largest
+// channel (G runs of channels that are no multiple of 8 long: a kernel of single
+// channels). Two reductions over the row (the sum of squares, the largest
 // magnitude) cross the waves in LDS; short runs of channels are summed side by
 // side (4000 rows of 4096 in 64 runs: 35 -> 22 us). Rows leave past the caches (2
 // to 10 % faster; loads that do are slower).
@@ -29,11 +29,12 @@
 namespace ssd {
 namespace {
 
-constexpr int kMaxWaves = 16;
+constexpr int kMaxWaves = 8;
+constexpr int VEC = 8;  // channels of a piece
 
 // A piece of a row as loaded: VEC channels, of which the last piece of a row that
 // is no multiple of 8 long has fewer (n; the rest are zeros, and are not written).
-template <int DT, int VEC>
+template <int DT>
 struct RawPiece {
   static constexpr int V = RawVec<DT>::V;
   RawVec<DT> v[VEC / V];
@@ -52,14 +53,6 @@ struct RawPiece {
   }
   __device__ __forceinline__ float get(int e) const { return v[e / V].get(e % V); }
 };
-template <int DT>
-struct RawPiece<DT, 1> {
-  typename Store<DT>::T v;
-  template <bool AL>
-  __device__ __forceinline__ void load(const void* p, int64_t i, int) { v = ((const typename Store<DT>::T*)p)[i]; }
-  __device__ __forceinline__ float get(int) const { return Store<DT>::to_f(v); }
-};
-
 // Four whole numbers of [-127, 127] as bytes: the conversions write their low
 // bytes straight into place.
 __device__ __forceinline__ uint32_t pack4_codes(const float* v) {
@@ -70,49 +63,43 @@ __device__ __forceinline__ uint32_t pack4_codes(const float* v) {
   return d;
 }
 
-template <int DT, int VEC, bool AL>
+template <int DT, bool AL>
 __device__ __forceinline__ void st_piece(void* p, int64_t i, int n, const float* v) {
-  if constexpr (VEC == 1) {
-    ((typename Store<DT>::T*)p)[i] = to_store<DT>(v[0]);
-  } else {
-    constexpr int V = RawVec<DT>::V;
-    if (AL || n >= VEC) {
+  constexpr int V = RawVec<DT>::V;
+  if (AL || n >= VEC) {
 #pragma unroll
-      for (int k = 0; k < VEC / V; ++k) {
-        RawVec<DT> r;
-        r.set(v + k * V);
-        r.template store_nt<AL>(p, i + k * V);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e < n) ((typename Store<DT>::T*)p)[i + e] = to_store<DT>(v[e]);
+    for (int k = 0; k < VEC / V; ++k) {
+      RawVec<DT> r;
+      r.set(v + k * V);
+      r.template store_nt<AL>(p, i + k * V);
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e < n) ((typename Store<DT>::T*)p)[i + e] = to_store<DT>(v[e]);
   }
 }
 
-// The codes of VEC values v in steps: v + copysign(0.5 - 2^-25, v), truncated,
-// is v rounded half away from zero; |v| is at most 127 (1 + 2^-22), so there is
+// v + copysign(0.5 - 2^-25, v), truncated, is v rounded half away from zero.
+__device__ __forceinline__ float code(float v) { return truncf(v + __builtin_copysignf(0.49999997f, v)); }
+
+// The codes of VEC values v in steps; |v| is at most 127 (1 + 2^-22), so there is
 // nothing to clamp. On return v holds the codes.
-template <int VEC, bool AL>
+template <bool AL>
 __device__ __forceinline__ void st_codes(int8_t* p, int n, float* v) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) v[e] = truncf(v[e] + __builtin_copysignf(0.49999997f, v[e]));
-  if constexpr (VEC == 1) {
-    p[0] = (int8_t)(int)v[0];
+  for (int e = 0; e < VEC; ++e) v[e] = code(v[e]);
+  typedef uint32_t v2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t v2_any __attribute__((ext_vector_type(2), aligned(1)));
+  const uint32_t lo = pack4_codes(v), hi = pack4_codes(v + 4);
+  if constexpr (AL) {
+    __builtin_nontemporal_store((v2){lo, hi}, (v2*)p);
+  } else if (n >= VEC) {
+    __builtin_nontemporal_store((v2_any){lo, hi}, (v2_any*)p);
   } else {
-    typedef uint32_t v2 __attribute__((ext_vector_type(2)));
-    typedef uint32_t v2_any __attribute__((ext_vector_type(2), aligned(1)));
-    const uint32_t lo = pack4_codes(v), hi = pack4_codes(v + 4);
-    if constexpr (AL) {
-      __builtin_nontemporal_store((v2){lo, hi}, (v2*)p);
-    } else if (n >= VEC) {
-      __builtin_nontemporal_store((v2_any){lo, hi}, (v2_any*)p);
-    } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e < n) p[e] = (int8_t)(int)v[e];
-    }
+    for (int e = 0; e < VEC; ++e)
+      if (e < n) p[e] = (int8_t)(int)v[e];
   }
 }
 
@@ -136,17 +123,72 @@ __device__ __forceinline__ float scale_for(float m) { return m > 1.f ? 0x1p-80f 
 // 1 / sqrt(m), 0 for m = 0 (a row of zeros without eps is zeros, not NaN).
 __device__ __forceinline__ float inv_root(float m) { return m > 0.f ? rsqrtf(m) : 0.f; }
 
+// The step of a row whose largest magnitude has these bits: most / 127, 1 where that
+// rounds to zero. The codes are those of the quotient y / scale as fp32 rounds it: a
+// product with 1 / scale, and its remainder (exact in one multiply-add) brought in,
+// which costs no time (16384 rows of 5120 fp16, gated, codes only: 83 us; 87 with
+// y * (127 / most), whose codes next to a border were the neighbours'). Rows of steps
+// below 2^-64 are scaled up with them (up), exactly, so that the remainder is no
+// subnormal; a subnormal step may be well below most / 127: codes end at 127.
+struct Step {
+  float scale, unit, inv;
+  bool tiny;
+  __device__ __forceinline__ explicit Step(uint32_t most) {
+    scale = __uint_as_float(most) / 127.f;
+    if (scale == 0.f) scale = 1.f;
+    tiny = scale < 0x1p-64f;
+    unit = tiny ? scale * 0x1p64f : scale;
+    inv = 1.f / unit;
+  }
+  __device__ __forceinline__ float up(float y) const {
+    return fminf(fmaxf(y * 0x1p64f, -127.f * unit), 127.f * unit);
+  }
+  __device__ __forceinline__ float quotient(float y) const {
+    const float v = y * inv;
+    return fmaf(fmaf(-v, unit, y), inv, v);
+  }
+};
+
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The mean of squares of each group goes to done(g, mean) in one lane. A group has n
+// channels, and its squares are at(g gp) .. at(g gp + gp - 1).
+//
+// A wave takes a group at a time ...
+template <class At, class Done>
+__device__ __forceinline__ void group_means(int groups, int gp, int n, int wave, int nw, At at, Done done) {
+  for (int g = wave; g < groups; g += nw) {
+    float t = 0.f;
+    for (int k = lane_id(); k < gp; k += kWave) t += at(g * gp + k);
+    t = wave_sum(t);
+    if (lane_id() == 0) done(g, t / (float)n);
+  }
+}
+// ... or several side by side, with 2^sh lanes each.
+template <class At, class Done>
+__device__ __forceinline__ void short_group_means(int groups, int gp, int n, int sh, int wave, int nw, At at, Done done) {
+  const int lanes = 1 << sh, sub = lane_id() & (lanes - 1);
+  for (int g0 = wave * (kWave >> sh); g0 < groups; g0 += nw * (kWave >> sh)) {
+    const int g = g0 + (lane_id() >> sh);
+    float t = 0.f;
+    if (g < groups)
+      for (int k = sub; k < gp; k += lanes) t += at(g * gp + k);
+    for (int m = lanes / 2; m >= 1; m >>= 1) t += __shfl_xor(t, m);
+    if (g < groups && sub == 0) done(g, t / (float)n);
+  }
+}
+// The largest power of two up to v, as its exponent.
+__device__ __forceinline__ int log2_down(int v) { return 31 - __builtin_clz(v); }
+
 // One row for each workgroup (of the first 2^20, then on), or (WAVE: rows of one
 // piece a lane) for each wave. The mean is over the row (PARTS 0), or over groups
 // of at least 64 pieces (1) or fewer (2).
-template <int DT, int RT, bool GATED, int PARTS, int VEC, int V, bool AL, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(NormArgs a) {
+template <int DT, int RT, bool GATED, int PARTS, int V, bool AL, bool WAVE>
+__global__ __launch_bounds__(WAVE ? 256 : 512) void k_norm(NormArgs a) {
   extern __shared__ float s_parts[];  // PARTS: the sum of squares of each piece, then 1/rms of each group
   __shared__ float s_sum[kMaxWaves];
   __shared__ uint32_t s_max[kMaxWaves];
@@ -166,9 +208,9 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
 
     // everything is requested before anything is used; threads behind the last
     // piece load it too (no load is conditional on the lane)
-    RawPiece<DT, VEC> xr[V], zr[V];
-    RawPiece<RT, VEC> rr[V];
-    RawPiece<DT_F32, VEC> wr[V];
+    RawPiece<DT> xr[V], zr[V];
+    RawPiece<RT> rr[V];
+    RawPiece<DT_F32> wr[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int p = min(tid + i * nt, np - 1), c = p * VEC, n = a.cols - c;
@@ -191,7 +233,7 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
       }
       if (p >= np) ss[i] = 0.f;
       if constexpr (!GATED)
-        if (a.residual_out && p < np) st_piece<RT, VEC, AL>(a.residual_out, base + p * VEC, a.cols - p * VEC, r[i]);
+        if (a.residual_out && p < np) st_piece<RT, AL>(a.residual_out, base + p * VEC, a.cols - p * VEC, r[i]);
     }
 
     // 1 / rms, of the row or of each group. Where the sum of squares left fp32's range
@@ -236,7 +278,6 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
       float* const s_rs = s_part + np;
       float* const s_out = s_sum + (WAVE ? wave_id() : 0);  // whether a group's mean is out of range
       if (tid == 0) *s_out = 0.f;
-      // the sum of each group's pieces goes to done(g, sum) in one lane
       auto groups = [&](auto done) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -244,24 +285,9 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
           if (p < np) s_part[p] = ss[i];
         }
         sync();
-        if constexpr (PARTS == 1) {
-          for (int g = wave; g < a.groups; g += nw) {
-            float t = 0.f;
-            for (int k = lane_id(); k < gp; k += kWave) t += s_part[g * gp + k];
-            t = wave_sum(t);
-            if (lane_id() == 0) done(g, t / (float)(gp * VEC));
-          }
-        } else {  // as many lanes a group as the largest power of two up to its pieces
-          const int sh = 31 - __builtin_clz(gp), lanes = 1 << sh, sub = lane_id() & (lanes - 1);
-          for (int g0 = wave * (kWave >> sh); g0 < a.groups; g0 += nw * (kWave >> sh)) {
-            const int g = g0 + (lane_id() >> sh);
-            float t = 0.f;
-            if (g < a.groups)
-              for (int k = sub; k < gp; k += lanes) t += s_part[g * gp + k];
-            for (int m = lanes / 2; m >= 1; m >>= 1) t += __shfl_xor(t, m);
-            if (g < a.groups && sub == 0) done(g, t / (float)(gp * VEC));
-          }
-        }
+        auto at = [&](int k) { return s_part[k]; };
+        if constexpr (PARTS == 1) group_means(a.groups, gp, gp * VEC, wave, nw, at, done);
+        else short_group_means(a.groups, gp, gp * VEC, log2_down(gp), wave, nw, at, done);
         sync();
       };
       groups([&](int g, float mean) {
@@ -307,44 +333,29 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
         most = 0;
         for (int i = 0; i < nw; ++i) most = max(most, s_max[i]);
       }
-      // The step, most / 127, is 1 where that rounds to zero. The codes are those of
-      // the quotient y / scale as fp32 rounds it: a product with 1 / scale, and its
-      // remainder (exact in one multiply-add) brought in, which costs no time (16384
-      // rows of 5120 fp16, gated, codes only: 83 us; 87 with y * (127 / most), whose
-      // codes next to a border were the neighbours'). Steps below 2^-64 are
-      // scaled up with their rows, exactly, so that the remainder is no subnormal; a
-      // subnormal step may be well below most / 127, and its codes end at 127.
-      const float top = __uint_as_float(most);
-      float scale = top / 127.f;
-      if (scale == 0.f) scale = 1.f;
-      const bool tiny = scale < 0x1p-64f;
-      const float unit = tiny ? scale * 0x1p64f : scale, inv = 1.f / unit;
-      if (tiny) {
-        const float end = 127.f * unit;
+      const Step st(most);
+      if (st.tiny) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) r[i][e] = fminf(fmaxf(r[i][e] * 0x1p64f, -end), end);
+          for (int e = 0; e < VEC; ++e) r[i][e] = st.up(r[i][e]);
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int p = tid + i * nt;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float v = r[i][e] * inv;
-          r[i][e] = fmaf(fmaf(-v, unit, r[i][e]), inv, v);
-        }
-        if (p < np) st_codes<VEC, AL>(a.q + base + p * VEC, a.cols - p * VEC, r[i]);
+        for (int e = 0; e < VEC; ++e) r[i][e] = st.quotient(r[i][e]);
+        if (p < np) st_codes<AL>(a.q + base + p * VEC, a.cols - p * VEC, r[i]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) r[i][e] *= scale;
+        for (int e = 0; e < VEC; ++e) r[i][e] *= st.scale;
       }
-      if (tid == 0) a.scale[row] = scale;
+      if (tid == 0) a.scale[row] = st.scale;
     }
     if (a.out) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int p = tid + i * nt;
-        if (p < np) st_piece<DT, VEC, AL>(a.out, base + p * VEC, a.cols - p * VEC, r[i]);
+        if (p < np) st_piece<DT, AL>(a.out, base + p * VEC, a.cols - p * VEC, r[i]);
       }
     }
     // the next row's sums overwrite this one's: with codes, the barrier of the
@@ -353,11 +364,88 @@ __global__ __launch_bounds__(WAVE ? 256 : VEC == 8 ? 512 : 1024) void k_norm(Nor
   }
 }
 
-template <int DT, int RT, bool GATED, int PARTS, int VEC, int V, bool AL, bool WAVE = false>
+// Gated rows in groups whose size is no multiple of 8, channel by channel. The row
+// lies in LDS (up to 64 KB, and the groups' 1 / rms as much again) instead of
+// registers, of which 16 channels in each of 1024 threads spilled 55. Up to 1024
+// channels a wave where rows are many, 512 where they are few; loops unrolled twice
+// (once: 458 -> 555 us in the first of these, four times: 64 -> 65 in the second).
+// us, and with rows in registers: 4000 x 16380 in groups of 4 bf16 458, 620; 16384 x
+// 1400 of 14 fp16 64, 87; 5000 x 4097 of 241 fp16 62, 217; 8 x 5100 of 204 7.8, 15;
+// 16384 x 2001 of 87 bf16 92, 103; 16384 x 60 of 12 11.4, 10.1.
+template <int DT>
+__global__ __launch_bounds__(512) void k_norm_channels(NormArgs a) {
+  typedef typename Store<DT>::T T;
+  extern __shared__ float s_r[];
+  __shared__ uint32_t s_max[kMaxWaves];
+  __shared__ int s_out;  // whether a group's mean is out of range
+  float* const s_rs = s_r + a.cols;
+  const int nt = blockDim.x, nw = nt / kWave, tid = threadIdx.x, gp = a.cols / a.groups;
+  // 16 lanes a group at most where that keeps all waves busy: fewer steps of a sum
+  const int sh = min(log2_down(gp), a.groups > 2 * nw ? 4 : 6);
+  const float per = 1.f / (float)gp;
+  // channel c's group: (c + 1/2) / gp lies at least 1 / 2 gp from a whole number, and
+  // two roundings of up to 16384 / gp are far less
+  auto group = [&](int c) { return (int)(((float)c + 0.5f) * per); };
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const int64_t base = row * (int64_t)a.cols;
+    const T* const y = (const T*)a.x + base;
+    const T* const z = (const T*)a.z + row * a.ld_z;
+    if (tid == 0) s_out = 0;
+#pragma unroll 2
+    for (int c = tid; c < a.cols; c += nt) s_r[c] = Store<DT>::to_f(y[c]) * silu_rows<DT>(Store<DT>::to_f(z[c]));
+    auto groups = [&](auto done) {
+      __syncthreads();
+      short_group_means(a.groups, gp, gp, sh, wave_id(), nw, [&](int k) { return s_r[k] * s_r[k]; }, done);
+      __syncthreads();
+    };
+    groups([&](int g, float mean) {
+      const float m = mean + a.eps;
+      const bool in = in_range(m);
+      s_rs[g] = in ? inv_root(m) : -scale_for(m);
+      if (!in) s_out = 1;
+    });
+    if (s_out) {
+      for (int c = tid; c < a.cols; c += nt) {
+        const float by = s_rs[group(c)];
+        if (by < 0.f) s_r[c] *= -by;
+      }
+      groups([&](int g, float mean) {
+        const float by = s_rs[g];
+        if (by < 0.f) s_rs[g] = inv_root(mean + a.eps * by * by);
+      });
+    }
+    uint32_t most = 0;
+#pragma unroll 2
+    for (int c = tid; c < a.cols; c += nt) {
+      const float v = s_r[c] * s_rs[group(c)] * a.weight[c];
+      most = max(most, __float_as_uint(v) & 0x7fffffffu);
+      if (a.q) s_r[c] = v;
+      else ((T*)a.out)[base + c] = to_store<DT>(v);
+    }
+    if (a.q) {
+      most = wave_max(most);
+      if (lane_id() == 0) s_max[wave_id()] = most;
+      __syncthreads();
+      most = 0;
+      for (int i = 0; i < nw; ++i) most = max(most, s_max[i]);
+      const Step st(most);
+#pragma unroll 2
+      for (int c = tid; c < a.cols; c += nt) {
+        const float v = code(st.quotient(st.tiny ? st.up(s_r[c]) : s_r[c]));
+        a.q[base + c] = (int8_t)(int)v;
+        if (a.out) ((T*)a.out)[base + c] = to_store<DT>(v * st.scale);
+      }
+      if (tid == 0) a.scale[row] = st.scale;
+    }
+    __syncthreads();  // the next row overwrites what this one's threads read
+  }
+}
+
+template <int DT, int RT, bool GATED, int PARTS, int V, bool AL, bool WAVE = false>
 hipError_t go(const NormArgs& a, int waves, hipStream_t st) {
   const size_t lds = PARTS ? (WAVE ? waves : 1) * (size_t)(a.cols / VEC + a.groups) * sizeof(float) : 0;
   const int64_t wgs = WAVE ? (a.rows + waves - 1) / waves : a.rows;
-  hipLaunchKernelGGL((k_norm<DT, RT, GATED, PARTS, VEC, V, AL, WAVE>), dim3((unsigned)min(wgs, (int64_t)1 << 20)),
+  hipLaunchKernelGGL((k_norm<DT, RT, GATED, PARTS, V, AL, WAVE>), dim3((unsigned)min(wgs, (int64_t)1 << 20)),
                      dim3(waves * kWave), lds, st, a);
   return hipGetLastError();
 }
@@ -373,23 +461,21 @@ hipError_t pick_pieces(const NormArgs& a, hipStream_t st) {
   // rows of one wave: four to a workgroup, without barriers (16384 rows of 320 9.2
   // us, one to a workgroup 10.0; 64 rows 3.0 and 3.2)
   if constexpr (PARTS != 1)  // (two groups of them have at most 32 pieces each)
-    if (waves == 1) return go<DT, RT, GATED, PARTS, 8, 1, AL, true>(a, 4, st);
+    if (waves == 1) return go<DT, RT, GATED, PARTS, 1, AL, true>(a, 4, st);
   switch (v) {
-    case 1: return go<DT, RT, GATED, PARTS, 8, 1, AL>(a, waves, st);
-    case 2: return go<DT, RT, GATED, PARTS, 8, 2, AL>(a, waves, st);
-    case 3: return go<DT, RT, GATED, PARTS, 8, 3, AL>(a, waves, st);
-    default: return go<DT, RT, GATED, PARTS, 8, 4, AL>(a, waves, st);
+    case 1: return go<DT, RT, GATED, PARTS, 1, AL>(a, waves, st);
+    case 2: return go<DT, RT, GATED, PARTS, 2, AL>(a, waves, st);
+    case 3: return go<DT, RT, GATED, PARTS, 3, AL>(a, waves, st);
+    default: return go<DT, RT, GATED, PARTS, 4, AL>(a, waves, st);
   }
 }
 
-// Single channels, 1, 4 or 16 of a thread.
-template <int DT, int PARTS>
+template <int DT>
 hipError_t pick_channels(const NormArgs& a, hipStream_t st) {
-  const int v = a.cols <= 1024 ? 1 : a.cols <= 4096 ? 4 : 16;
-  const int waves = ((a.cols + v - 1) / v + kWave - 1) / kWave;
-  if (v == 1) return go<DT, DT, true, PARTS, 1, 1, false>(a, waves, st);
-  if (v == 4) return go<DT, DT, true, PARTS, 1, 4, false>(a, waves, st);
-  return go<DT, DT, true, PARTS, 1, 16, false>(a, waves, st);
+  const int per = a.rows > 1024 ? 1024 : 512, waves = min((a.cols + per - 1) / per, 8);
+  const size_t lds = (size_t)(a.cols + a.groups) * sizeof(float);
+  hipLaunchKernelGGL((k_norm_channels<DT>), dim3((unsigned)min(a.rows, (int64_t)1 << 20)), dim3(waves * kWave), lds, st, a);
+  return hipGetLastError();
 }
 
 template <int DT, int RT, bool GATED>
@@ -408,7 +494,7 @@ hipError_t pick(const NormArgs& a, hipStream_t st) {
     return al ? pick_pieces<DT, RT, GATED, 0, true>(a, st) : pick_pieces<DT, RT, GATED, 0, false>(a, st);
   }
   if constexpr (GATED)
-    return a.cols / a.groups >= kWave ? pick_channels<DT, 1>(a, st) : pick_channels<DT, 2>(a, st);
+    return pick_channels<DT>(a, st);
   return hipErrorInvalidValue;
 }
 

@@ -173,6 +173,31 @@ def test_norm_rows_of_zeros_without_eps(gpu_lib, cols, groups):
 
 
 # ---------------------------------------------------------------------------
+# groups of odd sizes in long rows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,codes", [("fp32", False), ("fp32", True), ("fp16", True), ("bf16", True), ("bf16", False)])
+@pytest.mark.parametrize("rows,cols,groups", [(3, 5100, 25), (2, 8204, 7), (2, 16380, 4095), (2, 16384, 16384),
+                                              (5, 4097, 17), (3, 16383, 3), (3, 12300, 615)])
+def test_gated_norm_long_rows_of_odd_groups(gpu_lib, rows, cols, groups, dtype, codes):
+    import torch
+    L = gpu_lib
+    print("odd groups", rows, cols, groups, dtype, codes, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    td = _t(torch, dtype)
+    y = torch.randn(rows, cols, generator=g, device="cuda").to(td)
+    z = (2 * torch.randn(rows, cols + 3, generator=g, device="cuda")).to(td)[:, 3:]
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    out = torch.empty((rows, cols), dtype=td, device="cuda")
+    q = torch.empty((rows, cols), dtype=torch.int8, device="cuda") if codes else None
+    s = torch.empty(rows, device="cuda") if codes else None
+    L.ssd_gated_norm(y, z, groups, w, EPS, out, q, s)
+    torch.cuda.synchronize()
+    n = LO.rms_rows(_np(y) * LO.silu(_np(z)), groups, _np(w), EPS)
+    _check_rows(torch, L, n, np.abs(n) * (128 + 2 * np.abs(_np(z))) * U, out, q, s, dtype)
+
+
+# ---------------------------------------------------------------------------
 # exponentials of large arguments
 # ---------------------------------------------------------------------------
 

@@ -275,3 +275,64 @@ def test_decode_step_exponentials_of_large_arguments(gpu_lib, dtype):
     v = LO.silu(_np(x))
     ref = 32 * v[:, :H_ * P].reshape(B, H_, P, 1) * v[:, None, None, H_ * P:H_ * P + N]
     _within(_np(h), ref, 22 * U * np.abs(ref), "fp32", "dt x B")
+
+
+# ---------------------------------------------------------------------------
+# products for every kernel
+# ---------------------------------------------------------------------------
+
+# with test_gpu_layer.MM: every kernel of the dispatch, with and without a tail of K,
+# with sums shorter and longer than its buffers, and with tiles that end with the
+# matrix (test_layer_native.py asserts it)
+MM_KERNELS = [(1, 16, 2048), (1, 3870, 512), (3, 4281, 1536), (2, 4427, 1072), (1, 5236, 3088), (1, 5357, 3584),
+              (16, 9000, 3600), (2245, 33, 512), (2140, 33, 16), (3698, 17, 544), (18, 3004, 1552), (103, 6937, 528),
+              (99, 7287, 1024), (41, 11479, 1616), (333, 2560, 5120), (333, 2560, 5136), (333, 8512, 2064),
+              (340, 8500, 1040), (384, 3864, 864), (165, 7380, 1024), (4099, 2571, 5136), (3000, 10576, 1040),
+              (687, 11060, 1536), (1790, 4864, 5024)]
+
+
+@pytest.mark.parametrize("M,N,K", MM_KERNELS)
+def test_matmul_every_kernel(gpu_lib, M, N, K):
+    """Sums of both signs up to the largest, with and without bias, in the three types:
+    exact sums, so 3 roundings and the type's."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(M + 3 * N + 7 * K)
+    a = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    a[-1], w[-1] = -128, -128
+    sa = (0.5 + torch.rand(M, generator=g, device="cuda")) / 128
+    sw = (0.5 + torch.rand(N, generator=g, device="cuda")) / 128 / K ** 0.5
+    bias = torch.randn(N, generator=g, device="cuda")
+    acc = a.double() @ w.double().t().contiguous()
+    part = acc * sa.double()[:, None] * sw.double()
+    for dtype in ("fp32", "fp16", "bf16"):
+        for b in (None, bias):
+            print("matmul", M, N, K, dtype, b is not None, flush=True)
+            buf = torch.full((M * N + 128,), 7.0, dtype=_t(torch, dtype), device="cuda")
+            out = buf[64:64 + M * N].view(M, N)
+            L.ssd_matmul_i8(a, sa, w, sw, b, out)
+            torch.cuda.synchronize()
+            assert (buf[:64] == 7).all() and (buf[64 + M * N:] == 7).all()
+            ref = part + (b.double() if b is not None else 0)
+            fi = torch.finfo(out.dtype)
+            bound = 3 * U * part.abs() + U * ref.abs() + fi.eps / 2 * (1 + U * 8) * out.double().abs().clamp(min=fi.tiny)
+            err = (out.double() - ref).abs()
+            assert (err <= bound).all(), (dtype, b is not None, float((err / bound).max()))
+
+
+def test_matmul_sums_are_exact_on_every_call(gpu_lib):
+    """With steps of powers of two and sums below 2^24 the fp32 outputs are the whole
+    numbers themselves: split sums lose nothing, on any call."""
+    import torch
+    L = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for M, N, K in ((8, 2560, 1024), (100, 80, 1040), (333, 2560, 1024), (333, 8512, 1040), (4099, 2571, 768)):
+        a = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+        w = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+        sa, sw = torch.full((M,), 0.25, device="cuda"), torch.full((N,), 4.0, device="cuda")
+        ref = (a.double() @ w.double().t().contiguous()).float()  # |sums| <= 127^2 K < 2^24
+        for _ in range(4):
+            out = torch.full((M, N), float("nan"), device="cuda")
+            L.ssd_matmul_i8(a, sa, w, sw, None, out)
+            assert torch.equal(out, ref), (M, N, K)

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import layer_oracle as LO
+from tests import _helpers as H
 from tests.test_gpu_layer import EPS, U, _check_rows, _np, _t, _within
 
 pytestmark = pytest.mark.gpu
@@ -336,3 +337,75 @@ def test_matmul_sums_are_exact_on_every_call(gpu_lib):
             out = torch.full((M, N), float("nan"), device="cuda")
             L.ssd_matmul_i8(a, sa, w, sw, None, out)
             assert torch.equal(out, ref), (M, N, K)
+
+
+# ---------------------------------------------------------------------------
+# the INT8 path from prompt to tokens
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_int8_prompts_then_tokens(gpu_lib, dtype):
+    """Convolution, the INT8 forward of ragged prompts on scales calibrated from the
+    convolution's own outputs, then fused INT8 steps on the 8-bit state: states are
+    the oracle's to the bit, outputs within the INT8 path's error. The oracle takes
+    what the GPU hands from call to call (X, B, C, dt, each held to its definition by
+    its own tests; a step's are those of a convolution that rounds nothing)."""
+    import torch
+    from oracle import ssd_oracle as SO
+    from tests.test_gpu_layer import _conv_case
+    L = gpu_lib
+    B, n, more, H_, P, N, G, W = 3, 150, 6, 8, 32, 64, 2, 4
+    td = _t(torch, dtype)
+    c = _conv_case(torch, 31, B, n + more, H_, P, N, G, W, dtype)
+    conv = L.ConvParams(c["w"], c["b"], c["dtb"])
+    g = torch.Generator(device="cuda").manual_seed(32)
+    A, D = -torch.exp(2 * torch.rand(H_, generator=g, device="cuda")), torch.randn(H_, generator=g, device="cuda")
+    ends = [150, 1, 97]
+    lengths = torch.tensor(ends, dtype=torch.int32, device="cuda")
+
+    def convolve(x, raw, ring, pos, lens, t):
+        b, k = x.shape[:2]
+        o = [torch.empty(s, dtype=t, device="cuda") for s in ((b, k, H_, P), (b, k, G, N), (b, k, G, N), (b, k, H_))]
+        sh = L.make_shape(b, k, H_, P, N, G, 64, "fp32" if t is torch.float32 else dtype)
+        L.ssd_conv_forward(sh, conv, x, raw, *o, ring, pos, lens)
+        return sh, o
+
+    ring = torch.zeros((B, W, c["cd"]), dtype=td, device="cuda")
+    pos = torch.zeros(B, dtype=torch.int32, device="cuda")
+    sh, (X, Bo, Co, dt) = convolve(c["xbc"][:, :n].contiguous(), c["raw"][:, :n].contiguous(), ring, pos, lengths, td)
+    sc = L.calibrate(lambda s: sh, [{"x": X, "dt": dt, "B": Bo, "C": Co}], A)
+    h = torch.empty((B, H_, P, N), dtype=torch.int8, device="cuda")
+    Y = torch.empty((B, n, H_, P), dtype=td, device="cuda")
+    L.ssd_forward(sh, L.SSD_PATH_INT8, X, dt, A, Bo, Co, D, sc, Y, final_state=h)
+    torch.cuda.synchronize()
+    An, Dn = _np(A), _np(D)
+    scales = {k: v.astype(np.float64).reshape((H_, P) if v.size == H_ * P else (G,)) for k, v in sc.host.items()}
+    states = []
+    for b, e in enumerate(ends):
+        v = [_np(t[b:b + 1, :e]) for t in (X, dt, Bo, Co)]
+        r = SO.forward_int8(v[0], v[1], An, v[2], v[3], Dn, scales, 64)
+        states.append(r["passed"][:, -1])
+        assert np.array_equal(h[b].cpu().numpy(), states[-1][0]), f"prompt {b}"
+        # single positions have no spread to measure by: the largest prompts' channels
+        if e > 64:
+            assert H.chan_err(_np(Y[b:b + 1, :e]), r["y"], dtype) <= 5e-2
+    ref = np.concatenate(states)
+    pos += lengths
+    ys, rs = [], []
+    for t in range(more):
+        x = torch.stack([c["xbc"][b, ends[b] + t] for b in range(B)])
+        raw = torch.stack([c["raw"][b, ends[b] + t] for b in range(B)])
+        _, o = convolve(x.float()[:, None].contiguous(), raw.float()[:, None].contiguous(), ring.float(), pos, None,
+                        torch.float32)
+        Xs, Bs, Cs, dts = (_np(k)[:, 0] for k in o)
+        y = torch.empty((B, H_, P), dtype=td, device="cuda")
+        L.ssd_conv_decode_step(L.make_shape(B, 1, H_, P, N, G, 64, dtype), L.SSD_PATH_INT8, conv, x, raw, A, D, sc,
+                               ring, pos, h, y)
+        pos += 1
+        torch.cuda.synchronize()
+        s = SO.decode_step_int8(Xs, dts, An, Bs, Cs, Dn, scales, ref)
+        ref = s["h"]
+        assert np.array_equal(h.cpu().numpy(), ref), t
+        ys.append(_np(y))
+        rs.append(s["y"])
+    assert H.chan_err(np.stack(ys, 1), np.stack(rs, 1), dtype) <= 5e-2

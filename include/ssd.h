@@ -58,11 +58,13 @@ enum {
   SSD_E_SHAPE = 2,       /* negative or zero sizes, H % G != 0, size overflow */
   SSD_E_UNSUPPORTED = 3, /* chunk not in {64,128,256}, P not in {16,32,64},
                             N not in {16,32,64,128}, unknown dtype or path */
-  SSD_E_ALIGN = 4,       /* a buffer is not 16-byte aligned */
+  SSD_E_ALIGN = 4,       /* a buffer is not aligned as the call asks: 16 bytes, but
+                            where it says element (strided rows, per-row arrays) */
   SSD_E_WORKSPACE = 5,   /* workspace smaller than ssd_workspace_bytes() */
   SSD_E_HIP = 6,         /* the HIP runtime reported a launch error */
   SSD_E_INTERNAL = 7,
-  SSD_E_VALUE = 8,       /* a calibration maximum is negative, NaN or infinite */
+  SSD_E_VALUE = 8,       /* a calibration maximum is negative, NaN or infinite, or a
+                            weight NaN or infinite */
   SSD_E_TOO_LARGE = 9    /* ssd_forward_noalloc: the problem needs more workspace
                             than SSD_NOALLOC_SCRATCH_BYTES */
 };

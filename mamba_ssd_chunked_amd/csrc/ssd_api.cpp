@@ -121,7 +121,7 @@ const char* ssd_status_string(int status) {
     case SSD_E_NULL: return "a required pointer is NULL";
     case SSD_E_SHAPE: return "invalid shape (sizes, H % G, or size overflow)";
     case SSD_E_UNSUPPORTED: return "unsupported chunk, headdim, dstate, dtype, path, taps or K";
-    case SSD_E_ALIGN: return "a buffer is not 16-byte aligned";
+    case SSD_E_ALIGN: return "a buffer is not aligned as the call asks (16 bytes, or its element's)";
     case SSD_E_WORKSPACE: return "workspace too small";
     case SSD_E_HIP: return "HIP runtime error";
     case SSD_E_INTERNAL: return "internal error";

@@ -258,3 +258,10 @@ def test_rows_of_no_columns_are_refused():
     L.ssd_matmul_i8(e(0, 64, dtype=torch.int8), e(0), e(16, 64, dtype=torch.int8), torch.zeros(16), None, e(0, 16))
     L.ssd_add_norm(e(0, 64), None, None, torch.ones(64), 1e-5, e(0, 64))
     L.ssd_gated_norm(e(0, 64), e(0, 64), 1, torch.ones(64), 1e-5, e(0, 64))
+
+
+def test_alignment_error_names_both_alignments():
+    """A float array at an odd address and a strided row at half an element are refused
+    with the same status as a dense buffer at 4 bytes: its text says so."""
+    assert mm(sa=ODD) == norm(x=ODD) == norm(out=MIS) == L.SSD_E_ALIGN
+    assert "16 bytes" in L.status_string(L.SSD_E_ALIGN) and "element" in L.status_string(L.SSD_E_ALIGN)

@@ -57,7 +57,8 @@ enum {
   SSD_E_NULL = 1,        /* a required pointer is NULL */
   SSD_E_SHAPE = 2,       /* negative or zero sizes, H % G != 0, size overflow */
   SSD_E_UNSUPPORTED = 3, /* chunk not in {64,128,256}, P not in {16,32,64},
-                            N not in {16,32,64,128}, unknown dtype or path */
+                            N not in {16,32,64,128}, unknown dtype or path,
+                            taps not in {2,3,4}, K % 16 != 0 */
   SSD_E_ALIGN = 4,       /* a buffer is not aligned as the call asks: 16 bytes, but
                             where it says element (strided rows, per-row arrays) */
   SSD_E_WORKSPACE = 5,   /* workspace smaller than ssd_workspace_bytes() */
@@ -435,8 +436,8 @@ int ssd_matmul_i8(int64_t M, int64_t N, int64_t K, const int8_t* a, const float*
 size_t ssd_matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Host-only: a weight matrix [N, K] (fp32, row-major) as 8-bit rows for
- * ssd_matmul_i8: w_scale[n] = fp32(max_k |w[n,k]| / 127) (1 for a row of
- * zeros), q = RHAZ(w / w_scale) evaluated in float64. A weight that is NaN or
+ * ssd_matmul_i8: w_scale[n] = fp32(max_k |w[n,k]| / 127) (1 where that rounds to
+ * zero), q = RHAZ(w / w_scale) evaluated in float64, at most 127 in size. A weight that is NaN or
  * infinite returns SSD_E_VALUE and nothing is written. */
 int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w_scale);
 

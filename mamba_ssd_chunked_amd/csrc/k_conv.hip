@@ -6,11 +6,16 @@
 // The work is one read of x | B | C and one write: memory bound. A thread owns
 // 16 bytes of channels and walks T positions down the sequence with the last
 // W - 1 inputs in registers, so every input is read once but for W - 1 rows at
-// the head of each tile (cache hits: the tile before reads them at its end).
+// the head of each tile. Those come from memory once more (the counters read 196 MB
+// for 179): the tile before mostly runs on another XCD, behind another L2.
 // Rows are loaded a set of kU ahead of their use (sets of 2 and 8 are slower by 6
 // and 15 %, tiles of 16 positions instead of 32 by 8 %), and written past the
-// caches (3 to 20 % faster: what is written exceeds them, and the tile heads
-// stay). 8 x 2048 x 5376 channels in fp16: 79 us, 4.5 TB/s of its 358 MB; three
+// caches: 3 to 20 % faster alone. With the SSD that reads them next, as much is lost
+// again in the middle (us, and with ordinary stores, 80 heads of 64 x 128 fp16, the
+// convolution and the float forward: 1 x 256 22.8, 22.4; 4 x 1024 102, 97; 8 x 2048
+// 307, 301; INT8 246, 243). Rows behind a sequence's end are read and computed like
+// the others before they are written as zeros: a ragged batch costs what a full one
+// does. 8 x 2048 x 5376 channels in fp16: 79 us, 4.5 TB/s of its 358 MB; three
 // waves on each SIMD hold 160 registers each (weights 40, window 24, sets 32),
 // and a fourth, with 128, spills (193 us). The blocks behind those of the
 // convolution compute dt.

@@ -12,13 +12,16 @@
 // channel (G runs of channels that are no multiple of 8 long: a kernel of single
 // channels). Two reductions over the row (the sum of squares, the largest
 // magnitude) cross the waves in LDS; short runs of channels are summed side by
-// side (4000 rows of 4096 in 64 runs: 35 -> 22 us). Rows leave past the caches (2
-// to 10 % faster; loads that do are slower).
-// Measured: 16384 rows of 2560 bf16 with an fp32 residual, codes and values
-// 98 us, 5.5 TB/s of 545 MB; 16384 of 5120 fp16, gated, 111 us, 5.3 TB/s (139 us
-// while the loads waited for one another and the codes took 3 more operations:
-// 63 % of the VALU's cycles were busy); 8 rows of 2560 3.3 us, a launch and two
-// memory round trips.
+// side (4000 rows of 4096 in 64 runs: 35 -> 22 us). Rows leave past the caches: 2 to
+// 10 % faster alone (loads that do are slower). With the 8-bit product that reads the
+// codes next it is even at 8 rows (9.2 us, gated norm and Out Proj 9.0) and 16384
+// (534 against 538 with ordinary stores, gated 275 against 280), but costs 2 to 7 %
+// where they would still lie in the caches (2048 rows: 80.7 against 78.7, gated 54.0
+// against 50.4).
+// Measured: 16384 rows of 2560 bf16 with an fp32 residual, codes and values 98 to
+// 101 us, 5.5 TB/s of 545 MB (codes only 86); 16384 of 5120 fp16, gated, 104 to 107
+// us, 5.6 TB/s (139 us while the loads waited for one another; codes only 83 to 86);
+// 8 rows of 2560 3.3 us, a launch and two memory round trips.
 //
 // The largest magnitude is found on bit patterns (unsigned order), in which
 // NaN is above infinity and infinity above every number: a row that holds

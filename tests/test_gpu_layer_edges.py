@@ -174,6 +174,52 @@ def test_norm_rows_of_zeros_without_eps(gpu_lib, cols, groups):
 
 
 # ---------------------------------------------------------------------------
+# more rows than workgroups
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cols,groups,rows", [(528, 0, 1 << 20), (528, 2, 1 << 20), (1024, 2, 1 << 20), (12, 4, 1 << 20),
+                                              (16, 0, 1 << 22), (32, 2, 1 << 22)])
+def test_norm_workgroups_that_take_several_rows(gpu_lib, cols, groups, rows):
+    """Rows behind the last workgroup's, which go to workgroups that have done a row
+    already (one of zeros, of huge values, of NaN, ...), are as in a call of their own;
+    with the rows written over their inputs too."""
+    import torch
+    L = gpu_lib
+    more = 3000
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.randn(rows + more, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    for first in (7, rows + 200):
+        x[first] = 0
+        x[first + 4] *= 1e25
+        x[first + 8, cols // 2] = float("nan")
+        x[first + 12] *= 1e-25
+        x[first + 16, 0] = float("inf")
+    w = 1 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    z = torch.ones_like(x) if groups else None
+
+    def run(x, z, eps, out, q, s):
+        if groups:
+            L.ssd_gated_norm(x, z, groups, w, eps, out, q, s)
+        else:
+            L.ssd_add_norm(x, None, None, w, eps, out, q, s)
+
+    def outputs(x, z, codes, place):
+        q = torch.empty(x.shape, dtype=torch.int8, device="cuda") if codes else None
+        s = torch.empty(x.shape[0], device="cuda") if codes else None
+        x = x.clone() if place else x
+        out = x if place else torch.empty_like(x)
+        run(x, z, 0.0, out, q, s)
+        return [t for t in (out, q, s) if t is not None]
+
+    for codes, place in ((True, False), (False, True), (True, True)):
+        whole = outputs(x, z, codes, place)
+        for part in (slice(0, 5000), slice(rows - 100, rows + more)):
+            alone = outputs(x[part].contiguous(), None if z is None else z[part].contiguous(), codes, False)
+            for a, b in zip(whole, alone):
+                assert torch.equal(H.bits(a[part].contiguous()), H.bits(b)), (codes, place, part)
+        del whole
+
+# ---------------------------------------------------------------------------
 # groups of odd sizes in long rows
 # ---------------------------------------------------------------------------
 

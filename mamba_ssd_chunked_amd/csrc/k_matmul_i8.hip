@@ -4,9 +4,10 @@
 //
 // Few rows are bound by the read of w, and there by latency: 8 x 2560 x 5120
 // (13 MB) 4.4 us, of which 2 are a launch; 333 x 8512 x 2048 12 us. Large
-// products are bound by power: 16384 x 10576 x 2560 449 to 475 us by card and by how
-// long it has been busy (2.0 Pop/s; up to 514 us under a tracer; with all codes zero
-// 1.45 times as fast), 16384 x 10752 x 2560 392 us,
+// products are bound by power: 16384 x 10576 x 2560 449 to 475 us by card (2.0 Pop/s;
+// with all codes zero 1.45 times as fast; of a run that begins at rest the first
+// passes take 440 us, the fifth to the fifteenth 500 to 546, and from about the
+// thirtieth on all 465), 16384 x 10752 x 2560 392 us,
 // 8192 x 8192 x 8192 423 us (2.6 Pop/s). A step of 128 bytes of a 256 x 256 tile
 // is 2048 cycles of each SIMD's matrix unit and as many of the LDS (192 KB read,
 // 64 KB written); four waves of 128 x 128 blocks instead of eight of 64 x 128

@@ -20,8 +20,8 @@
 // against 50.4).
 // Measured: 16384 rows of 2560 bf16 with an fp32 residual, codes and values 98 to
 // 101 us, 5.5 TB/s of 545 MB (codes only 86); 16384 of 5120 fp16, gated, 104 to 107
-// us, 5.6 TB/s (139 us while the loads waited for one another; codes only 83 to 86);
-// 8 rows of 2560 3.3 us, a launch and two memory round trips.
+// us, 5.5 TB/s (139 us while the loads waited for one another; codes only 83 to 88);
+// 8 rows of 2560 3.5 us, a launch and two memory round trips.
 //
 // The largest magnitude is found on bit patterns (unsigned order), in which
 // NaN is above infinity and infinity above every number: a row that holds
@@ -130,7 +130,8 @@ __device__ __forceinline__ float inv_root(float m) { return m > 0.f ? rsqrtf(m) 
 // rounds to zero. The codes are those of the quotient y / scale as fp32 rounds it: a
 // product with 1 / scale, and its remainder (exact in one multiply-add) brought in,
 // which costs no time (16384 rows of 5120 fp16, gated, codes only: 83 us; 87 with
-// y * (127 / most), whose codes next to a border were the neighbours'). Rows of steps
+// y * (127 / most), some of whose codes next to a border were the neighbours'; 8 rows
+// of 2560 3.47 us and 3.39, as the two divisions follow one another). Rows of steps
 // below 2^-64 are scaled up with them (up), exactly, so that the remainder is no
 // subnormal; a subnormal step may be well below most / 127: codes end at 127.
 struct Step {

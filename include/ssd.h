@@ -56,9 +56,9 @@ enum {
   SSD_OK = 0,
   SSD_E_NULL = 1,        /* a required pointer is NULL */
   SSD_E_SHAPE = 2,       /* negative or zero sizes, H % G != 0, size overflow */
-  SSD_E_UNSUPPORTED = 3, /* chunk not in {64,128,256}, P not in {16,32,64},
-                            N not in {16,32,64,128}, unknown dtype or path,
-                            taps not in {2,3,4}, K % 16 != 0 */
+  SSD_E_UNSUPPORTED = 3, /* chunk not in {64,128,256}, P not in {16,32,64} (128 where
+                            a call says so), N not in {16,32,64,128}, unknown dtype,
+                            path or flag, taps not in {2,3,4}, K % 16 != 0 */
   SSD_E_ALIGN = 4,       /* a buffer is not aligned as the call asks: 16 bytes, but
                             where it says element (strided rows, per-row arrays) */
   SSD_E_WORKSPACE = 5,   /* workspace smaller than ssd_workspace_bytes() */
@@ -440,6 +440,48 @@ size_t ssd_matmul_i8_workspace_bytes(int64_t M, int64_t N, int64_t K);
  * zero), q = RHAZ(w / w_scale) evaluated in float64, at most 127 in size. A weight that is NaN or
  * infinite returns SSD_E_VALUE and nothing is written. */
 int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w_scale);
+
+/* ---------------------------------------------------------------------------
+ * Operators that stand beside the SSD in a layer.
+ * ------------------------------------------------------------------------- */
+
+/* The gated delta rule: a state that forgets with a decay, as the SSD's, and that
+ * replaces what it holds for a key instead of adding to it.
+ *   k_t, q_t = B_t[g(h)], C_t[g(h)]   (SSD_DELTA_UNIT: v / sqrt(sum v^2 + eps))
+ *   b_t = beta_t[h]                   (SSD_DELTA_LOGIT: 1 / (1 + exp(-beta_t[h])))
+ *   a_t = exp(dt_t[h] A[h])
+ *   S_t = a_t S_{t-1} + b_t (x_t - a_t S_{t-1} k_t) k_t^T,   y_t = scale S_t q_t
+ * Sizes and layouts as ssd_forward's: X, Y [B, L, H, P] (values), dt [B, L, H], B, C
+ * [B, L, G, N] (keys, queries) in shape->dtype, A [H] fp32, as ssd_conv_forward
+ * writes them; headdim may also be 128. beta: row (b, t) at beta + (b*L + t)*ld_beta,
+ * H values in shape->dtype, so that a part of In Proj's rows is read in place (element
+ * aligned, ld_beta >= H and < 2^28). States [B, H, P, N] fp32. Positions with dt = 0
+ * and a key of zeros (as ssd_conv_forward writes behind a sequence's end) leave the
+ * state unchanged. Sums, decays and states are fp32 or more; Y is rounded once.
+ * |b_t| |k_t|^2 <= 2 keeps the state bounded; that is not checked.
+ * shape->chunk and shape->schedule have no influence, but must be supported values;
+ * batch * nheads < 2^24 (SSD_E_SHAPE). scale must be finite, eps >= 0 and finite
+ * (SSD_E_SHAPE); unknown flags return SSD_E_UNSUPPORTED. */
+enum { SSD_DELTA_UNIT = 1, SSD_DELTA_LOGIT = 2 };
+
+/* Prompts. initial_state (NULL: zeros) is the state before the first position,
+ * final_state (NULL: not wanted) receives the one after the last; they may be the
+ * same buffer. With seqlen == 0 and batch > 0 final_state is a copy of initial_state
+ * (or zeros), and X, dt, B, C, beta and Y are not looked at. workspace: device memory
+ * of at least ssd_delta_workspace_bytes(shape) bytes (may be NULL when that is 0). */
+int ssd_delta_forward(const ssd_shape* shape, int flags, const void* X, const void* dt, const float* A,
+                      const void* B, const void* C, const void* beta, int64_t ld_beta, float scale, float eps,
+                      void* Y, const float* initial_state, float* final_state, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_delta_forward needs (0 for an invalid shape). Host only. */
+size_t ssd_delta_workspace_bytes(const ssd_shape* shape);
+
+/* One position: X [B,H,P], dt [B,H], B, C [B,G,N], beta rows [B], Y [B,H,P]; state is
+ * read and overwritten in place. shape->seqlen must be 1 (or batch 0). */
+int ssd_delta_step(const ssd_shape* shape, int flags, const void* X, const void* dt, const float* A,
+                   const void* B, const void* C, const void* beta, int64_t ld_beta, float scale, float eps,
+                   float* state, void* Y, void* stream);
 
 /* Static string for a status code. */
 const char* ssd_status_string(int status);

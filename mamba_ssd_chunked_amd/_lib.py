@@ -39,6 +39,8 @@ SSD_PATH_FLOAT = 0
 SSD_PATH_INT8 = 1
 SSD_PATH_ABL_QX = 2
 SSD_PATH_ABL_RECON = 3
+SSD_DELTA_UNIT = 1
+SSD_DELTA_LOGIT = 2
 SSD_SCHED_AUTO = 0
 SSD_SCHED_HEAD = 1
 SSD_SCHED_CHUNK = 2
@@ -114,6 +116,9 @@ def _load() -> ctypes.CDLL:
         "ssd_gated_norm": [I64, I64, I64, ctypes.c_int, P, P, I64, P, ctypes.c_float, P, P, P, P],
         "ssd_matmul_i8": [I64, I64, I64, P, P, P, P, P, ctypes.c_int, P, P, ctypes.c_size_t, P],
         "ssd_pack_weight_i8": [I64, I64, P, P, P],
+        "ssd_delta_forward": [SP, ctypes.c_int, P, P, P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, P, P, P,
+                              ctypes.c_size_t, P],
+        "ssd_delta_step": [SP, ctypes.c_int, P, P, P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -127,6 +132,8 @@ def _load() -> ctypes.CDLL:
     lib.ssd_matmul_i8_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_calibrate_workspace_bytes.argtypes = [SP]
     lib.ssd_calibrate_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_delta_workspace_bytes.argtypes = [SP]
+    lib.ssd_delta_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_status_string.argtypes = [ctypes.c_int]
     lib.ssd_status_string.restype = ctypes.c_char_p
     return lib
@@ -141,6 +148,7 @@ EXPORTED = ("ssd_quantize_bc", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state
             "ssd_calibrate_amax", "ssd_calibrate_workspace_bytes", "ssd_scales_from_amax",
             "ssd_conv_forward", "ssd_conv_decode_step", "ssd_add_norm", "ssd_gated_norm", "ssd_matmul_i8",
             "ssd_matmul_i8_workspace_bytes", "ssd_pack_weight_i8",
+            "ssd_delta_forward", "ssd_delta_workspace_bytes", "ssd_delta_step",
             "ssd_status_string")
 
 
@@ -611,3 +619,70 @@ def ssd_pack_weight_i8(w: np.ndarray):
     _check("ssd_pack_weight_i8", LIB.ssd_pack_weight_i8(a.shape[0], a.shape[1], a.ctypes.data, q.ctypes.data,
                                                         s.ctypes.data))
     return q, s
+
+
+# ---------------------------------------------------------------------------
+# operators that stand beside the SSD in a layer
+# ---------------------------------------------------------------------------
+
+def ssd_delta_workspace_bytes(shape) -> int:
+    return int(LIB.ssd_delta_workspace_bytes(ctypes.byref(shape)))
+
+
+def ssd_delta_workspace(shape, device="cuda"):
+    """A workspace for ``ssd_delta_forward`` on ``device`` (None where none is needed)."""
+    need = ssd_delta_workspace_bytes(shape)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _delta_inputs(shape, X, dt, A, B, C, beta, Y, dev):
+    """Addresses of the gated delta rule's inputs and output, which must fit the shape."""
+    td = _TORCH_DTYPE.get(shape.dtype)
+    n = shape.batch * shape.seqlen
+    hp, gn = n * shape.nheads * shape.headdim, n * shape.ngroups * shape.dstate
+    if beta.numel() != n * shape.nheads:
+        raise ValueError(f"beta must hold {n} rows of {shape.nheads} values, got {tuple(beta.shape)}")
+    pb, ldb = _rows(beta, "beta", shape.nheads, td, dev)
+    return (_dense(X, "X", hp, td, dev), _dense(dt, "dt", n * shape.nheads, td, dev),
+            _dense(A, "A", shape.nheads, torch.float32, dev), _dense(B, "B", gn, td, dev), _dense(C, "C", gn, td, dev),
+            pb, ldb), _dense(Y, "Y", hp, td, dev)
+
+
+def _delta_flags(unit, logit) -> int:
+    return (SSD_DELTA_UNIT if unit else 0) | (SSD_DELTA_LOGIT if logit else 0)
+
+
+def ssd_delta_forward(shape, X, dt, A, B, C, beta, Y, final_state=None, initial_state=None, workspace=None, scale=1.0,
+                      unit=True, logit=False, eps=1e-6, stream=None):
+    """The gated delta rule over prompts: values ``X``, keys ``B``, queries ``C``, write
+    strengths ``beta`` [..., H] (may be a column slice of In Proj's output; ``logit``: before
+    their logistic function). ``unit`` takes keys and queries to length 1. A ``workspace`` (uint8)
+    is allocated here if None, and returned."""
+    if shape.batch == 0:
+        return workspace
+    dev = _current_device()
+    ns = shape.batch * shape.nheads * shape.headdim * shape.dstate
+    inputs, py = _delta_inputs(shape, X, dt, A, B, C, beta, Y, dev)
+    need = ssd_delta_workspace_bytes(shape)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+    wsb = 0 if workspace is None else workspace.numel()
+    _check("ssd_delta_forward", LIB.ssd_delta_forward(
+        ctypes.byref(shape), _delta_flags(unit, logit), *inputs, scale, eps, py,
+        _dense(initial_state, "initial_state", ns, torch.float32, dev),
+        _dense(final_state, "final_state", ns, torch.float32, dev), _dense(workspace, "workspace", wsb, torch.uint8, dev),
+        wsb, _stream_on(stream, dev)))
+    return workspace
+
+
+def ssd_delta_step(shape, X, dt, A, B, C, beta, state, Y, scale=1.0, unit=True, logit=False, eps=1e-6, stream=None):
+    """One position of the gated delta rule: ``state`` [B,H,P,N] float32 is updated in place.
+    ``shape.seqlen`` must be 1."""
+    if shape.batch == 0:
+        return
+    dev = _current_device()
+    inputs, py = _delta_inputs(shape, X, dt, A, B, C, beta, Y, dev)
+    ns = shape.batch * shape.nheads * shape.headdim * shape.dstate
+    _check("ssd_delta_step", LIB.ssd_delta_step(
+        ctypes.byref(shape), _delta_flags(unit, logit), *inputs, scale, eps,
+        _dense(state, "state", ns, torch.float32, dev), py, _stream_on(stream, dev)))

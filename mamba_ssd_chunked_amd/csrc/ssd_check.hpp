@@ -22,8 +22,9 @@ inline bool mul_ok(int64_t a, int64_t b, int64_t* out) {
   return true;
 }
 
-// Validates the shape; fills d. *empty is set for batch == 0 or seqlen == 0.
-inline int check_shape(const ssd_shape* s, Dims* d, bool* empty) {
+// Validates the shape; fills d. *empty is set for batch == 0 or seqlen == 0. Heads of
+// 128 channels are for the calls that say so.
+inline int check_shape(const ssd_shape* s, Dims* d, bool* empty, bool wide_heads = false) {
   if (!s) return SSD_E_NULL;
   if (s->schedule < SSD_SCHED_AUTO || s->schedule > SSD_SCHED_CHUNK) return SSD_E_SHAPE;
   if (s->batch < 0 || s->seqlen < 0) return SSD_E_SHAPE;
@@ -32,7 +33,8 @@ inline int check_shape(const ssd_shape* s, Dims* d, bool* empty) {
   if (s->nheads % s->ngroups != 0) return SSD_E_SHAPE;
   if (s->dtype < SSD_DTYPE_F32 || s->dtype > SSD_DTYPE_BF16) return SSD_E_UNSUPPORTED;
   if (s->chunk != 64 && s->chunk != 128 && s->chunk != 256) return SSD_E_UNSUPPORTED;
-  if (s->headdim != 16 && s->headdim != 32 && s->headdim != 64) return SSD_E_UNSUPPORTED;
+  if (s->headdim != 16 && s->headdim != 32 && s->headdim != 64 && !(wide_heads && s->headdim == 128))
+    return SSD_E_UNSUPPORTED;
   if (s->dstate != 16 && s->dstate != 32 && s->dstate != 64 && s->dstate != 128)
     return SSD_E_UNSUPPORTED;
   // grid limits: H in x, chunks in y, batch in z

@@ -155,6 +155,29 @@ struct MatmulI8Args {
 };
 hipError_t launch_matmul_i8(int out_dtype, const MatmulI8Args& a, hipStream_t st);
 
+// Gated delta rule (k_delta.hip, k_delta_step.hip). Dims::c counts chunks of
+// kDeltaChunk positions, whatever the shape's own chunk.
+constexpr int kDeltaChunk = 64;
+struct DeltaArgs {
+  const void* X;
+  const void* dt;
+  const float* A;
+  const void* B;
+  const void* C;
+  const void* beta;  // rows ld_beta elements apart
+  int64_t ld_beta;
+  float scale, eps;
+  bool unit, logit;
+  void* Y;
+  const float* init;  // [B,H,P,N] or null: zeros
+  float* final_state; // [B,H,P,N] or null
+};
+// One position after the other (any length, none among them).
+hipError_t launch_delta_steps(const Dims& d, int dtype, const DeltaArgs& a, hipStream_t st);
+// Chunks of positions; ws holds delta_workspace_bytes().
+hipError_t launch_delta_chunks(const Dims& d, int dtype, const DeltaArgs& a, void* ws, hipStream_t st);
+size_t delta_workspace_bytes(const Dims& d, int dtype);
+
 // Zero fill of a device buffer by a kernel (so that a captured graph holds no
 // memset node); bytes is a multiple of 16 and p 16-byte aligned.
 hipError_t launch_zero_fill(void* p, size_t bytes, hipStream_t st);

@@ -1,0 +1,105 @@
+// C ABI of the operators that stand beside the SSD in a layer: the gated delta rule.
+// Argument validation (host only, before any launch) and dispatch to the HIP kernels.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/ssd.h"
+#include "ssd_check.hpp"
+#include "ssd_launch.hpp"
+
+using ssd::Dims;
+using namespace ssd::host;
+
+namespace {
+
+size_t elem_bytes(int dtype) { return dtype == SSD_DTYPE_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Sequences that are taken one position after the other.
+bool delta_in_steps(const Dims& d) { return d.L <= 16; }
+
+// The shape of the gated delta rule; d->c counts its own chunks.
+int delta_shape(const ssd_shape* shape, Dims* d, bool* empty) {
+  const int rc = check_shape(shape, d, empty, true);
+  if (rc) return rc;
+  // the grids' thread counts stay below 2^32
+  if (d->B * (int64_t)d->H >= (int64_t)1 << 24) return SSD_E_SHAPE;
+  d->c = (int)((d->L + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk);
+  int64_t t, u;
+  if (!mul_ok(d->B, d->c, &t) || !mul_ok(t, d->H, &u) || !mul_ok(u, 1 << 15, &u) || !mul_ok(t, d->G, &u) ||
+      !mul_ok(u, 1 << 17, &u))
+    return SSD_E_SHAPE;
+  return SSD_OK;
+}
+
+int delta_args(const Dims& d, int dtype, int flags, const void* X, const void* dt, const float* A, const void* B,
+               const void* C, const void* beta, int64_t ld_beta, float scale, float eps, const void* Y,
+               ssd::DeltaArgs* a) {
+  if (flags & ~(SSD_DELTA_UNIT | SSD_DELTA_LOGIT)) return SSD_E_UNSUPPORTED;
+  if (!std::isfinite(scale) || !(eps >= 0.0f) || !std::isfinite(eps)) return SSD_E_SHAPE;
+  int rc = check_ptrs({A});
+  if (rc) return rc;
+  if (d.L > 0) {
+    if ((rc = check_ptrs({X, dt, B, C, Y}))) return rc;
+    if (!beta) return SSD_E_NULL;
+    if (!aligned_to(beta, elem_bytes(dtype))) return SSD_E_ALIGN;
+    if (ld_beta < d.H || ld_beta >= (int64_t)1 << 28) return SSD_E_SHAPE;
+    int64_t t;
+    if (!mul_ok(d.B, d.L, &t) || !mul_ok(t, ld_beta, &t) || !mul_ok(t, 4, &t)) return SSD_E_SHAPE;
+  }
+  *a = ssd::DeltaArgs{X, dt, A, B, C, beta, ld_beta, scale, eps, (flags & SSD_DELTA_UNIT) != 0,
+                      (flags & SSD_DELTA_LOGIT) != 0, const_cast<void*>(Y), nullptr, nullptr};
+  return SSD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_delta_workspace_bytes(const ssd_shape* shape) {
+  Dims d;
+  bool empty;
+  if (delta_shape(shape, &d, &empty) || empty || delta_in_steps(d)) return 0;
+  return ssd::delta_workspace_bytes(d, shape->dtype);
+}
+
+int ssd_delta_forward(const ssd_shape* shape, int flags, const void* X, const void* dt, const float* A, const void* B,
+                      const void* C, const void* beta, int64_t ld_beta, float scale, float eps, void* Y,
+                      const float* initial_state, float* final_state, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  Dims d;
+  bool empty;
+  int rc = delta_shape(shape, &d, &empty);
+  if (rc) return rc;
+  ssd::DeltaArgs a;
+  if ((rc = delta_args(d, shape->dtype, flags, X, dt, A, B, C, beta, ld_beta, scale, eps, Y, &a))) return rc;
+  if ((rc = check_opt({initial_state, final_state, workspace}))) return rc;
+  a.init = initial_state;
+  a.final_state = final_state;
+  if (d.B == 0 || (d.L == 0 && !final_state)) return SSD_OK;
+  if (delta_in_steps(d)) return hip_status(ssd::launch_delta_steps(d, shape->dtype, a, (hipStream_t)stream));
+  if (workspace_bytes < ssd::delta_workspace_bytes(d, shape->dtype)) return SSD_E_WORKSPACE;
+  if (!workspace) return SSD_E_NULL;
+  return hip_status(ssd::launch_delta_chunks(d, shape->dtype, a, workspace, (hipStream_t)stream));
+}
+
+int ssd_delta_step(const ssd_shape* shape, int flags, const void* X, const void* dt, const float* A, const void* B,
+                   const void* C, const void* beta, int64_t ld_beta, float scale, float eps, float* state, void* Y,
+                   void* stream) {
+  Dims d;
+  bool empty;
+  int rc = delta_shape(shape, &d, &empty);
+  if (rc) return rc;
+  if (d.B > 0 && d.L != 1) return SSD_E_SHAPE;
+  ssd::DeltaArgs a;
+  if ((rc = delta_args(d, shape->dtype, flags, X, dt, A, B, C, beta, ld_beta, scale, eps, Y, &a))) return rc;
+  if ((rc = check_ptrs({state}))) return rc;
+  if (empty) return SSD_OK;
+  a.init = a.final_state = state;
+  return hip_status(ssd::launch_delta_steps(d, shape->dtype, a, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,43 @@
+"""The operators that stand beside the SSD in a layer in float64 NumPy, from their
+definitions: the gated delta rule. Independent of the HIP code.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def sigmoid(v):
+    v = np.asarray(v, np.float64)
+    t = np.exp(-np.abs(v))
+    return np.where(v >= 0, 1.0, t) / (1.0 + t)
+
+
+def unit(v, eps):
+    """v / sqrt(sum v^2 + eps) over the last axis; zeros stay zeros."""
+    n = np.sqrt((v * v).sum(-1, keepdims=True) + eps)
+    return np.divide(v, n, out=np.zeros_like(v), where=n > 0)
+
+
+def delta(x, dt, A, k, q, beta, scale, state):
+    """The gated delta rule, one position after the other: x [B, L, H, P], dt, beta
+    [B, L, H], A [H], k, q [B, L, G, N], state [B, H, P, N]. Returns y, the state after,
+    and both with every term taken by its magnitude (for rounding bounds)."""
+    B, L, H, P = x.shape
+    r = H // k.shape[2]
+    k, q = np.repeat(k, r, 2), np.repeat(q, r, 2)
+    s, mag = state.copy(), np.abs(state)
+    y, ymag = np.zeros(x.shape), np.zeros(x.shape)
+    for t in range(L):
+        a = np.exp(dt[:, t] * A)[..., None, None]
+        s *= a
+        mag *= a
+        sk = np.matmul(s, k[:, t, :, :, None])[..., 0]
+        mk = np.matmul(mag, np.abs(k[:, t, :, :, None]))[..., 0]
+        b = beta[:, t, :, None]
+        s += (b * (x[:, t] - sk))[..., None] * k[:, t, :, None, :]
+        mag += np.minimum(np.abs(b) * (np.abs(x[:, t]) + mk), 1e300)[..., None] * np.abs(k[:, t, :, None, :])
+        # a write replaces what the key held: the magnitude of what a stable rule keeps
+        mag = np.minimum(mag, np.abs(s) + np.sqrt((s * s).sum(-1, keepdims=True)) + np.abs(x[:, t])[..., None])
+        y[:, t] = scale * np.matmul(s, q[:, t, :, :, None])[..., 0]
+        ymag[:, t] = abs(scale) * np.matmul(mag, np.abs(q[:, t, :, :, None]))[..., 0]
+    return y, s, ymag, mag

@@ -28,6 +28,9 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", f"-I{os.path.join(ROOT, 'include')}", f"
 # does not know the feature, which is harmless.
 HIP_FLAGS = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-munsafe-fp-atomics"]
+# Flags of single sources. The gated delta rule's products feed one another through the
+# vector unit: their results stay in vector registers.
+SOURCE_FLAGS = {"k_delta.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _hipcc() -> str:
@@ -41,7 +44,7 @@ def _compile(src: str, hip: bool) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
     cmd = [_hipcc(), *COMMON]
     if hip:
-        cmd += HIP_FLAGS
+        cmd += HIP_FLAGS + SOURCE_FLAGS.get(src, [])
     cmd += ["-c", os.path.join(HERE, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

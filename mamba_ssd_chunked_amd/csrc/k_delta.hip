@@ -55,14 +55,14 @@ struct KeyPlan {
 };
 // Of each (batch, head, chunk): fragments of T diag(b) (6 that are not zero, two
 // parts), of Y's weights (6), then floats: for each position the factors of K S^T in R
-// (kFacK), of Q S^T in Y (kFacQ) and of U in S' (kFacU), the state's decay and the
-// factors that undo the scaling of T and of the weights.
+// (kFacK), of Q S^T in Y (kFacQ) and of U in S' (kFacU), the state's decay, the factors
+// that undo the scaling of T and of the weights, and the largest of kFacU.
 template <int DT>
 struct HeadPlan {
   static constexpr int kT = 0, kA = 12, kFac = 12 + 6 * Parts<DT>::kWeights, kFrags = kFac + 1;
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
-enum { kFacK = 0, kFacQ = kC, kFacU = 2 * kC, kDecay = 3 * kC, kInvT, kInvA };
+enum { kFacK = 0, kFacQ = kC, kFacU = 2 * kC, kDecay = 3 * kC, kInvT, kInvA, kMaxU };
 
 // The fragment of tile row i and step s of a lower triangle of 4 x 4 tiles.
 __device__ __forceinline__ constexpr int lower_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
@@ -70,25 +70,34 @@ __device__ __forceinline__ constexpr int lower_frag(int i, int s) { return i < 2
 // ---------------------------------------------------------------------------
 // scaling and parts
 // ---------------------------------------------------------------------------
-// The power of two that brings m to [2^8, 2^9) (as near as fp32 has one), and its inverse.
+// The power of two that brings m to [2^8, 2^9), and its inverse; from 2^-82 on down it
+// is 2^90, so that products of two of them stay in fp32's range.
 struct Scale {
   float by, inv;
   __device__ __forceinline__ explicit Scale(float m) {
-    const int e = min(262 - (int)((__float_as_uint(m) >> 23) & 255), 254);
+    const int e = min(262 - (int)((__float_as_uint(m) >> 23) & 255), 217);
     by = __uint_as_float((uint32_t)e << 23);
-    inv = __uint_as_float(e == 254 ? 0x00400000u : (uint32_t)(254 - e) << 23);
+    inv = __uint_as_float((uint32_t)(254 - e) << 23);
   }
 };
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-// Eight values as fp16 numbers, and what that leaves of them as eight more.
-__device__ __forceinline__ void split8(const float (&x)[8], v8h& hi, v8h& lo) {
+// Eight values, times a power of two, as fp16 numbers, and what that leaves of them
+// as eight more.
+__device__ __forceinline__ void split8(const float (&x)[8], float by, v8h& hi, v8h& lo) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) hi[e] = (_Float16)x[e];
+  for (int e = 0; e < 8; ++e) hi[e] = (_Float16)(x[e] * by);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) lo[e] = (_Float16)(x[e] - (float)hi[e]);
+  for (int e = 0; e < 8; ++e) lo[e] = (_Float16)fmaf(x[e], by, -(float)hi[e]);
 }
+// Rows 4 (lane / 16) .. of two result tiles, as an operand.
+__device__ __forceinline__ void split_tiles(v4f a, v4f b, float by, v8h& hi, v8h& lo) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  split8(x, by, hi, lo);
+}
+// 2^x
+__device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ v4f mma16(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -114,15 +123,11 @@ __device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(fabsf(v[0]), f
 // ---------------------------------------------------------------------------
 // A workgroup of four waves takes a chunk of a group's keys and queries, and `heads`
 // of the group's heads, a wave one at a time.
-struct PrepareLds {
+struct PrepareWave {
   static constexpr int kDiagRow = 20, kDiag = 16 * kDiagRow + 4;  // floats; the blocks start 4 banks apart
-  float4 kk[10][kWave], kq[10][kWave];  // tiles of K K^T and K Q^T: of tile row i, column j at i (i + 1) / 2 + j
-  float fk[kC], fq[kC];
-  struct Wave {
-    double g[kC];
-    float beta[kC], rows[kC], cols[kC], first[3][kC];
-    float diag[4 * kDiag];
-  } w[4];
+  float g[kC], g_low[kC];  // sums of dt A log2(e): twice fp32's bits, as their differences count
+  float beta[kC], cols[kC], rows[4][kC], first[3][kC];
+  float diag[4 * kDiag];
 };
 
 template <int DT, int N>
@@ -131,8 +136,12 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
   typedef KeyPlan<DT, N> KP_;
   typedef HeadPlan<DT> HP_;
   constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
-  __shared__ __attribute__((aligned(16))) PrepareLds lds;
-  __shared__ __attribute__((aligned(16))) char frags[8 * KS * KP * kFrag];  // K's, then Q's
+  // K's fragments, then Q's; once the tiles are made, what a wave holds of its head
+  constexpr int kFragBytes = 8 * KS * KP * kFrag, kWaveBytes = 4 * sizeof(PrepareWave);
+  __shared__ __attribute__((aligned(16))) char frags[kFragBytes > kWaveBytes ? kFragBytes : kWaveBytes];
+  // tiles of K K^T and K Q^T: of tile row i, column j at i (i + 1) / 2 + j
+  __shared__ __attribute__((aligned(16))) float4 lds_kk[10][kWave], lds_kq[10][kWave];
+  __shared__ __attribute__((aligned(16))) float lds_fk[kC], lds_fq[kC];
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_id(), sub = lane >> 4, col = lane & 15;
 
   for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
@@ -187,8 +196,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
             // a row of zeros without eps stays zeros; next to a far larger eps the row counts for nothing
             f = eps > 0x1p126f ? sc.inv * rsqrtf(a.eps) : ss > 0.f ? rsqrtf(ss) : 0.f;
           }
-          if (which) lds.fq[row] = f * a.scale;
-          else lds.fk[row] = f;
+          if (which) lds_fq[row] = f * a.scale;
+          else lds_fk[row] = f;
         }
         if (s < KS) {
 #pragma unroll
@@ -200,7 +209,7 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
               t[4 + e] = x[16 + 4 * q + e];
             }
             v8h hi, lo;
-            split8(t, hi, lo);
+            split8(t, 1.f, hi, lo);
             const int at = ((which * KP * 4 + (row >> 4)) * KS + s) * kFrag + (q * 16 + (row & 15)) * 16;
             *(v8h*)(frags + at) = hi;
             if (hb == 0) *(v8h*)(out_keys + at) = hi;
@@ -245,11 +254,11 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
           acc = mma16(frag(0, 1, left, s), frag(which, 0, right, s), acc);
         }
       }
-      (which ? lds.kq : lds.kk)[u][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      (which ? lds_kq : lds_kk)[u][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     }
     __syncthreads();
 
-    PrepareLds::Wave& w = lds.w[wv];
+    PrepareWave& w = ((PrepareWave*)frags)[wv];
     const int last = min(hpg, (hb + 1) * heads);
     for (int hi_ = hb * heads + wv; hi_ < last; hi_ += 4) {
       const int h = g * hpg + hi_;
@@ -261,24 +270,36 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
         const bool live = pos0 + lane < L;
         const float dt = live ? ld_f<DT>(a.dt, pos * H + h) : 0.f;
         const float beta = live ? delta_beta<DT>(a, pos, h) : 0.f;
-        double gs = (double)dt * (double)a.A[h];  // decays' sums in 64 bits: their differences count
+        double gs = (double)dt * ((double)a.A[h] * 1.4426950408889634);
 #pragma unroll
         for (int o = 1; o < kWave; o *= 2) {
           const double up = __shfl_up(gs, o);
           if (lane >= o) gs += up;
         }
         const double end = __shfl(gs, lane | 15), total_g = __shfl(gs, kC - 1);
-        const float fk = lds.fk[lane], fq = lds.fq[lane], eg = expf((float)gs);
-        w.g[lane] = gs;
+        const float fk = lds_fk[lane], fq = lds_fq[lane], eg = exp2((float)gs);
+        const float fu = exp2((float)(total_g - gs)) * fk;
+        w.g[lane] = (float)gs;
+        w.g_low[lane] = (float)(gs - (double)(float)gs);
         w.beta[lane] = beta;
-        w.rows[lane] = beta * fk;
-        w.cols[lane] = expf((float)(end - gs)) * fk;  // from the position to the end of its 16
+        w.cols[lane] = exp2((float)(end - gs)) * fk;  // from the position to the end of its 16
+        w.rows[3][lane] = beta * fk;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) w.first[q][lane] = expf((float)fmin(gs - __shfl(gs, 16 * q + 15), 0.0));
+        for (int q = 0; q < 3; ++q) {  // from the end of the 16 positions q
+          const float first = exp2((float)fmin(gs - __shfl(gs, 16 * q + 15), 0.0));
+          w.first[q][lane] = first;
+          w.rows[q][lane] = beta * fk * first;
+        }
         fac[kFacK + lane] = eg * fk;
         fac[kFacQ + lane] = eg * fq;
-        fac[kFacU + lane] = expf((float)(total_g - gs)) * fk;
-        if (lane == 0) fac[kDecay] = expf((float)total_g);
+        fac[kFacU + lane] = fu;
+        float most = fu;
+#pragma unroll
+        for (int o = 1; o < kWave; o *= 2) most = fmaxf(most, __shfl_xor(most, o));
+        if (lane == 0) {
+          fac[kDecay] = exp2((float)total_g);
+          fac[kMaxU] = most;
+        }
       }
       wave_sync();
 
@@ -288,20 +309,19 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j <= i; ++j) {
-          const float4 kk = lds.kk[i * (i + 1) / 2 + j][lane], rf = *(const float4*)&w.rows[16 * i + 4 * sub];
+          const float4 kk = lds_kk[i * (i + 1) / 2 + j][lane], rf = *(const float4*)&w.rows[j < i ? j : 3][16 * i + 4 * sub];
           const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, rv[4] = {rf.x, rf.y, rf.z, rf.w};
           if (j < i) {
-            const float4 ff = *(const float4*)&w.first[j][16 * i + 4 * sub];
-            const float fv[4] = {ff.x, ff.y, ff.z, ff.w}, c = w.cols[16 * j + col];
+            const float c = w.cols[16 * j + col];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) l[i][j][e] = rv[e] * fv[e] * c * kv[e];
+            for (int e = 0; e < 4; ++e) l[i][j][e] = rv[e] * c * kv[e];
           } else {
-            const double gj = w.g[16 * i + col];
-            const float c = lds.fk[16 * i + col];
+            const float gj = w.g[16 * i + col], gl = w.g_low[16 * i + col], c = lds_fk[16 * i + col];
+            const v4f gi = *(const v4f*)&w.g[16 * i + 4 * sub], gil = *(const v4f*)&w.g_low[16 * i + 4 * sub];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float gamma = expf((float)fmin(w.g[16 * i + 4 * sub + e] - gj, 0.0));
-              w.diag[i * PrepareLds::kDiag + (4 * sub + e) * PrepareLds::kDiagRow + col] =
+              const float gamma = exp2(fminf((gi[e] - gj) + (gil[e] - gl), 0.f));
+              w.diag[i * PrepareWave::kDiag + (4 * sub + e) * PrepareWave::kDiagRow + col] =
                   col < 4 * sub + e ? rv[e] * c * gamma * kv[e] : 0.f;
             }
           }
@@ -309,27 +329,27 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
       wave_sync();
       // inverses of the diagonal blocks: 16 lanes a block, each a column, from the top
       {
-        const float* const d = w.diag + sub * PrepareLds::kDiag;
+        const float* const d = w.diag + sub * PrepareWave::kDiag;
         float t[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float v = i == col ? 1.f : 0.f;
 #pragma unroll
-          for (int k = 0; k < i; ++k) v = fmaf(-d[i * PrepareLds::kDiagRow + k], t[k], v);
+          for (int k = 0; k < i; ++k) v = fmaf(-d[i * PrepareWave::kDiagRow + k], t[k], v);
           t[i] = v;
         }
         wave_sync();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w.diag[sub * PrepareLds::kDiag + i * PrepareLds::kDiagRow + col] = t[i];
+        for (int i = 0; i < 16; ++i) w.diag[sub * PrepareWave::kDiag + i * PrepareWave::kDiagRow + col] = t[i];
       }
       wave_sync();
       v4f dc[4];  // the blocks' own tiles
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float* const d = w.diag + i * PrepareLds::kDiag;
+        const float* const d = w.diag + i * PrepareWave::kDiag;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dc[i][e] = d[(4 * sub + e) * PrepareLds::kDiagRow + col];
-        const float4 v = *(const float4*)(d + col * PrepareLds::kDiagRow + 4 * sub);
+        for (int e = 0; e < 4; ++e) dc[i][e] = d[(4 * sub + e) * PrepareWave::kDiagRow + col];
+        const float4 v = *(const float4*)(d + col * PrepareWave::kDiagRow + 4 * sub);
         x[i][i] = (v4f){v.x, v.y, v.z, v.w};
       }
       // x: transposed tiles of T, from T_ij = -(sum_{j<k<=i} T_ik L_kj) T_jj
@@ -350,14 +370,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int s = 0; s <= i / 2; ++s) {
-            float t[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[e] = m[i][2 * s][e] * by;
-              t[4 + e] = 2 * s + 1 <= i ? m[i][2 * s + 1][e] * by : 0.f;
-            }
             v8h hi, lo;
-            split8(t, hi, lo);
+            split_tiles(m[i][2 * s], 2 * s + 1 <= i ? m[i][2 * s + 1 <= i ? 2 * s + 1 : 0] : (v4f)(0.f), by, hi, lo);
             *(v8h*)(out + (first + lower_frag(i, s)) * kFrag + lane * 16) = hi;
             if (parts == 2) *(v8h*)(out + (first + 6 + lower_frag(i, s)) * kFrag + lane * 16) = lo;
           }
@@ -386,20 +400,20 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j <= i; ++j) {
-          const float4 kq = lds.kq[i * (i + 1) / 2 + j][lane];
-          const float kv[4] = {kq.x, kq.y, kq.z, kq.w}, fq = lds.fq[16 * i + col];
+          const float4 kq = lds_kq[i * (i + 1) / 2 + j][lane];
+          const float kv[4] = {kq.x, kq.y, kq.z, kq.w}, fq = lds_fq[16 * i + col];
           if (j < i) {
             const float4 cf = *(const float4*)&w.cols[16 * j + 4 * sub];
             const float cv[4] = {cf.x, cf.y, cf.z, cf.w}, r = fq * w.first[j][16 * i + col];
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[i][j][e] = r * cv[e] * kv[e];
           } else {
-            const double gi = w.g[16 * i + col];
-            const float4 cf = *(const float4*)&lds.fk[16 * i + 4 * sub];
-            const float cv[4] = {cf.x, cf.y, cf.z, cf.w};
+            const float gi = w.g[16 * i + col], gil = w.g_low[16 * i + col];
+            const v4f gj = *(const v4f*)&w.g[16 * i + 4 * sub], gl = *(const v4f*)&w.g_low[16 * i + 4 * sub];
+            const v4f cv = *(const v4f*)&lds_fk[16 * i + 4 * sub];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float gamma = expf((float)fmin(gi - w.g[16 * i + 4 * sub + e], 0.0));
+              const float gamma = exp2(fminf((gi - gj[e]) + (gil - gl[e]), 0.f));
               x[i][j][e] = 4 * sub + e <= col ? fq * cv[e] * gamma * kv[e] : 0.f;
             }
           }
@@ -421,14 +435,14 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_key
 // ---------------------------------------------------------------------------
 // NC consecutive values of a row.
 template <int DT, int NC>
-__device__ __forceinline__ void load_cols(const void* p, int64_t at, float (&v)[NC]) {
+__device__ __forceinline__ void load_cols(const char* p, float (&v)[NC]) {
   if constexpr (NC == 1) {
-    v[0] = ld_f<DT>(p, at);
+    v[0] = ld_f<DT>(p, 0);
   } else if constexpr (DT == DT_F32) {
-    const float2 t = *(const float2*)((const float*)p + at);
+    const float2 t = *(const float2*)p;
     v[0] = t.x; v[1] = t.y;
   } else {
-    const uint32_t t = *(const uint32_t*)((const u16*)p + at);
+    const uint32_t t = *(const uint32_t*)p;
     if constexpr (DT == DT_BF16) {
       v[0] = __uint_as_float(t << 16); v[1] = __uint_as_float(t & 0xffff0000u);
     } else {
@@ -438,231 +452,327 @@ __device__ __forceinline__ void load_cols(const void* p, int64_t at, float (&v)[
   }
 }
 template <int DT, int NC>
-__device__ __forceinline__ void store_cols(void* p, int64_t at, const float (&v)[NC]) {
-  if constexpr (NC == 1) ((typename Store<DT>::T*)p)[at] = to_store<DT>(v[0]);
-  else if constexpr (DT == DT_F32) *(float2*)((float*)p + at) = make_float2(v[0], v[1]);
-  else *(uint32_t*)((u16*)p + at) = pack2<DT>(v[0], v[1]);
+__device__ __forceinline__ void store_cols(char* p, const float (&v)[NC]) {
+  if constexpr (NC == 1) *(typename Store<DT>::T*)p = to_store<DT>(v[0]);
+  else if constexpr (DT == DT_F32) *(float2*)p = make_float2(v[0], v[1]);
+  else *(uint32_t*)p = pack2<DT>(v[0], v[1]);
 }
 
 // The largest of a column, of which a lane has m of its 4 rows in each tile.
 __device__ __forceinline__ float column_max(float m) {
-  m = fmaxf(m, __shfl_xor(m, 16));
-  return fmaxf(m, __shfl_xor(m, 32));
+  const uint32_t b = __float_as_uint(m);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t c = __float_as_uint(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const auto q = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
-template <int DT, int N, int NC>
-__global__ __launch_bounds__(256) void k_delta_scan(DeltaArgs a, const char* ws_keys, const char* ws_heads, int64_t L,
-                                                  int H, int G, int hpg, int P, int chunks, int64_t items) {
+// 16 bytes per lane from global memory straight into LDS: lane i's bytes land at l + 16 i.
+__device__ __forceinline__ void copy_frag(const char* g, char* l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) char*)g,
+                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+}
+
+// A workgroup of W waves takes W * 16 NC rows of a head's state. The chunk's fragments
+// come through LDS in two halves, K and Q (phase 1), and the rest (phase 2): the copies
+// of the next chunk's half are on their way while the other half is used, with one
+// barrier in between.
+template <int DT, int N, int NC, int W>
+__global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaArgs a, const char* ws_keys, const char* ws_heads, int64_t L,
+                                                     int H, int G, int hpg, int P, int chunks) {
   typedef KeyPlan<DT, N> KP_;
   typedef HeadPlan<DT> HP_;
   constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
   constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
-  const int lane = lane_id(), sub = lane >> 4, col = lane & 15;
-  const int64_t item = (int64_t)blockIdx.x * 4 + wave_id();
-  if (item >= items) return;
-  const int slices = P / (16 * NC);
-  const int64_t unit = item / slices, b = unit / H;
+  constexpr int kFirst = KP_::kT, kTurned = KP_::kFrags - KP_::kT;  // K and Q; K^T
+  __shared__ __attribute__((aligned(1024))) char buf1[kFirst * kFrag];
+  __shared__ __attribute__((aligned(1024))) char buf2[(kTurned + HP_::kFrags) * kFrag];
+  const int lane = lane_id(), wv = wave_id(), sub = lane >> 4, col = lane & 15;
+  const int slices = P / (16 * NC * W);
+  const int64_t unit = blockIdx.x / slices, b = unit / H;
   const int h = (int)(unit % H), g = h / hpg;
-  const int p0 = (int)(item % slices) * 16 * NC + NC * col;  // the lane's columns: p0 .. p0 + NC - 1
+  const int p0 = ((int)(blockIdx.x % slices) * W + wv) * 16 * NC + NC * col;  // the lane's columns: p0 .. p0 + NC - 1
   const char* keys = ws_keys + (b * G + g) * (int64_t)chunks * KP_::kBytes + lane * 16;
-  const char* head = ws_heads + unit * (int64_t)chunks * HP_::kBytes;
+  const char* head = ws_heads + unit * (int64_t)chunks * HP_::kBytes + lane * 16;
 
+  auto copy1 = [&](const char* k) {
+#pragma unroll
+    for (int f = 0; f < kFirst; f += W)
+      if (kFirst % W == 0 || f + wv < kFirst) copy_frag(k + (f + wv) * kFrag, buf1 + (f + wv) * kFrag);
+  };
+  auto copy2 = [&](const char* k, const char* hd) {
+#pragma unroll
+    for (int f = 0; f < kTurned; f += W)
+      if (kTurned % W == 0 || f + wv < kTurned) copy_frag(k + (kFirst + f + wv) * kFrag, buf2 + (f + wv) * kFrag);
+#pragma unroll
+    for (int f = 0; f < HP_::kFrags; f += W)
+      if (HP_::kFrags % W == 0 || f + wv < HP_::kFrags)
+        copy_frag(hd + (f + wv) * kFrag, buf2 + (kTurned + f + wv) * kFrag);
+  };
+  // this wave's copies have arrived; behind the barrier all have, and what was read before it is free
+  auto meet = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto key = [&](int f) { return *(const v8h*)(buf1 + f * kFrag + lane * 16); };
+  auto turned = [&](int f) { return *(const v8h*)(buf2 + f * kFrag + lane * 16); };
+  auto weight = [&](int f) { return *(const v8h*)(buf2 + (kTurned + f) * kFrag + lane * 16); };
+  const float* const fac = (const float*)(buf2 + (kTurned + HP_::kFac) * kFrag);
+
+  copy1(keys);
+  copy2(keys, head);
+  // Rows of X and Y: a uniform address for each of a chunk's, and the lane's place in
+  // it (64 rows are less than 2^32 bytes). Behind the end of the sequence the last row
+  // stands in: what it meets in T is zero.
+  constexpr int kE = sizeof(typename Store<DT>::T);
+  const uint32_t step = (uint32_t)H * P * kE, place = 4 * sub * step + p0 * kE;
+  const char* x_at = (const char*)a.X + (b * L * H + h) * P * kE;
+  char* y_at = (char*)a.Y + (b * L * H + h) * P * kE;
+  float v[4][4][NC];
+  auto load_values = [&](int n) {
+    if (n >= kC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) load_cols<DT, NC>(x_at + (uint64_t)(16 * i + e) * step + place, v[i][e]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          load_cols<DT, NC>(x_at + (min(16 * i + 4 * sub + e, n - 1) * step + p0 * kE), v[i][e]);
+    }
+    x_at += (uint64_t)kC * step;
+  };
+  load_values((int)min(L, (int64_t)kC));
   v4f s[NC][NT];
+  // The state is held times a power of two, one for each of its rows: 1 / inv_s.
+  float inv_s[NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
+  for (int c = 0; c < NC; ++c) {
+    float m = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
       s[c][n] = a.init ? *(const v4f*)(a.init + (unit * P + p0 + c) * (int64_t)N + 16 * n + 4 * sub) : (v4f)(0.f);
-
-  for (int ck = 0; ck < chunks; ++ck, keys += KP_::kBytes, head += HP_::kBytes) {
-    const float* const fac = (const float*)(head + HP_::kFac * kFrag);
-    auto key = [&](int f) { return *(const v8h*)(keys + f * kFrag); };
-    auto weight = [&](int f) { return *(const v8h*)(head + f * kFrag + lane * 16); };
-    const int64_t pos0 = (int64_t)ck * kC + 4 * sub;
-
-    float v[4][4][NC];
+      m = fmaxf(m, max4(s[c][n]));
+    }
+    const Scale sc(column_max(m));
+    inv_s[c] = sc.inv;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t pos = pos0 + 16 * i + e;
-        load_cols<DT, NC>(a.X, ((b * L + min(pos, L - 1)) * H + h) * P + p0, v[i][e]);
-        if (pos >= L) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) v[i][e][c] = 0.f;
-        }
-      }
+    for (int n = 0; n < NT; ++n) s[c][n] *= sc.by;
+  }
+  meet();
 
-    // K S^T and Q S^T
+  float one = 1.f;  // not known to be it: x 1 - hi, rounded to fp16, is one operation
+  asm volatile("" : "+v"(one));
+  for (int ck = 0; ck < chunks; ++ck) {
+    const bool more = ck + 1 < chunks;
+    const int left = (int)min(L - (int64_t)ck * kC, (int64_t)kC);  // positions of this chunk
+    keys += KP_::kBytes;
+    head += HP_::kBytes;
+    // phase 1: K S^T and Q S^T
     v4f ks[NC][4], qs[NC][4];
-    float inv_s[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      float m = 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) m = fmaxf(m, max4(s[c][n]));
-      const Scale sc(column_max(m));
-      inv_s[c] = sc.inv;
 #pragma unroll
       for (int i = 0; i < 4; ++i) ks[c][i] = qs[c][i] = (v4f)(0.f);
+    }
 #pragma unroll
-      for (int t = 0; t < KS; ++t) {
-        float x[8];
+    for (int t = 0; t < KS; ++t) {
+      v8h hi[NC], lo[NC];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = s[c][2 * t][e] * sc.by;
-          x[4 + e] = 2 * t + 1 < NT ? s[c][2 * t + 1][e] * sc.by : 0.f;
-        }
-        v8h hi, lo;
-        split8(x, hi, lo);
+      for (int c = 0; c < NC; ++c)
+        split_tiles(s[c][2 * t], 2 * t + 1 < NT ? s[c][2 * t + 1 < NT ? 2 * t + 1 : 0] : (v4f)(0.f), one, hi[c], lo[c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const v8h k = key(KP_::kK + i * KS + t), q = key(KP_::kQ + i * KS + t);
-          ks[c][i] = mma16(k, hi, ks[c][i]);
-          ks[c][i] = mma16(k, lo, ks[c][i]);
-          qs[c][i] = mma16(q, hi, qs[c][i]);
-          if constexpr (SY == 2) qs[c][i] = mma16(q, lo, qs[c][i]);
+      for (int i = 0; i < 4; ++i) {
+        const v8h k = key(KP_::kK + i * KS + t), q = key(KP_::kQ + i * KS + t);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          ks[c][i] = mma16(k, hi[c], ks[c][i]);
+          qs[c][i] = mma16(q, hi[c], qs[c][i]);
+          ks[c][i] = mma16(k, lo[c], ks[c][i]);
+          if constexpr (SY == 2) qs[c][i] = mma16(q, lo[c], qs[c][i]);
           if constexpr (KP == 2) {
-            ks[c][i] = mma16(key(KP_::kK + (4 + i) * KS + t), hi, ks[c][i]);
-            qs[c][i] = mma16(key(KP_::kQ + (4 + i) * KS + t), hi, qs[c][i]);
+            ks[c][i] = mma16(key(KP_::kK + (4 + i) * KS + t), hi[c], ks[c][i]);
+            qs[c][i] = mma16(key(KP_::kQ + (4 + i) * KS + t), hi[c], qs[c][i]);
           }
         }
       }
     }
-    // U = T diag(b) (V - e^g K S^T)
+    meet();
+    if (more) copy1(keys);
+
+    // phase 2: U = T diag(b) (V - e^g K S^T), times 1 / inv_u
     v4f u[NC][4];
+    float inv_u[NC], max_u[NC];
+    {
+      float by[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      v4f r[4];
-      float m = 0.f;
+      for (int c = 0; c < NC; ++c) {
+        float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4f f = *(const v4f*)(fac + kFacK + 16 * i + 4 * sub);
+        for (int i = 0; i < 4; ++i) {
+          const v4f f = *(const v4f*)(fac + kFacK + 16 * i + 4 * sub);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[i][e] = fmaf(-f[e] * inv_s[c], ks[c][i][e], v[i][e][c]);
-        m = fmaxf(m, max4(r[i]));
-        u[c][i] = (v4f)(0.f);
+          for (int e = 0; e < 4; ++e) ks[c][i][e] = fmaf(-f[e] * inv_s[c], ks[c][i][e], v[i][e][c]);
+          m = fmaxf(m, max4(ks[c][i]));
+          u[c][i] = (v4f)(0.f);
+        }
+        const Scale sc(column_max(m));
+        by[c] = sc.by;
+        inv_u[c] = sc.inv * fac[kInvT];
       }
-      const Scale sc(column_max(m));
+      if (more) load_values((int)min(L - (int64_t)(ck + 1) * kC, (int64_t)kC));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        float x[8];
+        v8h hi[NC], lo[NC];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = r[2 * t][e] * sc.by;
-          x[4 + e] = r[2 * t + 1][e] * sc.by;
-        }
-        v8h hi, lo;
-        split8(x, hi, lo);
+        for (int c = 0; c < NC; ++c) split_tiles(ks[c][2 * t], ks[c][2 * t + 1], by[c], hi[c], lo[c]);
 #pragma unroll
         for (int i = 2 * t; i < 4; ++i) {
-          const v8h w = weight(HP_::kT + lower_frag(i, t));
-          u[c][i] = mma16(w, hi, u[c][i]);
-          u[c][i] = mma16(w, lo, u[c][i]);
-          u[c][i] = mma16(weight(HP_::kT + 6 + lower_frag(i, t)), hi, u[c][i]);
+          const v8h w = weight(HP_::kT + lower_frag(i, t)), wl = weight(HP_::kT + 6 + lower_frag(i, t));
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            u[c][i] = mma16(w, hi[c], u[c][i]);
+            u[c][i] = mma16(w, lo[c], u[c][i]);
+            u[c][i] = mma16(wl, hi[c], u[c][i]);
+          }
         }
       }
-      const float inv = fac[kInvT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[c][i] = u[c][i] * inv * sc.inv;
+      for (int c = 0; c < NC; ++c) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = fmaxf(m, max4(u[c][i]));
+        max_u[c] = column_max(m);
+      }
     }
     // Y
-    float y[4][4][NC];
+    {
+      v4f yd[NC][4];
+      float by[NC], inv[NC];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float m = 0.f;
+      for (int c = 0; c < NC; ++c) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) m = fmaxf(m, max4(u[c][i]));
-      const Scale sc(column_max(m));
-      v4f yd[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) yd[i] = (v4f)(0.f);
+        for (int i = 0; i < 4; ++i) yd[c][i] = (v4f)(0.f);
+        const Scale sc(max_u[c]);
+        by[c] = sc.by;
+        inv[c] = sc.inv * inv_u[c] * fac[kInvA];
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        float x[8];
+        v8h hi[NC], lo[NC];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = u[c][2 * t][e] * sc.by;
-          x[4 + e] = u[c][2 * t + 1][e] * sc.by;
-        }
-        v8h hi, lo;
-        split8(x, hi, lo);
+        for (int c = 0; c < NC; ++c) split_tiles(u[c][2 * t], u[c][2 * t + 1], by[c], hi[c], lo[c]);
 #pragma unroll
         for (int i = 2 * t; i < 4; ++i) {
           const v8h w = weight(HP_::kA + lower_frag(i, t));
-          yd[i] = mma16(w, hi, yd[i]);
-          if constexpr (UY == 2) yd[i] = mma16(w, lo, yd[i]);
-          if constexpr (AP == 2) yd[i] = mma16(weight(HP_::kA + 6 + lower_frag(i, t)), hi, yd[i]);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            yd[c][i] = mma16(w, hi[c], yd[c][i]);
+            if constexpr (UY == 2) yd[c][i] = mma16(w, lo[c], yd[c][i]);
+            if constexpr (AP == 2) yd[c][i] = mma16(weight(HP_::kA + 6 + lower_frag(i, t)), hi[c], yd[c][i]);
+          }
         }
       }
-      const float inv = fac[kInvA];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const v4f f = *(const v4f*)(fac + kFacQ + 16 * i + 4 * sub);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[i][e][c] = fmaf(f[e] * inv_s[c], qs[c][i][e], yd[i][e] * inv * sc.inv);
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) yd[c][i][e] = fmaf(f[e] * inv_s[c], qs[c][i][e], yd[c][i][e] * inv[c]);
       }
+      auto store = [&](int i, int e) {
+        float y[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) y[c] = yd[c][i][e];
+        store_cols<DT, NC>(y_at + (uint64_t)(16 * i + e) * step + place, y);
+      };
+      if (left >= kC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store(i, e);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * i + 4 * sub + e < left) store(i, e);
+      }
+      y_at += (uint64_t)kC * step;
     }
+    // S' = e^{g_63} S + (e^{g_63 - g} U)^T K, the products added to the scaled state: its
+    // largest value is brought to 2^8 and U's part to 2 at most, so that the sums (64
+    // terms, keys up to 2^8) stay below 2^16 as fp16's range asks.
+    {
+      const float decay = fac[kDecay], most = fac[kMaxU] * 256.f;
+      float by[NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+      for (int c = 0; c < NC; ++c) {
+        float m = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t pos = pos0 + 16 * i + e;
-        if (pos < L) store_cols<DT, NC>(a.Y, ((b * L + pos) * H + h) * P + p0, y[i][e]);
+        for (int n = 0; n < NT; ++n) m = fmaxf(m, max4(s[c][n]));
+        const Scale sc(fmaxf(column_max(m) * inv_s[c] * decay, max_u[c] * inv_u[c] * most));
+        const float keep = decay * (inv_s[c] * sc.by);
+        by[c] = inv_u[c] * sc.by;
+        inv_s[c] = sc.inv;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[c][n] *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[c][i] *= *(const v4f*)(fac + kFacU + 16 * i + 4 * sub);
       }
-    // S' = e^{g_63} S + (e^{g_63 - g} U)^T K
-    const float decay = fac[kDecay];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float m = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u[c][i] *= *(const v4f*)(fac + kFacU + 16 * i + 4 * sub);
-        m = fmaxf(m, max4(u[c][i]));
-      }
-      const Scale sc(column_max(m));
-      v4f ds[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) ds[n] = (v4f)(0.f);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        float x[8];
+        v8h hi[NC], lo[NC];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = u[c][2 * t][e] * sc.by;
-          x[4 + e] = u[c][2 * t + 1][e] * sc.by;
-        }
-        v8h hi, lo;
-        split8(x, hi, lo);
+        for (int c = 0; c < NC; ++c) split_tiles(u[c][2 * t], u[c][2 * t + 1], by[c], hi[c], lo[c]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const v8h k = key(KP_::kT + 2 * n + t);
-          ds[n] = mma16(k, hi, ds[n]);
-          ds[n] = mma16(k, lo, ds[n]);
-          if constexpr (KP == 2) ds[n] = mma16(key(KP_::kT + 2 * NT + 2 * n + t), hi, ds[n]);
+          const v8h k = turned(2 * n + t);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            s[c][n] = mma16(k, hi[c], s[c][n]);
+            s[c][n] = mma16(k, lo[c], s[c][n]);
+            if constexpr (KP == 2) s[c][n] = mma16(turned(2 * NT + 2 * n + t), hi[c], s[c][n]);
+          }
         }
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[c][n][e] = fmaf(ds[n][e], sc.inv, s[c][n][e] * decay);
     }
+    meet();
+    if (more) copy2(keys, head);
   }
   if (a.final_state) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        *(v4f*)(a.final_state + (unit * P + p0 + c) * (int64_t)N + 16 * n + 4 * sub) = s[c][n];
+        *(v4f*)(a.final_state + (unit * P + p0 + c) * (int64_t)N + 16 * n + 4 * sub) = s[c][n] * inv_s[c];
   }
 }
 
-template <int DT, int N, int NC>
+template <int DT, int N, int NC, int W>
 hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, hipStream_t st) {
-  const int64_t items = d.B * d.H * (d.P / (16 * NC));
-  hipLaunchKernelGGL((k_delta_scan<DT, N, NC>), dim3((unsigned)((items + 3) / 4)), dim3(256), 0, st, a, keys, heads, d.L,
-                     d.H, d.G, d.hpg, d.P, d.c, items);
+  const int64_t wgs = d.B * d.H * (d.P / (16 * NC * W));
+  hipLaunchKernelGGL((k_delta_scan<DT, N, NC, W>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
+                     d.G, d.hpg, d.P, d.c);
   return hipGetLastError();
+}
+
+// Four waves of 16 rows each where the head has them (us at 4, 2 and 1 waves: 8 x 2048
+// positions of 80 heads of 64 x 128, 16 bits, 594, 1403 and 2311 before later steps; one
+// sequence of 2048, 64 heads, 192, 214 and 246). Waves of 32 rows read LDS half as
+// often, but leave each SIMD one wave: 439 us with 16, 559 with 32.
+template <int DT, int N>
+hipError_t pick_scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, hipStream_t st) {
+  switch (d.P) {
+    case 16: return scan<DT, N, 1, 1>(d, a, keys, heads, st);
+    case 32: return scan<DT, N, 1, 2>(d, a, keys, heads, st);
+    default: return scan<DT, N, 1, 4>(d, a, keys, heads, st);
+  }
 }
 
 template <int DT, int N>
@@ -680,8 +790,7 @@ hipError_t go(const Dims& d, const DeltaArgs& a, char* ws, hipStream_t st) {
                      heads, d.L, d.H, d.G, d.hpg, d.c, blocks, per, total);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return d.P % 32 == 0 && d.B * d.H * (d.P / 32) >= 4 * ncu ? scan<DT, N, 2>(d, a, ws, heads, st)
-                                                             : scan<DT, N, 1>(d, a, ws, heads, st);
+  return pick_scan<DT, N>(d, a, ws, heads, st);
 }
 
 template <int DT>

@@ -483,6 +483,38 @@ int ssd_delta_step(const ssd_shape* shape, int flags, const void* X, const void*
                    const void* B, const void* C, const void* beta, int64_t ld_beta, float scale, float eps,
                    float* state, void* Y, void* stream);
 
+/* Activations of ssd_matmul and ssd_block_norm. GELU is u Phi(u) with the normal
+ * distribution's Phi, GELU_TANH the approximation
+ * u (1 + tanh(sqrt(2 / pi) (u + 0.044715 u^3))) / 2; RELU2 is relu(u)^2. */
+enum {
+  SSD_ACT_NONE = 0,
+  SSD_ACT_RELU = 1,
+  SSD_ACT_RELU2 = 2,
+  SSD_ACT_SILU = 3,
+  SSD_ACT_SIGMOID = 4,
+  SSD_ACT_GELU = 5,
+  SSD_ACT_GELU_TANH = 6
+};
+
+/* Matrix product with its epilogue (projections of a layer in floating point):
+ *   out[m,n] = act(sum_k a[m,k] w[n,k] + bias[n]) + residual[m,n]
+ * a [M, K] at row distance ld_a (element aligned: a part of wider rows is read in
+ * place) and w [N, K] dense in dtype; bias [N] fp32 (NULL: 0); act an SSD_ACT_*
+ * code; out [M, N] and residual [M, N] (NULL: 0) dense in out_dtype, which is dtype or
+ * SSD_DTYPE_F32. residual may be out itself. Sums and the epilogue are fp32, rounded
+ * once (fp32 operands are multiplied in fp32). Any K; rows that are 16-byte aligned
+ * and a multiple of 16 bytes long are fastest. M, N < 2^26, M * N < 2^40, K <= ld_a <
+ * 2^22 (SSD_E_SHAPE); M == 0 is a valid empty problem. An unknown activation or type,
+ * or an out_dtype that is neither, returns SSD_E_UNSUPPORTED. workspace: device memory
+ * of at least ssd_matmul_workspace_bytes(M, N, K, dtype) bytes, 16-byte aligned. No
+ * product needs one at present: that is 0, and NULL will do. */
+int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_t ld_a, const void* w,
+               const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes ssd_matmul needs: 0. Host only. */
+size_t ssd_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+
 /* Static string for a status code. */
 const char* ssd_status_string(int status);
 

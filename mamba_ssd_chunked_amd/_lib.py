@@ -41,6 +41,13 @@ SSD_PATH_ABL_QX = 2
 SSD_PATH_ABL_RECON = 3
 SSD_DELTA_UNIT = 1
 SSD_DELTA_LOGIT = 2
+SSD_ACT_NONE = 0
+SSD_ACT_RELU = 1
+SSD_ACT_RELU2 = 2
+SSD_ACT_SILU = 3
+SSD_ACT_SIGMOID = 4
+SSD_ACT_GELU = 5
+SSD_ACT_GELU_TANH = 6
 SSD_SCHED_AUTO = 0
 SSD_SCHED_HEAD = 1
 SSD_SCHED_CHUNK = 2
@@ -118,6 +125,8 @@ def _load() -> ctypes.CDLL:
         "ssd_pack_weight_i8": [I64, I64, P, P, P],
         "ssd_delta_forward": [SP, ctypes.c_int, P, P, P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, P, P, P,
                               ctypes.c_size_t, P],
+        "ssd_matmul": [I64, I64, I64, ctypes.c_int, P, I64, P, P, ctypes.c_int, P, ctypes.c_int, P, P, ctypes.c_size_t,
+                       P],
         "ssd_delta_step": [SP, ctypes.c_int, P, P, P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, P, P],
     }
     for name, args in sig.items():
@@ -132,6 +141,8 @@ def _load() -> ctypes.CDLL:
     lib.ssd_matmul_i8_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_calibrate_workspace_bytes.argtypes = [SP]
     lib.ssd_calibrate_workspace_bytes.restype = ctypes.c_size_t
+    lib.ssd_matmul_workspace_bytes.argtypes = [I64, I64, I64, ctypes.c_int]
+    lib.ssd_matmul_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_delta_workspace_bytes.argtypes = [SP]
     lib.ssd_delta_workspace_bytes.restype = ctypes.c_size_t
     lib.ssd_status_string.argtypes = [ctypes.c_int]
@@ -149,6 +160,7 @@ EXPORTED = ("ssd_quantize_bc", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state
             "ssd_conv_forward", "ssd_conv_decode_step", "ssd_add_norm", "ssd_gated_norm", "ssd_matmul_i8",
             "ssd_matmul_i8_workspace_bytes", "ssd_pack_weight_i8",
             "ssd_delta_forward", "ssd_delta_workspace_bytes", "ssd_delta_step",
+            "ssd_matmul", "ssd_matmul_workspace_bytes",
             "ssd_status_string")
 
 
@@ -686,3 +698,36 @@ def ssd_delta_step(shape, X, dt, A, B, C, beta, state, Y, scale=1.0, unit=True, 
     _check("ssd_delta_step", LIB.ssd_delta_step(
         ctypes.byref(shape), _delta_flags(unit, logit), *inputs, scale, eps,
         _dense(state, "state", ns, torch.float32, dev), py, _stream_on(stream, dev)))
+
+
+def ssd_matmul_workspace_bytes(m, n, k, dtype) -> int:
+    return int(LIB.ssd_matmul_workspace_bytes(m, n, k, _code(dtype)))
+
+
+def ssd_matmul_workspace(a, w, out):
+    """A workspace for ``ssd_matmul`` on these tensors (None where none is needed)."""
+    need = ssd_matmul_workspace_bytes(out.numel() // max(1, out.shape[-1]), w.shape[0], w.shape[1], a.dtype)
+    return torch.empty(need, dtype=torch.uint8, device=out.device) if need else None
+
+
+def ssd_matmul(a, w, bias, out, act=SSD_ACT_NONE, residual=None, workspace=None, stream=None):
+    """out = act(a @ w.T + bias) + residual for a [..., K] (may be a column slice), w [N, K] of a's
+    type; ``out`` and ``residual`` (which may be the same tensor) in that type or float32; bias float32 or
+    None. ``workspace``: see the C call (None will do)."""
+    n, k = w.shape
+    if a.shape[-1] != k:
+        raise ValueError("a and w must agree in their last dimension")
+    if k == 0:
+        raise ValueError("a and w hold no columns")
+    m = a.numel() // k
+    if m == 0:
+        return
+    dev = _current_device()
+    td, to = a.dtype, out.dtype
+    pa, lda = _rows(a, "a", k, td, dev)
+    wsb = 0 if workspace is None else workspace.numel()
+    pw = _dense(workspace, "workspace", wsb, torch.uint8, dev)
+    _check("ssd_matmul", LIB.ssd_matmul(
+        m, n, k, _code(td), pa, lda, _dense(w, "w", n * k, td, dev), _dense(bias, "bias", n, torch.float32, dev), act,
+        _dense(residual, "residual", m * n, to, dev), _code(to), _dense(out, "out", m * n, to, dev), pw, wsb,
+        _stream_on(stream, dev)))

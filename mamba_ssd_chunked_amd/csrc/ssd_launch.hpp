@@ -178,6 +178,19 @@ hipError_t launch_delta_steps(const Dims& d, int dtype, const DeltaArgs& a, hipS
 hipError_t launch_delta_chunks(const Dims& d, int dtype, const DeltaArgs& a, void* ws, hipStream_t st);
 size_t delta_workspace_bytes(const Dims& d, int dtype);
 
+// Matrix product with bias, activation and residual (k_matmul.hip).
+struct MatmulArgs {
+  int64_t M, N, K;
+  const void* a;
+  int64_t lda;  // elements between a's rows
+  const void* w;
+  const float* bias;     // [N] or null
+  int act;               // SSD_ACT_*
+  const void* residual;  // [M, N] in the output's type, or null; may be out
+  void* out;
+};
+hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& a, hipStream_t st);
+
 // Zero fill of a device buffer by a kernel (so that a captured graph holds no
 // memset node); bytes is a multiple of 16 and p 16-byte aligned.
 hipError_t launch_zero_fill(void* p, size_t bytes, hipStream_t st);

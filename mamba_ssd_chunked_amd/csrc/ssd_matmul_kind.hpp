@@ -34,7 +34,7 @@ constexpr MatmulKind kMatmulKind[kMatmulKinds] = {
     {256, 256, 1, 256, 1.7f, 11.3f, 9.58f},
 };
 
-inline int pick_matmul_kind(int64_t M, int64_t N, int64_t K, int64_t ncu) {
+inline int pick_matmul_kind(int64_t M, int64_t N, int64_t K, int64_t ncu, float slower = 1.f) {
   int best = 0;
   float least = 0.f;
   for (int i = 0; i < kMatmulKinds; ++i) {
@@ -43,7 +43,7 @@ inline int pick_matmul_kind(int64_t M, int64_t N, int64_t K, int64_t ncu) {
     const int64_t blocks = ((M + q.rows - 1) / q.rows) * ((N + q.cols - 1) / q.cols);
     const int64_t slots = ncu * q.per_cu;
     const float rounds = q.rows < 64 ? (float)blocks / (float)slots : (float)((blocks + slots - 1) / slots);
-    const float us = q.a + rounds * (q.b + q.c * (float)((K + q.round - 1) / q.round * q.round) / 1024.f);
+    const float us = q.a + rounds * (q.b + slower * q.c * (float)((K + q.round - 1) / q.round * q.round) / 1024.f);
     if (i == 0 || us < least) {
       best = i;
       least = us;

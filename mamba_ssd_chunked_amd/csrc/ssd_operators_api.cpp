@@ -1,5 +1,5 @@
-// C ABI of the operators that stand beside the SSD in a layer: the gated delta rule.
-// Argument validation (host only, before any launch) and dispatch to the HIP kernels.
+// C ABI of the operators that stand beside the SSD in a layer: the gated delta rule
+// and the product with an epilogue. Argument validation (host only, before any launch) and dispatch to the HIP kernels.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -17,6 +17,8 @@ namespace {
 size_t elem_bytes(int dtype) { return dtype == SSD_DTYPE_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+bool known_dtype(int dtype) { return dtype >= SSD_DTYPE_F32 && dtype <= SSD_DTYPE_BF16; }
 
 // Sequences that are taken one position after the other.
 bool delta_in_steps(const Dims& d) { return d.L <= 16; }
@@ -100,6 +102,27 @@ int ssd_delta_step(const ssd_shape* shape, int flags, const void* X, const void*
   if (empty) return SSD_OK;
   a.init = a.final_state = state;
   return hip_status(ssd::launch_delta_steps(d, shape->dtype, a, (hipStream_t)stream));
+}
+
+// No kernel needs a workspace: sums that are split over waves meet in LDS.
+size_t ssd_matmul_workspace_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+
+int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_t ld_a, const void* w,
+               const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace, size_t,
+               void* stream) {
+  constexpr int64_t kMost = (int64_t)1 << 26;  // rows: tile indexes and offsets in a tile's rows fit 32 bits
+  constexpr int64_t kMostLd = (int64_t)1 << 22;  // 256 rows are less than 2^32 bytes
+  if (M < 0 || N <= 0 || K <= 0 || M >= kMost || N >= kMost || M * N >= (int64_t)1 << 40) return SSD_E_SHAPE;
+  if (ld_a < K || ld_a >= kMostLd) return SSD_E_SHAPE;
+  if (!known_dtype(dtype) || (out_dtype != dtype && out_dtype != SSD_DTYPE_F32)) return SSD_E_UNSUPPORTED;
+  if (act < SSD_ACT_NONE || act > SSD_ACT_GELU_TANH) return SSD_E_UNSUPPORTED;
+  if (!a || !w || !out) return SSD_E_NULL;
+  if (!aligned_to(a, elem_bytes(dtype)) || !aligned_to(bias, 4)) return SSD_E_ALIGN;
+  const int rc = check_opt({w, residual, out, workspace});
+  if (rc) return rc;
+  if (M == 0) return SSD_OK;
+  ssd::MatmulArgs m{M, N, K, a, ld_a, w, bias, act, residual, out};
+  return hip_status(ssd::launch_matmul(dtype, out_dtype, m, (hipStream_t)stream));
 }
 
 }  // extern "C"

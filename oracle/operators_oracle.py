@@ -41,3 +41,20 @@ def delta(x, dt, A, k, q, beta, scale, state):
         y[:, t] = scale * np.matmul(s, q[:, t, :, :, None])[..., 0]
         ymag[:, t] = abs(scale) * np.matmul(mag, np.abs(q[:, t, :, :, None]))[..., 0]
     return y, s, ymag, mag
+
+
+def activation(v, act):
+    if act == "relu":
+        return np.maximum(v, 0.0)
+    if act == "relu2":
+        return np.maximum(v, 0.0) ** 2
+    if act == "silu":
+        return v * sigmoid(v)
+    if act == "sigmoid":
+        return sigmoid(v)
+    if act == "gelu":
+        from scipy.special import ndtr
+        return v * ndtr(v)
+    if act == "gelu_tanh":
+        return 0.5 * v * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3)))
+    return np.asarray(v, np.float64)

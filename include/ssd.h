@@ -515,6 +515,28 @@ int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_
 /* Workspace bytes ssd_matmul needs: 0. Host only. */
 size_t ssd_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
 
+/* From one block of a layer to the next: the norm after the block, its gate, the
+ * residual and its scale, and the norm before the next block, with the rows in 8 bits:
+ *   u = x / sqrt(mean(x^2) + eps) * post_weight
+ *   r = act(gate) u + res_scale residual
+ *   y = r / sqrt(mean(r^2) + eps) * weight, its codes and steps as ssd_add_norm's
+ * x [rows, cols] at row distance ld_x, dtype SSD_DTYPE_*; post_weight and weight [cols]
+ * fp32. gate in dtype (NULL: 1): row r reads row r / rows_per_gate of it, at distance
+ * ld_gate >= cols: a gate for each token (1), one for each sequence (its length), or one
+ * for all (rows); gate_act SSD_ACT_NONE, SSD_ACT_SILU or SSD_ACT_SIGMOID
+ * (SSD_E_UNSUPPORTED otherwise). residual and residual_out (r) [rows, cols] dense in
+ * res_dtype, dtype or SSD_DTYPE_F32 (either may be NULL: no residual, r not kept; they
+ * may be the same buffer). out, q and scale as in ssd_add_norm; out may be x itself
+ * (at ld_x == cols). With neither out nor q residual_out is required, and weight is
+ * not looked at. Everything is computed in fp32; r goes into the second norm before
+ * it is rounded to res_dtype. Rows whose squares leave fp32's range and rows of zeros
+ * as in ssd_add_norm. rows <= 2^31 - 1, cols <= 16384, rows_per_gate > 0, res_scale
+ * finite (SSD_E_SHAPE); rows == 0 is a valid empty problem. */
+int ssd_block_norm(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ld_x, const float* post_weight,
+                   const void* gate, int64_t ld_gate, int64_t rows_per_gate, int gate_act, const void* residual,
+                   float res_scale, int res_dtype, void* residual_out, const float* weight, float eps, void* out,
+                   int8_t* q, float* scale, void* stream);
+
 /* Static string for a status code. */
 const char* ssd_status_string(int status);
 

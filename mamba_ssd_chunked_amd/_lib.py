@@ -127,6 +127,8 @@ def _load() -> ctypes.CDLL:
                               ctypes.c_size_t, P],
         "ssd_matmul": [I64, I64, I64, ctypes.c_int, P, I64, P, P, ctypes.c_int, P, ctypes.c_int, P, P, ctypes.c_size_t,
                        P],
+        "ssd_block_norm": [I64, I64, ctypes.c_int, P, I64, P, P, I64, I64, ctypes.c_int, P, ctypes.c_float, ctypes.c_int,
+                           P, P, ctypes.c_float, P, P, P, P],
         "ssd_delta_step": [SP, ctypes.c_int, P, P, P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, P, P],
     }
     for name, args in sig.items():
@@ -160,7 +162,7 @@ EXPORTED = ("ssd_quantize_bc", "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state
             "ssd_conv_forward", "ssd_conv_decode_step", "ssd_add_norm", "ssd_gated_norm", "ssd_matmul_i8",
             "ssd_matmul_i8_workspace_bytes", "ssd_pack_weight_i8",
             "ssd_delta_forward", "ssd_delta_workspace_bytes", "ssd_delta_step",
-            "ssd_matmul", "ssd_matmul_workspace_bytes",
+            "ssd_matmul", "ssd_matmul_workspace_bytes", "ssd_block_norm",
             "ssd_status_string")
 
 
@@ -731,3 +733,31 @@ def ssd_matmul(a, w, bias, out, act=SSD_ACT_NONE, residual=None, workspace=None,
         m, n, k, _code(td), pa, lda, _dense(w, "w", n * k, td, dev), _dense(bias, "bias", n, torch.float32, dev), act,
         _dense(residual, "residual", m * n, to, dev), _code(to), _dense(out, "out", m * n, to, dev), pw, wsb,
         _stream_on(stream, dev)))
+
+
+def ssd_block_norm(x, post_weight, residual, residual_out, weight, eps, out=None, q=None, scale=None, gate=None,
+                   gate_act=SSD_ACT_NONE, rows_per_gate=1, res_scale=1.0, stream=None):
+    """u = RMSNorm of x's rows, r = act(gate) * u + res_scale * residual, and RMSNorm of r's rows
+    in ``out`` and as codes ``q`` with a step ``scale`` each. Row i reads row i // rows_per_gate of
+    ``gate``. ``x`` and ``gate`` may be column slices; ``residual`` and ``residual_out`` share a type,
+    x's or float32 (either may be None)."""
+    cols, td, n = x.shape[-1], x.dtype, x.numel()
+    if cols == 0:
+        raise ValueError("the rows hold no channels")
+    if n == 0:
+        return
+    dev = _current_device()
+    rows = n // cols
+    px, ldx = _rows(x, "x", cols, td, dev)
+    pg, ldg = None, 0
+    if gate is not None:
+        pg, ldg = _rows(gate, "gate", cols, td, dev)
+        if rows_per_gate <= 0 or gate.numel() // cols < -(-rows // rows_per_gate):
+            raise ValueError(f"{rows} rows need a gate for each {rows_per_gate}, got {tuple(gate.shape)}")
+    rt = td if residual is None and residual_out is None else (residual_out if residual is None else residual).dtype
+    _check("ssd_block_norm", LIB.ssd_block_norm(
+        rows, cols, _code(td), px, ldx, _dense(post_weight, "post_weight", cols, torch.float32, dev), pg, ldg,
+        rows_per_gate, gate_act, _dense(residual, "residual", n, rt, dev), res_scale, _code(rt),
+        _dense(residual_out, "residual_out", n, rt, dev), _dense(weight, "weight", cols, torch.float32, dev), eps,
+        _dense(out, "out", n, td, dev), _dense(q, "q", n, torch.int8, dev),
+        _dense(scale, "scale", rows, torch.float32, dev), _stream_on(stream, dev)))

@@ -19,7 +19,7 @@ OBJ_DIR = os.path.join(ROOT, "_build", "obj")
 
 HIP_SOURCES = ["k_modules.hip", "k_fused.hip", "k_fused_i8.hip", "k_chunked_i8.hip", "k_calib.hip",
                "k_decode.hip", "k_epilogue.hip", "ssd_noalloc.hip", "k_conv.hip", "k_conv_decode.hip", "k_norm.hip",
-               "k_matmul_i8.hip", "k_delta.hip", "k_delta_step.hip", "k_matmul.hip"]
+               "k_matmul_i8.hip", "k_delta.hip", "k_delta_step.hip", "k_matmul.hip", "k_block_norm.hip"]
 CPP_SOURCES = ["ssd_api.cpp", "ssd_layer_api.cpp", "ssd_operators_api.cpp"]
 
 ARCH = "gfx950"

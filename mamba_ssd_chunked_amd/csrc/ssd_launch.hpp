@@ -191,6 +191,28 @@ struct MatmulArgs {
 };
 hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& a, hipStream_t st);
 
+// Norms after and before a block, with its gate and the residual (k_block_norm.hip).
+struct BlockNormArgs {
+  int64_t rows;
+  int cols;
+  const void* x;
+  int64_t ld_x;
+  const float* post;
+  const void* gate;  // row r reads gate row r / per; null: 1
+  int64_t ld_gate;
+  int64_t per;
+  int act;  // SSD_ACT_NONE, SSD_ACT_SILU or SSD_ACT_SIGMOID
+  const void* residual;
+  float res_scale;
+  void* residual_out;
+  const float* weight;
+  float eps;
+  void* out;
+  int8_t* q;
+  float* scale;
+};
+hipError_t launch_block_norm(int dtype, int res_dtype, const BlockNormArgs& a, hipStream_t st);
+
 // Zero fill of a device buffer by a kernel (so that a captured graph holds no
 // memset node); bytes is a multiple of 16 and p 16-byte aligned.
 hipError_t launch_zero_fill(void* p, size_t bytes, hipStream_t st);

@@ -1,5 +1,5 @@
-// C ABI of the operators that stand beside the SSD in a layer: the gated delta rule
-// and the product with an epilogue. Argument validation (host only, before any launch) and dispatch to the HIP kernels.
+// C ABI of the operators that stand beside the SSD in a layer: the gated delta
+// rule, the product with an epilogue and the norms between two blocks. Argument validation (host only, before any launch) and dispatch to the HIP kernels.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -123,6 +123,37 @@ int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_
   if (M == 0) return SSD_OK;
   ssd::MatmulArgs m{M, N, K, a, ld_a, w, bias, act, residual, out};
   return hip_status(ssd::launch_matmul(dtype, out_dtype, m, (hipStream_t)stream));
+}
+
+int ssd_block_norm(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ld_x, const float* post_weight,
+                   const void* gate, int64_t ld_gate, int64_t rows_per_gate, int gate_act, const void* residual,
+                   float res_scale, int res_dtype, void* residual_out, const float* weight, float eps, void* out,
+                   int8_t* q, float* scale, void* stream) {
+  if (!known_dtype(dtype)) return SSD_E_UNSUPPORTED;
+  if (rows < 0 || rows > INT32_MAX || cols <= 0 || cols > 16384) return SSD_E_SHAPE;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || !std::isfinite(res_scale)) return SSD_E_SHAPE;
+  if (!x || !post_weight || (!out && !q && !residual_out)) return SSD_E_NULL;
+  if ((q == nullptr) != (scale == nullptr) || ((out || q) && !weight)) return SSD_E_NULL;
+  int64_t t;
+  if (ld_x < cols || !mul_ok(rows, ld_x, &t) || !mul_ok(t, 4, &t)) return SSD_E_SHAPE;
+  if (!aligned_to(x, elem_bytes(dtype)) || !aligned_to(scale, 4)) return SSD_E_ALIGN;
+  const int rc = check_opt({post_weight, weight, out, q});
+  if (rc) return rc;
+  if (gate) {
+    if (gate_act != SSD_ACT_NONE && gate_act != SSD_ACT_SILU && gate_act != SSD_ACT_SIGMOID) return SSD_E_UNSUPPORTED;
+    if (rows_per_gate <= 0 || ld_gate < cols || !mul_ok(rows, ld_gate, &t) || !mul_ok(t, 4, &t)) return SSD_E_SHAPE;
+    if (!aligned_to(gate, elem_bytes(dtype))) return SSD_E_ALIGN;
+  }
+  if (residual || residual_out) {
+    if (!known_dtype(res_dtype) || (res_dtype != dtype && res_dtype != SSD_DTYPE_F32)) return SSD_E_UNSUPPORTED;
+    if (!aligned16(residual) || !aligned16(residual_out)) return SSD_E_ALIGN;
+  }
+  if (rows == 0) return SSD_OK;
+  // a gate of more rows than there are is one for all of them
+  const int64_t per = gate ? (rows_per_gate < rows ? rows_per_gate : rows) : 1;
+  ssd::BlockNormArgs a{rows, (int)cols, x, ld_x, post_weight, gate, ld_gate, per, gate_act, residual, res_scale,
+                       residual_out, weight, eps, out, q, scale};
+  return hip_status(ssd::launch_block_norm(dtype, residual || residual_out ? res_dtype : dtype, a, (hipStream_t)stream));
 }
 
 }  // extern "C"

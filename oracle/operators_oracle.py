@@ -58,3 +58,15 @@ def activation(v, act):
     if act == "gelu_tanh":
         return 0.5 * v * (1.0 + np.tanh(np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3)))
     return np.asarray(v, np.float64)
+
+
+def rms(v, eps):
+    """1 / sqrt(mean(v^2) + eps) of rows, 0 where that is infinite."""
+    m = (v * v).mean(-1, keepdims=True) + eps
+    return np.where(m > 0, 1.0 / np.sqrt(np.where(m > 0, m, 1.0)), 0.0)
+
+
+def block_norm(x, post, gate, res, res_scale, weight, eps):
+    """r and y of a block's norms: x [rows, cols], gate and res [rows, cols] (1, 0 for none)."""
+    r = x * rms(x, eps) * post * gate + res_scale * res
+    return r, r * rms(r, eps) * weight

@@ -6,24 +6,26 @@
 //   Y = scale (diag(e^g) Q S^T + (Q K^T . e^{g_i - g_j}, j <= i) U),
 //   S' = e^{g_63} S + (diag(e^{g_63 - g}) U)^T K.
 //
-// Two launches. k_delta_prepare forms, for every chunk at once, what does not need
-// the state: keys and queries as matrix operands, T diag(b) and the weights of U in Y.
-// k_delta_scan goes through a head's chunks in order with the state in registers; a
-// wave owns 16 NC rows of S (columns here: S^T is [N, P]), which no other needs.
+// Three launches. For every chunk at once, k_delta_keys forms a group's keys and queries
+// as matrix operands, and k_delta_prepare a head's T diag(b) and the weights of U in Y,
+// none of which needs the state. k_delta_scan then goes through a head's chunks in order,
+// with the state in registers: a wave owns 16 rows of S, which no other needs.
 //
-// The products of the scan follow one another without a step through LDS: the
-// 16 x 16 result tiles hold, in lane i, rows 4 (i / 16) .. + 3 of column i % 16, and
-// two of them are an operand of 32 rows whose order of rows the other operand takes
-// on too. An operand's lane i thus has, of step s, the 8 positions
-// 32 s + 4 (i / 16) + (0..3) and 16 more than those ("fragments" below).
+// The scan's products follow one another without a step through LDS: the 16 x 16
+// result tiles hold, in lane i, rows 4 (i / 16) .. + 3 of column i % 16, and two of them
+// are an operand of 32 rows whose order of rows the other operand takes on too (columns
+// here are rows of S: S^T is [N, P]). An operand's lane i thus has, of step s, the 8
+// positions 32 s + 4 (i / 16) + (0..3) and 16 more than those ("fragments" below).
 //
 // Precision. The state is kept and returned in fp32, so that no operand of the
 // products that lead to it may be rounded to 16 bits. Each is taken as a sum of two
 // fp16 numbers (22 significant bits), after a power of two has brought the largest of
-// its column (or row, or matrix) to 2^8: what is below 2^-32 of that is lost. Keys and
+// its column (or row, or tile row) to 2^8: what is below 2^-32 of that is lost. Keys and
 // queries of 16-bit types are exact in one fp16 number in that way, fp32 ones in two.
 // Products of two lower parts (2^-22 of the rest) are left out. For Y alone, which is
-// rounded to 16 bits, fewer parts do: see kStateY, kNewY.
+// rounded to 16 bits, fewer parts do: see Parts.
+#include <type_traits>
+
 #include "ssd_delta.hpp"
 
 namespace ssd {
@@ -41,31 +43,56 @@ struct Parts {
 };
 
 // ---------------------------------------------------------------------------
-// workspace
+// workspace and LDS
 // ---------------------------------------------------------------------------
 constexpr int kFrag = 1024;  // bytes: 16 for each lane
 
 // Of each (batch, group, chunk): fragments of K and Q (4 tiles of 16 positions, KS
-// steps of 32 channels) and of K^T (NT tiles of 16 channels, 2 steps of 32 positions).
+// steps of 32 channels) and of K^T (NT tiles of 16 channels, 2 steps of 32 positions),
+// each row's factor, what undoes its scaling and makes it of length 1 (K's 64, Q's), and
+// the fp32 tiles of the lower triangles of K K^T (rows i, columns j of tile (i, j)) and of
+// Q K^T, transposed.
 template <int DT, int N>
 struct KeyPlan {
   static constexpr int KS = (N + 31) / 32, NT = N / 16, KP = Parts<DT>::kKeys;
-  static constexpr int kK = 0, kQ = 4 * KS * KP, kT = 8 * KS * KP, kFrags = kT + 2 * NT * KP;
+  static constexpr int kK = 0, kQ = 4 * KS * KP, kT = 8 * KS * KP, kTurned = 2 * NT * KP;
+  static constexpr int kFac = kT + kTurned, kKK = kFac + 1, kKQ = kKK + 10, kFrags = kKQ + 10;
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
-// Of each (batch, head, chunk): fragments of T diag(b) (6 that are not zero, two
-// parts), of Y's weights (6), then floats: for each position the factors of K S^T in R
-// (kFacK), of Q S^T in Y (kFacQ) and of U in S' (kFacU), the state's decay, the factors
-// that undo the scaling of T and of the weights, and the largest of kFacU.
+// Tile (i, j) of a lower triangle of 4 x 4, in rows.
+__device__ __forceinline__ constexpr int lower_tile_at(int i, int j) { return i * (i + 1) / 2 + j; }
+// Factors of a chunk of a head: for each position of K S^T in R (fac_k), of Q S^T in Y
+// (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling); the state's
+// decay over the chunk, the largest of fac_u without that, and what undoes the scaling
+// of each tile row of T and of Y's weights.
+struct Factors {
+  float fac_k[kC], fac_q[kC], fac_u[kC];
+  float decay, most, inv_t[4], inv_a[4];
+};
+// Of each (batch, head, chunk): fragments of T diag(b) (6
+// that are not zero, two parts), of Y's weights (6), and the factors.
 template <int DT>
 struct HeadPlan {
   static constexpr int kT = 0, kA = 12, kFac = 12 + 6 * Parts<DT>::kWeights, kFrags = kFac + 1;
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
-enum { kFacK = 0, kFacQ = kC, kFacU = 2 * kC, kDecay = 3 * kC, kInvT, kInvA, kMaxU };
+static_assert(sizeof(Factors) <= kFrag, "a fragment's room");
 
 // The fragment of tile row i and step s of a lower triangle of 4 x 4 tiles.
 __device__ __forceinline__ constexpr int lower_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
+
+// What a head's chunk is made of besides keys and queries, for each position. g: sums
+// of dt A log2(e), twice fp32's bits, as their differences count; cols: the decay from
+// the position to the end of its 16, times K's factor; first[j]: the decay to the
+// position from the end of the 16 positions j; rows[j]: the same times beta and K's
+// factor, rows[3] without it.
+struct Gates {
+  float g[kC], g_low[kC], beta[kC], cols[kC], rows[4][kC], first[3][kC], fk[kC], fq[kC];
+  Factors f;
+};
+// L's four diagonal tiles, and then their inverses, with rows 20 floats apart and tiles
+// 4 banks.
+constexpr int kDiagRow = 20, kDiag = 16 * kDiagRow + 4;
 
 // ---------------------------------------------------------------------------
 // scaling and parts
@@ -83,18 +110,40 @@ struct Scale {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-// Eight values, times a power of two, as fp16 numbers, and what that leaves of them
-// as eight more.
-__device__ __forceinline__ void split8(const float (&x)[8], float by, v8h& hi, v8h& lo) {
+// Eight values, four times a factor each, as fp16 numbers, and what that leaves of them as eight
+// more. (The empty asm keeps the compiler from forming the first ones twice, packed and
+// one by one.)
+__device__ __forceinline__ void split8(const float (&x)[8], float by0, float by4, v8h& hi, v8h& lo) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) hi[e] = (_Float16)(x[e] * by);
+  for (int e = 0; e < 8; e += 2) {
+    const float by = e < 4 ? by0 : by4;
+    uint32_t w = pack2<DT_F16>(x[e] * by, x[e + 1] * by);
+    asm("" : "+v"(w));
+    const v2h h = __builtin_bit_cast(v2h, w);
+    hi[e] = h[0];
+    hi[e + 1] = h[1];
+    lo[e] = (_Float16)fmaf(x[e], by, -(float)h[0]);
+    lo[e + 1] = (_Float16)fmaf(x[e + 1], by, -(float)h[1]);
+  }
+}
+// The same of values as they are; `one` is a 1 that the compiler does not know (x 1 - hi,
+// rounded to fp16, is one operation).
+__device__ __forceinline__ void split8_unscaled(const float (&x)[8], float one, v8h& hi, v8h& lo) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) lo[e] = (_Float16)fmaf(x[e], by, -(float)hi[e]);
+  for (int e = 0; e < 8; e += 2) {
+    uint32_t w = pack2<DT_F16>(x[e], x[e + 1]);
+    asm("" : "+v"(w));
+    const v2h h = __builtin_bit_cast(v2h, w);
+    hi[e] = h[0];
+    hi[e + 1] = h[1];
+    lo[e] = (_Float16)fmaf(x[e], one, -(float)h[0]);
+    lo[e + 1] = (_Float16)fmaf(x[e + 1], one, -(float)h[1]);
+  }
 }
 // Rows 4 (lane / 16) .. of two result tiles, as an operand.
-__device__ __forceinline__ void split_tiles(v4f a, v4f b, float by, v8h& hi, v8h& lo) {
+__device__ __forceinline__ void split_tiles(v4f a, v4f b, float by_a, float by_b, v8h& hi, v8h& lo) {
   const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  split8(x, by, hi, lo);
+  split8(x, by_a, by_b, hi, lo);
 }
 // 2^x
 __device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -102,362 +151,30 @@ __device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x
 __device__ __forceinline__ v4f mma16(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-// 16 x 16 x 16 in fp32: a holds rows (lane % 16) of the left matrix, columns 4 (lane / 16)
-// + (0..3); b a result tile.
-__device__ __forceinline__ v4f mma32(v4f a, v4f b, v4f c) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-  return c;
-}
-
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-__device__ __forceinline__ float max4(v4f v) { return fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))); }
-
-// ---------------------------------------------------------------------------
-// preparation
-// ---------------------------------------------------------------------------
-// A workgroup of four waves takes a chunk of a group's keys and queries, and `heads`
-// of the group's heads, a wave one at a time.
-struct PrepareWave {
-  static constexpr int kDiagRow = 20, kDiag = 16 * kDiagRow + 4;  // floats; the blocks start 4 banks apart
-  float g[kC], g_low[kC];  // sums of dt A log2(e): twice fp32's bits, as their differences count
-  float beta[kC], cols[kC], rows[4][kC], first[3][kC];
-  float diag[4 * kDiag];
-};
-
-template <int DT, int N>
-__global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, char* ws_keys, char* ws_heads, int64_t L, int H,
-                                                     int G, int hpg, int chunks, int blocks, int heads, int64_t total) {
-  typedef KeyPlan<DT, N> KP_;
-  typedef HeadPlan<DT> HP_;
-  constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
-  // K's fragments, then Q's; once the tiles are made, what a wave holds of its head
-  constexpr int kFragBytes = 8 * KS * KP * kFrag, kWaveBytes = 4 * sizeof(PrepareWave);
-  __shared__ __attribute__((aligned(16))) char frags[kFragBytes > kWaveBytes ? kFragBytes : kWaveBytes];
-  // tiles of K K^T and K Q^T: of tile row i, column j at i (i + 1) / 2 + j
-  __shared__ __attribute__((aligned(16))) float4 lds_kk[10][kWave], lds_kq[10][kWave];
-  __shared__ __attribute__((aligned(16))) float lds_fk[kC], lds_fq[kC];
-  const int tid = threadIdx.x, lane = lane_id(), wv = wave_id(), sub = lane >> 4, col = lane & 15;
-
-  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
-    const int hb = (int)(item % blocks);
-    const int64_t bgc = item / blocks;  // (b G + g) chunks + chunk
-    const int ck = (int)(bgc % chunks);
-    const int64_t bg = bgc / chunks, b = bg / G;
-    const int g = (int)(bg % G);
-    const int64_t pos0 = (int64_t)ck * kC;
-    char* const out_keys = ws_keys + bgc * KP_::kBytes;
-
-    // Rows of K and Q: four threads a row, a step's 32 channels each.
-    {
-      const int row = tid >> 2, s = tid & 3;
-      const bool live = s < KS && pos0 + row < L;
+__device__ __forceinline__ float max4(float m, v4f v) {
+  m = fmaxf(fmaxf(m, fabsf(v[0])), fabsf(v[1]));
+  return fmaxf(fmaxf(m, fabsf(v[2])), fabsf(v[3]));
+}
+// The largest magnitude of N tiles: a chain of maxima for each row of a tile.
+template <int N>
+__device__ __forceinline__ float tiles_max(const v4f (&t)[N]) {
+  v4f m = (v4f)(0.f);
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const void* const src = which ? a.C : a.B;
-        constexpr int E = N < 32 ? N : 32;
-        float x[32];
+  for (int n = 0; n + 1 < N; n += 2)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
-        if (live) {
-          const int64_t at = ((b * L + pos0 + row) * G + g) * N + s * 32;
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(fmaxf(m[e], fabsf(t[n][e])), fabsf(t[n + 1][e]));
+  if constexpr (N % 2) {
 #pragma unroll
-          for (int e = 0; e < E; e += 8) {
-            float t[8];
-            ld8_f<DT>(src, at + e, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[e + i] = t[i];
-          }
-        }
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(x[e]));
-        m = fmaxf(m, __shfl_xor(m, 1));
-        m = fmaxf(m, __shfl_xor(m, 2));
-        const Scale sc(m);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          x[e] *= sc.by;
-          ss = fmaf(x[e], x[e], ss);
-        }
-        ss += __shfl_xor(ss, 1);
-        ss += __shfl_xor(ss, 2);
-        if (s == 0) {
-          float f = sc.inv;
-          if (a.unit) {
-            const float eps = a.eps * sc.by * sc.by;
-            ss += eps;
-            // a row of zeros without eps stays zeros; next to a far larger eps the row counts for nothing
-            f = eps > 0x1p126f ? sc.inv * rsqrtf(a.eps) : ss > 0.f ? rsqrtf(ss) : 0.f;
-          }
-          if (which) lds_fq[row] = f * a.scale;
-          else lds_fk[row] = f;
-        }
-        if (s < KS) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float t[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[e] = x[4 * q + e];
-              t[4 + e] = x[16 + 4 * q + e];
-            }
-            v8h hi, lo;
-            split8(t, 1.f, hi, lo);
-            const int at = ((which * KP * 4 + (row >> 4)) * KS + s) * kFrag + (q * 16 + (row & 15)) * 16;
-            *(v8h*)(frags + at) = hi;
-            if (hb == 0) *(v8h*)(out_keys + at) = hi;
-            if constexpr (KP == 2) {
-              constexpr int kLo = 4 * KS * kFrag;
-              *(v8h*)(frags + at + kLo) = lo;
-              if (hb == 0) *(v8h*)(out_keys + at + kLo) = lo;
-            }
-          }
-        }
-      }
-    }
-    __syncthreads();
-
-    if (hb == 0) {
-      for (int f = wv; f < 2 * NT * KP; f += 4) {  // K^T: channel 16 nt + col, positions of step s
-        const int part = f / (2 * NT), nt = f / 2 % NT, s = f & 1, n = 16 * nt + col;
-        const char* const from = frags + part * 4 * KS * kFrag + (n >> 5) * kFrag + ((n & 15) >> 2) * 256 + ((n & 3) + ((n >> 4) & 1) * 4) * 2;
-        v8h v;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int p = 4 * sub + (e & 3);  // of tile 2 s + e / 4
-          v[e] = *(const _Float16*)(from + (2 * s + (e >> 2)) * KS * kFrag + p * 16);
-        }
-        *(v8h*)(out_keys + (KP_::kT + f) * kFrag + lane * 16) = v;
-      }
-    }
-    // tiles of K K^T (rows i, columns j) and K Q^T (rows j, columns i), j <= i
-    auto frag = [&](int which, int part, int tile, int s) {
-      return *(const v8h*)(frags + (((which * KP + part) * 4 + tile) * KS + s) * kFrag + lane * 16);
-    };
-    for (int t = wv; t < 20; t += 4) {
-      const int which = t >= 10, u = which ? t - 10 : t;
-      const int i = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, j = u - i * (i + 1) / 2;
-      const int left = which ? j : i, right = which ? i : j;
-      v4f acc = (v4f)(0.f);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        acc = mma16(frag(0, 0, left, s), frag(which, 0, right, s), acc);
-        if constexpr (KP == 2) {
-          acc = mma16(frag(0, 0, left, s), frag(which, 1, right, s), acc);
-          acc = mma16(frag(0, 1, left, s), frag(which, 0, right, s), acc);
-        }
-      }
-      (which ? lds_kq : lds_kk)[u][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    }
-    __syncthreads();
-
-    PrepareWave& w = ((PrepareWave*)frags)[wv];
-    const int last = min(hpg, (hb + 1) * heads);
-    for (int hi_ = hb * heads + wv; hi_ < last; hi_ += 4) {
-      const int h = g * hpg + hi_;
-      char* const out = ws_heads + ((b * H + h) * (int64_t)chunks + ck) * HP_::kBytes;
-      float* const fac = (float*)(out + HP_::kFac * kFrag);
-      // a lane for each position; behind the end nothing decays and nothing is written
-      {
-        const int64_t pos = b * L + pos0 + lane;
-        const bool live = pos0 + lane < L;
-        const float dt = live ? ld_f<DT>(a.dt, pos * H + h) : 0.f;
-        const float beta = live ? delta_beta<DT>(a, pos, h) : 0.f;
-        double gs = (double)dt * ((double)a.A[h] * 1.4426950408889634);
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) {
-          const double up = __shfl_up(gs, o);
-          if (lane >= o) gs += up;
-        }
-        const double end = __shfl(gs, lane | 15), total_g = __shfl(gs, kC - 1);
-        const float fk = lds_fk[lane], fq = lds_fq[lane], eg = exp2((float)gs);
-        const float fu = exp2((float)(total_g - gs)) * fk;
-        w.g[lane] = (float)gs;
-        w.g_low[lane] = (float)(gs - (double)(float)gs);
-        w.beta[lane] = beta;
-        w.cols[lane] = exp2((float)(end - gs)) * fk;  // from the position to the end of its 16
-        w.rows[3][lane] = beta * fk;
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {  // from the end of the 16 positions q
-          const float first = exp2((float)fmin(gs - __shfl(gs, 16 * q + 15), 0.0));
-          w.first[q][lane] = first;
-          w.rows[q][lane] = beta * fk * first;
-        }
-        fac[kFacK + lane] = eg * fk;
-        fac[kFacQ + lane] = eg * fq;
-        fac[kFacU + lane] = fu;
-        float most = fu;
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) most = fmaxf(most, __shfl_xor(most, o));
-        if (lane == 0) {
-          fac[kDecay] = exp2((float)total_g);
-          fac[kMaxU] = most;
-        }
-      }
-      wave_sync();
-
-      // L: tiles below the diagonal stay in registers, the diagonal ones go to LDS
-      v4f l[4][4], x[4][4];  // tile row, tile column
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          const float4 kk = lds_kk[i * (i + 1) / 2 + j][lane], rf = *(const float4*)&w.rows[j < i ? j : 3][16 * i + 4 * sub];
-          const float kv[4] = {kk.x, kk.y, kk.z, kk.w}, rv[4] = {rf.x, rf.y, rf.z, rf.w};
-          if (j < i) {
-            const float c = w.cols[16 * j + col];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) l[i][j][e] = rv[e] * c * kv[e];
-          } else {
-            const float gj = w.g[16 * i + col], gl = w.g_low[16 * i + col], c = lds_fk[16 * i + col];
-            const v4f gi = *(const v4f*)&w.g[16 * i + 4 * sub], gil = *(const v4f*)&w.g_low[16 * i + 4 * sub];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float gamma = exp2(fminf((gi[e] - gj) + (gil[e] - gl), 0.f));
-              w.diag[i * PrepareWave::kDiag + (4 * sub + e) * PrepareWave::kDiagRow + col] =
-                  col < 4 * sub + e ? rv[e] * c * gamma * kv[e] : 0.f;
-            }
-          }
-        }
-      wave_sync();
-      // inverses of the diagonal blocks: 16 lanes a block, each a column, from the top
-      {
-        const float* const d = w.diag + sub * PrepareWave::kDiag;
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float v = i == col ? 1.f : 0.f;
-#pragma unroll
-          for (int k = 0; k < i; ++k) v = fmaf(-d[i * PrepareWave::kDiagRow + k], t[k], v);
-          t[i] = v;
-        }
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w.diag[sub * PrepareWave::kDiag + i * PrepareWave::kDiagRow + col] = t[i];
-      }
-      wave_sync();
-      v4f dc[4];  // the blocks' own tiles
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* const d = w.diag + i * PrepareWave::kDiag;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dc[i][e] = d[(4 * sub + e) * PrepareWave::kDiagRow + col];
-        const float4 v = *(const float4*)(d + col * PrepareWave::kDiagRow + 4 * sub);
-        x[i][i] = (v4f){v.x, v.y, v.z, v.w};
-      }
-      // x: transposed tiles of T, from T_ij = -(sum_{j<k<=i} T_ik L_kj) T_jj
-#pragma unroll
-      for (int off = 1; off < 4; ++off)
-#pragma unroll
-        for (int j = 0; j + off < 4; ++j) {
-          const int i = j + off;
-          v4f acc = (v4f)(0.f);
-#pragma unroll
-          for (int k = j + 1; k <= i; ++k) acc = mma32(l[k][j], x[i][k], acc);
-          x[i][j] = -mma32(dc[j], acc, (v4f)(0.f));
-        }
-
-      // two tiles of a row as a fragment
-      auto write = [&](const v4f (&m)[4][4], float by, int first, int parts) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int s = 0; s <= i / 2; ++s) {
-            v8h hi, lo;
-            split_tiles(m[i][2 * s], 2 * s + 1 <= i ? m[i][2 * s + 1 <= i ? 2 * s + 1 : 0] : (v4f)(0.f), by, hi, lo);
-            *(v8h*)(out + (first + lower_frag(i, s)) * kFrag + lane * 16) = hi;
-            if (parts == 2) *(v8h*)(out + (first + 6 + lower_frag(i, s)) * kFrag + lane * 16) = lo;
-          }
-      };
-      auto largest = [&](const v4f (&m)[4][4]) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j <= i; ++j) v = fmaxf(v, max4(m[i][j]));
-#pragma unroll
-        for (int o = 1; o < kWave; o *= 2) v = fmaxf(v, __shfl_xor(v, o));
-        return v;
-      };
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          const float4 v = *(const float4*)&w.beta[16 * j + 4 * sub];
-          x[i][j] *= (v4f){v.x, v.y, v.z, v.w};
-        }
-      const Scale st(largest(x));
-      write(x, st.by, HP_::kT, 2);
-      // Y's weights, transposed too: rows j, columns i
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j <= i; ++j) {
-          const float4 kq = lds_kq[i * (i + 1) / 2 + j][lane];
-          const float kv[4] = {kq.x, kq.y, kq.z, kq.w}, fq = lds_fq[16 * i + col];
-          if (j < i) {
-            const float4 cf = *(const float4*)&w.cols[16 * j + 4 * sub];
-            const float cv[4] = {cf.x, cf.y, cf.z, cf.w}, r = fq * w.first[j][16 * i + col];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][j][e] = r * cv[e] * kv[e];
-          } else {
-            const float gi = w.g[16 * i + col], gil = w.g_low[16 * i + col];
-            const v4f gj = *(const v4f*)&w.g[16 * i + 4 * sub], gl = *(const v4f*)&w.g_low[16 * i + 4 * sub];
-            const v4f cv = *(const v4f*)&lds_fk[16 * i + 4 * sub];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float gamma = exp2(fminf((gi - gj[e]) + (gil - gl[e]), 0.f));
-              x[i][j][e] = 4 * sub + e <= col ? fq * cv[e] * gamma * kv[e] : 0.f;
-            }
-          }
-        }
-      const Scale sa(largest(x));
-      write(x, sa.by, HP_::kA, AP);
-      if (lane == 0) {
-        fac[kInvT] = st.inv;
-        fac[kInvA] = sa.inv;
-      }
-      wave_sync();  // the next head's values overwrite this one's
-    }
-    __syncthreads();
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], fabsf(t[N - 1][e]));
   }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-
-// ---------------------------------------------------------------------------
-// scan
-// ---------------------------------------------------------------------------
-// NC consecutive values of a row.
-template <int DT, int NC>
-__device__ __forceinline__ void load_cols(const char* p, float (&v)[NC]) {
-  if constexpr (NC == 1) {
-    v[0] = ld_f<DT>(p, 0);
-  } else if constexpr (DT == DT_F32) {
-    const float2 t = *(const float2*)p;
-    v[0] = t.x; v[1] = t.y;
-  } else {
-    const uint32_t t = *(const uint32_t*)p;
-    if constexpr (DT == DT_BF16) {
-      v[0] = __uint_as_float(t << 16); v[1] = __uint_as_float(t & 0xffff0000u);
-    } else {
-      const v2h h = __builtin_bit_cast(v2h, t);
-      v[0] = (float)h[0]; v[1] = (float)h[1];
-    }
-  }
-}
-template <int DT, int NC>
-__device__ __forceinline__ void store_cols(char* p, const float (&v)[NC]) {
-  if constexpr (NC == 1) *(typename Store<DT>::T*)p = to_store<DT>(v[0]);
-  else if constexpr (DT == DT_F32) *(float2*)p = make_float2(v[0], v[1]);
-  else *(uint32_t*)p = pack2<DT>(v[0], v[1]);
-}
-
 // The largest of a column, of which a lane has m of its 4 rows in each tile.
 __device__ __forceinline__ float column_max(float m) {
   const uint32_t b = __float_as_uint(m);
@@ -466,331 +183,786 @@ __device__ __forceinline__ float column_max(float m) {
   const auto q = __builtin_amdgcn_permlane32_swap(c, c, false, false);
   return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true)));
+}
+// The largest of a wave's values, none of them negative.
+__device__ __forceinline__ float wave_most(float v) {
+  return column_max(dpp_max<0x140>(dpp_max<0x141>(dpp_max<0x4E>(dpp_max<0xB1>(v)))));
+}
 
 // 16 bytes per lane from global memory straight into LDS: lane i's bytes land at l + 16 i.
 __device__ __forceinline__ void copy_frag(const char* g, char* l) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) char*)g,
                                    (__attribute__((address_space(3))) void*)l, 16, 0, 0);
 }
+// Fragments f, f + n, ... of `count`.
+template <int COUNT, int WAVES>
+__device__ __forceinline__ void copy_frags(const char* g, char* l, int wave) {
+  const char* const from = g + lane_id() * 16;
+#pragma unroll
+  for (int f = 0; f < COUNT; f += WAVES)
+    if (COUNT % WAVES == 0 || f + wave < COUNT) copy_frag(from + (f + wave) * kFrag, l + (f + wave) * kFrag);
+}
+// This wave's memory operations are done but for the newest BEHIND (64: whatever), and
+// its LDS operations; behind the barrier all waves' are, and what was read is free.
+template <int BEHIND>
+__device__ __forceinline__ void meet() {
+  constexpr int n = BEHIND < 63 ? BEHIND : 63;
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | ((n >> 4) << 14));  // vmcnt, lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
-// A workgroup of W waves takes W * 16 NC rows of a head's state. The chunk's fragments
-// come through LDS in two halves, K and Q (phase 1), and the rest (phase 2): the copies
-// of the next chunk's half are on their way while the other half is used, with one
-// barrier in between.
-template <int DT, int N, int NC, int W>
-__global__ __launch_bounds__(64 * W) void k_delta_scan(DeltaArgs a, const char* ws_keys, const char* ws_heads, int64_t L,
-                                                     int H, int G, int hpg, int P, int chunks) {
+// ---------------------------------------------------------------------------
+// keys and queries
+// ---------------------------------------------------------------------------
+// A tile of K K^T (rows of tile row i, columns j) or of K Q^T (rows j, columns i), from
+// fragments of K and Q.
+template <int DT, int N>
+__device__ __forceinline__ v4f key_tile(const char* frags, bool queries, int i, int j) {
   typedef KeyPlan<DT, N> KP_;
-  typedef HeadPlan<DT> HP_;
-  constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
-  constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
-  constexpr int kFirst = KP_::kT, kTurned = KP_::kFrags - KP_::kT;  // K and Q; K^T
-  __shared__ __attribute__((aligned(1024))) char buf1[kFirst * kFrag];
-  __shared__ __attribute__((aligned(1024))) char buf2[(kTurned + HP_::kFrags) * kFrag];
-  const int lane = lane_id(), wv = wave_id(), sub = lane >> 4, col = lane & 15;
-  const int slices = P / (16 * NC * W);
-  const int64_t unit = blockIdx.x / slices, b = unit / H;
-  const int h = (int)(unit % H), g = h / hpg;
-  const int p0 = ((int)(blockIdx.x % slices) * W + wv) * 16 * NC + NC * col;  // the lane's columns: p0 .. p0 + NC - 1
-  const char* keys = ws_keys + (b * G + g) * (int64_t)chunks * KP_::kBytes + lane * 16;
-  const char* head = ws_heads + unit * (int64_t)chunks * HP_::kBytes + lane * 16;
-
-  auto copy1 = [&](const char* k) {
+  constexpr int KS = KP_::KS, KP = KP_::KP;
+  const char* const left = frags + ((queries ? j : i) * KS + KP_::kK) * kFrag + lane_id() * 16;
+  const char* const right = frags + (queries ? i * KS + KP_::kQ : j * KS + KP_::kK) * kFrag + lane_id() * 16;
+  constexpr int kLo = 4 * KS * kFrag;
+  v4f acc = (v4f)(0.f);
 #pragma unroll
-    for (int f = 0; f < kFirst; f += W)
-      if (kFirst % W == 0 || f + wv < kFirst) copy_frag(k + (f + wv) * kFrag, buf1 + (f + wv) * kFrag);
-  };
-  auto copy2 = [&](const char* k, const char* hd) {
-#pragma unroll
-    for (int f = 0; f < kTurned; f += W)
-      if (kTurned % W == 0 || f + wv < kTurned) copy_frag(k + (kFirst + f + wv) * kFrag, buf2 + (f + wv) * kFrag);
-#pragma unroll
-    for (int f = 0; f < HP_::kFrags; f += W)
-      if (HP_::kFrags % W == 0 || f + wv < HP_::kFrags)
-        copy_frag(hd + (f + wv) * kFrag, buf2 + (kTurned + f + wv) * kFrag);
-  };
-  // this wave's copies have arrived; behind the barrier all have, and what was read before it is free
-  auto meet = [&]() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  auto key = [&](int f) { return *(const v8h*)(buf1 + f * kFrag + lane * 16); };
-  auto turned = [&](int f) { return *(const v8h*)(buf2 + f * kFrag + lane * 16); };
-  auto weight = [&](int f) { return *(const v8h*)(buf2 + (kTurned + f) * kFrag + lane * 16); };
-  const float* const fac = (const float*)(buf2 + (kTurned + HP_::kFac) * kFrag);
-
-  copy1(keys);
-  copy2(keys, head);
-  // Rows of X and Y: a uniform address for each of a chunk's, and the lane's place in
-  // it (64 rows are less than 2^32 bytes). Behind the end of the sequence the last row
-  // stands in: what it meets in T is zero.
-  constexpr int kE = sizeof(typename Store<DT>::T);
-  const uint32_t step = (uint32_t)H * P * kE, place = 4 * sub * step + p0 * kE;
-  const char* x_at = (const char*)a.X + (b * L * H + h) * P * kE;
-  char* y_at = (char*)a.Y + (b * L * H + h) * P * kE;
-  float v[4][4][NC];
-  auto load_values = [&](int n) {
-    if (n >= kC) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) load_cols<DT, NC>(x_at + (uint64_t)(16 * i + e) * step + place, v[i][e]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          load_cols<DT, NC>(x_at + (min(16 * i + 4 * sub + e, n - 1) * step + p0 * kE), v[i][e]);
+  for (int s = 0; s < KS; ++s) {
+    const v8h a = *(const v8h*)(left + s * kFrag), b = *(const v8h*)(right + s * kFrag);
+    acc = mma16(a, b, acc);
+    if constexpr (KP == 2) {
+      acc = mma16(a, *(const v8h*)(right + s * kFrag + kLo), acc);
+      acc = mma16(*(const v8h*)(left + s * kFrag + kLo), b, acc);
     }
-    x_at += (uint64_t)kC * step;
-  };
-  load_values((int)min(L, (int64_t)kC));
-  v4f s[NC][NT];
-  // The state is held times a power of two, one for each of its rows: 1 / inv_s.
-  float inv_s[NC];
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    float m = 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      s[c][n] = a.init ? *(const v4f*)(a.init + (unit * P + p0 + c) * (int64_t)N + 16 * n + 4 * sub) : (v4f)(0.f);
-      m = fmaxf(m, max4(s[c][n]));
-    }
-    const Scale sc(column_max(m));
-    inv_s[c] = sc.inv;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) s[c][n] *= sc.by;
   }
-  meet();
+  return acc;
+}
 
-  float one = 1.f;  // not known to be it: x 1 - hi, rounded to fp16, is one operation
-  asm volatile("" : "+v"(one));
-  for (int ck = 0; ck < chunks; ++ck) {
-    const bool more = ck + 1 < chunks;
-    const int left = (int)min(L - (int64_t)ck * kC, (int64_t)kC);  // positions of this chunk
-    keys += KP_::kBytes;
-    head += HP_::kBytes;
-    // phase 1: K S^T and Q S^T
-    v4f ks[NC][4], qs[NC][4];
+// A workgroup of four waves takes a chunk of a group, four threads a row, a step's 32
+// channels each.
+template <int DT, int N>
+__global__ __launch_bounds__(256) void k_delta_keys(DeltaArgs a, char* ws, int64_t L, int G, int chunks, int64_t total) {
+  typedef KeyPlan<DT, N> KP_;
+  constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, E = N < 32 ? N : 32;
+  __shared__ __attribute__((aligned(16))) char frags[8 * KS * KP * kFrag];  // K's, Q's
+  const int tid = threadIdx.x, lane = lane_id(), sub = lane >> 4, col = lane & 15;
+  const int row = tid >> 2, s = tid & 3;
+  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    const int ck = (int)(item % chunks);
+    const int64_t bg = item / chunks, b = bg / G, pos0 = (int64_t)ck * kC;
+    const int g = (int)(bg % G);
+    char* const out = ws + item * KP_::kBytes;
+    const bool live = s < KS && pos0 + row < L;  // rows behind the end are zeros
+    float x[2][32];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int which = 0; which < 2; ++which) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ks[c][i] = qs[c][i] = (v4f)(0.f);
+      for (int e = 0; e < 32; ++e) x[which][e] = 0.f;
+      if (live) {
+        const int64_t at = ((b * L + pos0 + row) * G + g) * N + s * 32;
+#pragma unroll
+        for (int e = 0; e < E; e += 8) {
+          float t[8];
+          ld8_f<DT>(which ? a.C : a.B, at + e, t);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[which][e + i] = t[i];
+        }
+      }
     }
 #pragma unroll
-    for (int t = 0; t < KS; ++t) {
-      v8h hi[NC], lo[NC];
+    for (int which = 0; which < 2; ++which) {
+      float(&v)[32] = x[which];
+      float m = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        split_tiles(s[c][2 * t], 2 * t + 1 < NT ? s[c][2 * t + 1 < NT ? 2 * t + 1 : 0] : (v4f)(0.f), one, hi[c], lo[c]);
+      for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(v[e]));
+      m = dpp_max<0x4E>(dpp_max<0xB1>(m));
+      const Scale sc(m);
+      float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v8h k = key(KP_::kK + i * KS + t), q = key(KP_::kQ + i * KS + t);
+      for (int e = 0; e < 32; ++e) {
+        v[e] *= sc.by;
+        ss = fmaf(v[e], v[e], ss);
+      }
+      ss = group_sum<4>(ss);
+      if (s == 0) {
+        float f = sc.inv;
+        if (a.unit) {
+          const float eps = a.eps * sc.by * sc.by;
+          ss += eps;
+          // a row of zeros without eps stays zeros; next to a far larger eps the row counts for nothing
+          f = eps > 0x1p126f ? sc.inv * rsqrtf(a.eps) : ss > 0.f ? rsqrtf(ss) : 0.f;
+        }
+        ((float*)(out + KP_::kFac * kFrag))[which * kC + row] = which ? f * a.scale : f;
+      }
+      if (s < KS) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          ks[c][i] = mma16(k, hi[c], ks[c][i]);
-          qs[c][i] = mma16(q, hi[c], qs[c][i]);
-          ks[c][i] = mma16(k, lo[c], ks[c][i]);
-          if constexpr (SY == 2) qs[c][i] = mma16(q, lo[c], qs[c][i]);
+        for (int q = 0; q < 4; ++q) {
+          float t[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            t[e] = v[4 * q + e];
+            t[4 + e] = v[16 + 4 * q + e];
+          }
+          v8h hi, lo;
+          split8(t, 1.f, 1.f, hi, lo);
+          const int at = ((which ? KP_::kQ : KP_::kK) + (row >> 4) * KS + s) * kFrag + (q * 16 + (row & 15)) * 16;
+          *(v8h*)(out + at) = hi;
+          *(v8h*)(frags + at) = hi;
           if constexpr (KP == 2) {
-            ks[c][i] = mma16(key(KP_::kK + (4 + i) * KS + t), hi[c], ks[c][i]);
-            qs[c][i] = mma16(key(KP_::kQ + (4 + i) * KS + t), hi[c], qs[c][i]);
+            constexpr int kLo = 4 * KS * kFrag;
+            *(v8h*)(out + at + kLo) = lo;
+            *(v8h*)(frags + at + kLo) = lo;
           }
         }
       }
     }
-    meet();
-    if (more) copy1(keys);
-
-    // phase 2: U = T diag(b) (V - e^g K S^T), times 1 / inv_u
-    v4f u[NC][4];
-    float inv_u[NC], max_u[NC];
-    {
-      float by[NC];
+    __syncthreads();
+    for (int f = wave_id(); f < 2 * NT * KP; f += 4) {  // K^T: channel 16 nt + col, positions of step t
+      const int part = f / (2 * NT), nt = f / 2 % NT, t = f & 1, n = 16 * nt + col;
+      const char* const from = frags + part * 4 * KS * kFrag + (n >> 5) * kFrag + ((n & 15) >> 2) * 256 +
+                               ((n & 3) + ((n >> 4) & 1) * 4) * 2;
+      v8h v;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const v4f f = *(const v4f*)(fac + kFacK + 16 * i + 4 * sub);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) ks[c][i][e] = fmaf(-f[e] * inv_s[c], ks[c][i][e], v[i][e][c]);
-          m = fmaxf(m, max4(ks[c][i]));
-          u[c][i] = (v4f)(0.f);
-        }
-        const Scale sc(column_max(m));
-        by[c] = sc.by;
-        inv_u[c] = sc.inv * fac[kInvT];
+      for (int e = 0; e < 8; ++e) {
+        const int p = 4 * sub + (e & 3);  // of tile 2 t + e / 4
+        v[e] = *(const _Float16*)(from + (2 * t + (e >> 2)) * KS * kFrag + p * 16);
       }
-      if (more) load_values((int)min(L - (int64_t)(ck + 1) * kC, (int64_t)kC));
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v8h hi[NC], lo[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) split_tiles(ks[c][2 * t], ks[c][2 * t + 1], by[c], hi[c], lo[c]);
-#pragma unroll
-        for (int i = 2 * t; i < 4; ++i) {
-          const v8h w = weight(HP_::kT + lower_frag(i, t)), wl = weight(HP_::kT + 6 + lower_frag(i, t));
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            u[c][i] = mma16(w, hi[c], u[c][i]);
-            u[c][i] = mma16(w, lo[c], u[c][i]);
-            u[c][i] = mma16(wl, hi[c], u[c][i]);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = fmaxf(m, max4(u[c][i]));
-        max_u[c] = column_max(m);
-      }
+      *(v8h*)(out + (KP_::kT + f) * kFrag + lane * 16) = v;
     }
-    // Y
-    {
-      v4f yd[NC][4];
-      float by[NC], inv[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) yd[c][i] = (v4f)(0.f);
-        const Scale sc(max_u[c]);
-        by[c] = sc.by;
-        inv[c] = sc.inv * inv_u[c] * fac[kInvA];
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v8h hi[NC], lo[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) split_tiles(u[c][2 * t], u[c][2 * t + 1], by[c], hi[c], lo[c]);
-#pragma unroll
-        for (int i = 2 * t; i < 4; ++i) {
-          const v8h w = weight(HP_::kA + lower_frag(i, t));
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            yd[c][i] = mma16(w, hi[c], yd[c][i]);
-            if constexpr (UY == 2) yd[c][i] = mma16(w, lo[c], yd[c][i]);
-            if constexpr (AP == 2) yd[c][i] = mma16(weight(HP_::kA + 6 + lower_frag(i, t)), hi[c], yd[c][i]);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4f f = *(const v4f*)(fac + kFacQ + 16 * i + 4 * sub);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) yd[c][i][e] = fmaf(f[e] * inv_s[c], qs[c][i][e], yd[c][i][e] * inv[c]);
-      }
-      auto store = [&](int i, int e) {
-        float y[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) y[c] = yd[c][i][e];
-        store_cols<DT, NC>(y_at + (uint64_t)(16 * i + e) * step + place, y);
-      };
-      if (left >= kC) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) store(i, e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (16 * i + 4 * sub + e < left) store(i, e);
-      }
-      y_at += (uint64_t)kC * step;
+    for (int t = wave_id(); t < 20; t += 4) {
+      const int u = t % 10, i = u < 1 ? 0 : u < 3 ? 1 : u < 6 ? 2 : 3, j = u - i * (i + 1) / 2;
+      *(v4f*)(out + (KP_::kKK + t) * kFrag + lane * 16) = key_tile<DT, N>(frags, t >= 10, i, j);
     }
-    // S' = e^{g_63} S + (e^{g_63 - g} U)^T K, the products added to the scaled state: its
-    // largest value is brought to 2^8 and U's part to 2 at most, so that the sums (64
-    // terms, keys up to 2^8) stay below 2^16 as fp16's range asks.
-    {
-      const float decay = fac[kDecay], most = fac[kMaxU] * 256.f;
-      float by[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float m = 0.f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) m = fmaxf(m, max4(s[c][n]));
-        const Scale sc(fmaxf(column_max(m) * inv_s[c] * decay, max_u[c] * inv_u[c] * most));
-        const float keep = decay * (inv_s[c] * sc.by);
-        by[c] = inv_u[c] * sc.by;
-        inv_s[c] = sc.inv;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[c][n] *= keep;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[c][i] *= *(const v4f*)(fac + kFacU + 16 * i + 4 * sub);
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v8h hi[NC], lo[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) split_tiles(u[c][2 * t], u[c][2 * t + 1], by[c], hi[c], lo[c]);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const v8h k = turned(2 * n + t);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            s[c][n] = mma16(k, hi[c], s[c][n]);
-            s[c][n] = mma16(k, lo[c], s[c][n]);
-            if constexpr (KP == 2) s[c][n] = mma16(turned(2 * NT + 2 * n + t), hi[c], s[c][n]);
-          }
-        }
-      }
-    }
-    meet();
-    if (more) copy2(keys, head);
-  }
-  if (a.final_state) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *(v4f*)(a.final_state + (unit * P + p0 + c) * (int64_t)N + 16 * n + 4 * sub) = s[c][n] * inv_s[c];
+    __syncthreads();
   }
 }
 
-template <int DT, int N, int NC, int W>
-hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, hipStream_t st) {
-  const int64_t wgs = d.B * d.H * (d.P / (16 * NC * W));
-  hipLaunchKernelGGL((k_delta_scan<DT, N, NC, W>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
+// ---------------------------------------------------------------------------
+// what a chunk of a head needs besides the state
+// ---------------------------------------------------------------------------
+// A position's step size, write strength and factors, one to a lane; behind the end
+// nothing decays and nothing is written.
+struct GateInputs {
+  float dt, beta, fk, fq;
+  template <int DT>
+  __device__ __forceinline__ void load(const DeltaArgs& a, const float* fac, int64_t row0, int64_t pos0, int64_t L, int H, int h) {
+    const bool live = pos0 + lane_id() < L;
+    const int64_t row = row0 + pos0 + lane_id();
+    dt = live ? ld_f<DT>(a.dt, row * H + h) : 0.f;
+    beta = live ? delta_beta<DT>(a, row, h) : 0.f;
+    fk = fac[lane_id()];
+    fq = fac[kC + lane_id()];
+  }
+};
+// A lane's value of a double, the same in all lanes.
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// v plus the value SHIFT lanes before in the row of 16.
+template <int SHIFT>
+__device__ __forceinline__ double row_add(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x110 + SHIFT, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), 0x110 + SHIFT, 0xf, 0xf, true);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float A) {
+  const int lane = lane_id(), sub = lane >> 4;
+  double gs = row_add<8>(row_add<4>(row_add<2>(row_add<1>((double)in.dt * ((double)A * 1.4426950408889634)))));
+  double end[4];  // of each 16 positions
+  end[0] = lane_value(gs, 15);
+  end[1] = end[0] + lane_value(gs, 31);
+  end[2] = end[1] + lane_value(gs, 47);
+  end[3] = end[2] + lane_value(gs, 63);
+  gs += sub == 0 ? 0.0 : sub == 1 ? end[0] : sub == 2 ? end[1] : end[2];
+  const double own = sub == 0 ? end[0] : sub == 1 ? end[1] : sub == 2 ? end[2] : end[3];
+  const float eg = exp2((float)gs), fu = exp2(fminf((float)(end[3] - gs), 0.f)) * in.fk;
+  w.g[lane] = (float)gs;
+  w.g_low[lane] = (float)(gs - (double)(float)gs);
+  w.beta[lane] = in.beta;
+  w.fk[lane] = in.fk;
+  w.fq[lane] = in.fq;
+  w.cols[lane] = exp2(fminf((float)(own - gs), 0.f)) * in.fk;
+  w.rows[3][lane] = in.beta * in.fk;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const float first = exp2(fminf((float)(gs - end[q]), 0.f));
+    w.first[q][lane] = first;
+    w.rows[q][lane] = in.beta * in.fk * first;
+  }
+  w.f.fac_k[lane] = eg * in.fk;
+  w.f.fac_q[lane] = eg * in.fq;
+  w.f.fac_u[lane] = fu;
+  const float most = wave_most(fu);
+  if (lane == 0) {
+    w.f.decay = exp2((float)end[3]);
+    w.f.most = most;
+  }
+}
+
+// L's tile (i, j) below the diagonal, from K K^T's.
+__device__ __forceinline__ v4f lower_tile(const Gates& w, v4f kk, int i, int j) {
+  const int sub = lane_id() >> 4, col = lane_id() & 15;
+  return *(const v4f*)&w.rows[j][16 * i + 4 * sub] * w.cols[16 * j + col] * kk;
+}
+// L's tile (i, i), into LDS.
+__device__ __forceinline__ void diagonal_tile(const Gates& w, v4f kk, int i, float* diag) {
+  const int sub = lane_id() >> 4, col = lane_id() & 15;
+  const float gj = w.g[16 * i + col], gl = w.g_low[16 * i + col], c = w.fk[16 * i + col];
+  const v4f gi = *(const v4f*)&w.g[16 * i + 4 * sub], gil = *(const v4f*)&w.g_low[16 * i + 4 * sub];
+  const v4f r = *(const v4f*)&w.rows[3][16 * i + 4 * sub];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float gamma = exp2(fminf((gi[e] - gj) + (gil[e] - gl), 0.f));
+    diag[i * kDiag + (4 * sub + e) * kDiagRow + col] = col < 4 * sub + e ? r[e] * c * gamma * kk[e] : 0.f;
+  }
+}
+// The inverses of the four diagonal blocks of 1 + L, in place: 16 lanes a block, each a
+// column. Each value that is final is taken out of all those below it at once, so that
+// 16 steps follow one another and not 120.
+__device__ __forceinline__ void invert_diagonal(float* diag) {
+  const int sub = lane_id() >> 4, col = lane_id() & 15;
+  float* const d = diag + sub * kDiag;
+  v4f l[16][4];
+#pragma unroll
+  for (int i = 1; i < 16; ++i)
+#pragma unroll
+    for (int q = 0; q <= (i - 1) / 4; ++q) l[i][q] = *(const v4f*)(d + i * kDiagRow + 4 * q);
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = i == col ? 1.f : 0.f;
+#pragma unroll
+  for (int k = 0; k < 15; ++k)
+#pragma unroll
+    for (int i = k + 1; i < 16; ++i) t[i] = fmaf(-l[i][k >> 2][k & 3], t[k], t[i]);
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) d[i * kDiagRow + col] = t[i];
+}
+
+// Tiles of a row of a lower triangle, transposed (rows are positions j, columns i), as
+// fragments for the products with R or U. Returns what undoes their scaling.
+template <int I, int PARTS>
+__device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out) {
+  const Scale sc(wave_most(tiles_max(x)));
+#pragma unroll
+  for (int s = 0; s <= I / 2; ++s) {
+    v8h hi, lo;
+    split_tiles(x[2 * s], 2 * s + 1 <= I ? x[2 * s + 1 <= I ? 2 * s + 1 : 0] : (v4f)(0.f), sc.by, sc.by, hi, lo);
+    *(v8h*)(out + lower_frag(I, s) * kFrag + lane_id() * 16) = hi;
+    if constexpr (PARTS == 2) *(v8h*)(out + (6 + lower_frag(I, s)) * kFrag + lane_id() * 16) = lo;
+  }
+  return sc.inv;
+}
+// Tile row I of T diag(b), from T_ij = -(sum_{j<k<=i} T_ik L_kj) T_jj. lower(k, j): L's
+// tiles; diag: the inverted blocks. The tiles are held transposed. Each one that is final
+// goes into the sums of all those before it at once.
+template <int I, class Lower>
+__device__ __forceinline__ void form_t_row(const Gates& w, const float* diag, Lower lower, char* out, Factors& f) {
+  const int sub = lane_id() >> 4, col = lane_id() & 15;
+  v4f x[I + 1], l[I + 1][I + 1], d[I + 1], beta[I + 1];
+  x[I] = *(const v4f*)(diag + I * kDiag + col * kDiagRow + 4 * sub);
+#pragma unroll
+  for (int k = I; k > 0; --k)
+#pragma unroll
+    for (int j = k - 1; j >= 0; --j) l[k][j] = lower(k, j);
+#pragma unroll
+  for (int j = I - 1; j >= 0; --j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[j][e] = diag[j * kDiag + (4 * sub + e) * kDiagRow + col];
+#pragma unroll
+  for (int j = 0; j <= I; ++j) beta[j] = *(const v4f*)&w.beta[16 * j + 4 * sub];
+#pragma unroll
+  for (int j = 0; j < I; ++j) x[j] = (v4f)(0.f);
+#pragma unroll
+  for (int k = I; k > 0; --k) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = k - 1; j >= 0; --j) x[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(l[k][j][e], x[k][e], x[j], 0, 0, 0);
+    // two halves, that need not wait for each other
+    v4f a = (v4f)(0.f), b = (v4f)(0.f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      a = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k - 1][e], x[k - 1][e], a, 0, 0, 0);
+      b = __builtin_amdgcn_mfma_f32_16x16x4f32(d[k - 1][2 + e], x[k - 1][2 + e], b, 0, 0, 0);
+    }
+    x[k - 1] = -(a + b);
+  }
+#pragma unroll
+  for (int j = 0; j <= I; ++j) x[j] *= beta[j];
+  const float inv = write_row<I, 2>(x, out);
+  if (lane_id() < 16) f.fac_u[16 * I + lane_id()] *= inv;
+  if (lane_id() == 0) f.inv_t[I] = inv;
+}
+// Tile row I of Y's weights of U.
+template <int PARTS, int I>
+__device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1], char* out, Factors& f) {
+  const int sub = lane_id() >> 4, col = lane_id() & 15;
+  const float fq = w.fq[16 * I + col];
+  v4f x[I + 1];
+#pragma unroll
+  for (int j = 0; j <= I; ++j) {
+    if (j < I) {
+      x[j] = *(const v4f*)&w.cols[16 * j + 4 * sub] * (fq * w.first[j < 3 ? j : 0][16 * I + col]) * kq[j];
+    } else {
+      const float gi = w.g[16 * I + col], gil = w.g_low[16 * I + col];
+      const v4f gj = *(const v4f*)&w.g[16 * I + 4 * sub], gl = *(const v4f*)&w.g_low[16 * I + 4 * sub];
+      const v4f cv = *(const v4f*)&w.fk[16 * I + 4 * sub];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float gamma = exp2(fminf((gi - gj[e]) + (gil - gl[e]), 0.f));
+        x[j][e] = 4 * sub + e <= col ? fq * cv[e] * gamma * kq[j][e] : 0.f;
+      }
+    }
+  }
+  const float inv = write_row<I, PARTS>(x, out);
+  if (lane_id() == 0) f.inv_a[I] = inv;
+}
+
+// Which of four waves does what of it. Part A: L's tiles; B: the inverse of L's
+// diagonal, Y's rows; C: T's rows. What of the keys' tiles a wave needs it holds itself.
+template <int DT, int N, int ROLE>
+struct Prepare {
+  typedef KeyPlan<DT, N> KP_;
+  static constexpr int AP = Parts<DT>::kWeights;
+  // tiles of K K^T: the diagonal one (ROLE, ROLE) and up to two below it
+  static constexpr int kBelow = ROLE == 0 || ROLE == 2 ? 2 : 1;
+  static constexpr int kI[2] = {ROLE == 0 ? 1 : ROLE == 1 ? 2 : 3, ROLE == 0 ? 2 : 3};
+  static constexpr int kJ[2] = {ROLE == 0 ? 0 : ROLE == 1 ? 1 : ROLE == 2 ? 0 : 2, ROLE == 0 ? 0 : 1};
+  // rows of Y's weights: role 1 rows 1 and 0, role 2 row 3, role 3 row 2
+  static constexpr int kRow = ROLE == 1 ? 1 : ROLE == 2 ? 3 : 2;
+  v4f kk[1 + kBelow], kq[kRow + 1], kq0[1];
+
+  __device__ __forceinline__ void load(const char* keys) {
+    auto tile = [&](int f) { return *(const v4f*)(keys + f * kFrag + lane_id() * 16); };
+    kk[0] = tile(KP_::kKK + lower_tile_at(ROLE, ROLE));
+#pragma unroll
+    for (int n = 0; n < kBelow; ++n) kk[1 + n] = tile(KP_::kKK + lower_tile_at(kI[n], kJ[n]));
+    if constexpr (ROLE > 0) {
+#pragma unroll
+      for (int j = 0; j <= kRow; ++j) kq[j] = tile(KP_::kKQ + lower_tile_at(kRow, j));
+    }
+    if constexpr (ROLE == 1) kq0[0] = tile(KP_::kKQ);
+  }
+  __device__ __forceinline__ void part_a(const Gates& w, v4f (*lower)[kWave], float* diag) {
+    diagonal_tile(w, kk[0], ROLE, diag);
+#pragma unroll
+    for (int n = 0; n < kBelow; ++n)
+      lower[kI[n] * (kI[n] - 1) / 2 + kJ[n]][lane_id()] = lower_tile(w, kk[1 + n], kI[n], kJ[n]);
+  }
+  __device__ __forceinline__ void part_b(Gates& w, float* diag, char* a_frags) {
+    if constexpr (ROLE == 0) invert_diagonal(diag);
+    else form_y_row<AP, kRow>(w, kq, a_frags, w.f);
+    if constexpr (ROLE == 1) form_y_row<AP, 0>(w, kq0, a_frags, w.f);
+  }
+  __device__ __forceinline__ void part_c(Gates& w, const v4f (*lower)[kWave], const float* diag, char* t_frags) {
+    form_t_row<ROLE>(w, diag, [&](int k, int j) { return lower[k * (k - 1) / 2 + j][lane_id()]; }, t_frags, w.f);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// the chain
+// ---------------------------------------------------------------------------
+// V's rows pass through LDS, W waves' columns of a row together: memory is asked for
+// 32 W bytes of a row in one piece, instead of 2 bytes for each value.
+template <int DT, int W>
+constexpr int kRowBytes = 16 * W * sizeof(typename Store<DT>::T);
+// A wave's part of the copies of n rows (of 64; behind the end of the sequence its last
+// row stands in: what it meets in T is zero) that are `step` bytes apart: sizeof(T) of them.
+template <int DT, int W>
+__device__ __forceinline__ void copy_values(const char* x, uint32_t step, int n, char* values, int wave) {
+  constexpr int kRow = kRowBytes<DT, W>, kLanes = kRow / 16, kRows = kWave / kLanes, kCopies = kC / kRows / W;
+  static_assert(kCopies == sizeof(typename Store<DT>::T), "copies of a wave");
+#pragma unroll
+  for (int c = 0; c < kCopies; ++c) {
+    const int first = (wave * kCopies + c) * kRows, row = min(first + lane_id() / kLanes, n - 1);
+    copy_frag(x + (row * step + lane_id() % kLanes * 16), values + first * kRow);
+  }
+}
+
+// A wave's 16 rows of a head's state (columns of S^T), and a chunk's way through it. The
+// state is held times a power of two, one for each row: 1 / inv_s.
+template <int DT, int N>
+struct Chain {
+  typedef KeyPlan<DT, N> KP_;
+  typedef typename Store<DT>::T T;
+  static constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
+  static constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
+  v4f s[NT], ks[4], qs[4], u[4];
+  v8h wt[6], wl[6];  // T's fragments
+  float inv_s, inv_r, max_s, max_u, one;
+  int place;  // of the lane's column in a row of the workgroup's
+
+  __device__ __forceinline__ static v8h frag(const char* p, int f) { return *(const v8h*)(p + f * kFrag + lane_id() * 16); }
+
+  __device__ __forceinline__ void init(const DeltaArgs& a, int64_t unit, int P, int p) {
+    const int sub = lane_id() >> 4;
+    place = (wave_id() * 16 + (lane_id() & 15)) * sizeof(T);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      s[n] = a.init ? *(const v4f*)(a.init + (unit * P + p) * (int64_t)N + 16 * n + 4 * sub) : (v4f)(0.f);
+    const Scale sc(column_max(tiles_max(s)));
+    inv_s = sc.inv;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n] *= sc.by;
+    one = 1.f;
+    asm volatile("" : "+v"(one));
+  }
+  __device__ __forceinline__ void finish(const DeltaArgs& a, int64_t unit, int P, int p) {
+    if (!a.final_state) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      *(v4f*)(a.final_state + (unit * P + p) * (int64_t)N + 16 * n + 4 * (lane_id() >> 4)) = s[n] * inv_s;
+  }
+  // K S^T and Q S^T. What comes out of LDS is read a step ahead of its use, here and
+  // below: a wave has its SIMD to itself, or nearly.
+  __device__ __forceinline__ void products(const char* keys) {
+    v8h k[2][4 * KP], q[2][4 * KP];
+    auto read = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < 4 * KP; ++i) {
+        k[t & 1][i] = frag(keys, KP_::kK + i * KS + t);
+        q[t & 1][i] = frag(keys, KP_::kQ + i * KS + t);
+      }
+    };
+    read(0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = (v4f)(0.f);
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      if (t + 1 < KS) read(t + 1);
+      v8h hi, lo;
+      const v4f a = s[2 * t], b = 2 * t + 1 < NT ? s[2 * t + 1 < NT ? 2 * t + 1 : 0] : (v4f)(0.f);
+      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      split8_unscaled(x, one, hi, lo);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][i], hi, ks[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][i], hi, qs[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][i], lo, ks[i]);
+      if constexpr (SY == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][i], lo, qs[i]);
+      }
+      if constexpr (KP == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][4 + i], hi, ks[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][4 + i], hi, qs[i]);
+      }
+    }
+    max_s = column_max(tiles_max(s));
+  }
+  // T's fragments, for what follows
+  __device__ __forceinline__ void read_t(const char* t_frags) {
+#pragma unroll
+    for (int n = 0; n < 6; ++n) {
+      wt[n] = frag(t_frags, n);
+      wl[n] = frag(t_frags, 6 + n);
+    }
+  }
+  // R = V - e^g K S^T, in the place of K S^T; values: V's rows, of W waves' columns.
+  template <int W>
+  __device__ __forceinline__ void remainders(const char* values, const Factors& f) {
+    const char* const at = values + 4 * (lane_id() >> 4) * kRowBytes<DT, W> + place;
+    float v[4][4];
+    v4f fk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fk[i] = *(const v4f*)(f.fac_k + 16 * i + 4 * (lane_id() >> 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[i][e] = ld_f<DT>(at + (16 * i + e) * kRowBytes<DT, W>, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ks[i][e] = fmaf(-fk[i][e] * inv_s, ks[i][e], v[i][e]);
+  }
+  // U = T diag(b) R, as u times inv_r and, of tile row i, inv_t[i].
+  __device__ __forceinline__ void changes(const Factors& f) {
+    const Scale sc(column_max(tiles_max(ks)));
+    inv_r = sc.inv;
+    v8h hi[2], lo[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) split_tiles(ks[2 * t], ks[2 * t + 1], sc.by, sc.by, hi[t], lo[t]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = mma16(wt[lower_frag(i, 0)], hi[0], (v4f)(0.f));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = mma16(wt[lower_frag(i, 0)], lo[0], u[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = mma16(wl[lower_frag(i, 0)], hi[0], u[i]);
+#pragma unroll
+    for (int i = 2; i < 4; ++i) u[i] = mma16(wt[lower_frag(i, 1)], hi[1], u[i]);
+#pragma unroll
+    for (int i = 2; i < 4; ++i) u[i] = mma16(wt[lower_frag(i, 1)], lo[1], u[i]);
+#pragma unroll
+    for (int i = 2; i < 4; ++i) u[i] = mma16(wl[lower_frag(i, 1)], hi[1], u[i]);
+    const v4f inv = *(const v4f*)f.inv_t;
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max4(0.f, u[i]) * inv[i];
+    max_u = column_max(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+  }
+  // Y of the chunk's `left` positions, through `stage` (32 rows of the wave's 16 columns), and
+  //   S' = e^{g_63} S + (e^{g_63 - g} U)^T K,
+  // the products added to the scaled state: its largest value is brought to 2^8 and U's
+  // part to 2 at most, so that the sums (64 terms, keys up to 2^8) stay below 2^16 as
+  // fp16's range asks.
+  __device__ __forceinline__ void outputs_and_state(const char* a_frags, const char* turned, const Factors& f, T* stage, char* out,
+                                                    uint32_t step, int left) {
+    const int sub = lane_id() >> 4;
+    v8h w[6 * AP], k[2][NT];
+    v4f fu[4];
+#pragma unroll
+    for (int n = 0; n < 6 * AP; ++n) w[n] = frag(a_frags, n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fu[i] = *(const v4f*)(f.fac_u + 16 * i + 4 * sub);
+    const v4f inv_t = *(const v4f*)f.inv_t, inv_a = *(const v4f*)f.inv_a;
+    const float decay = f.decay, most = f.most;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) k[0][n] = frag(turned, 2 * n);
+    v4f y[4];
+    const Scale sy(max_u);
+    {
+      v8h hi[2], lo[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        split_tiles(u[2 * t], u[2 * t + 1], inv_t[2 * t] * sy.by, inv_t[2 * t + 1] * sy.by, hi[t], lo[t]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 0)], hi[0], (v4f)(0.f));
+#pragma unroll
+      for (int i = 2; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 1)], hi[1], y[i]);
+      if constexpr (UY == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 0)], lo[0], y[i]);
+#pragma unroll
+        for (int i = 2; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 1)], lo[1], y[i]);
+      }
+      if constexpr (AP == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mma16(w[6 + lower_frag(i, 0)], hi[0], y[i]);
+#pragma unroll
+        for (int i = 2; i < 4; ++i) y[i] = mma16(w[6 + lower_frag(i, 1)], hi[1], y[i]);
+      }
+    }
+    const float was = inv_s;
+    const Scale sc(fmaxf(max_s * inv_s * decay, max_u * inv_r * most * 256.f));
+    const float keep = decay * (inv_s * sc.by), by = inv_r * sc.by;
+    inv_s = sc.inv;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n] *= keep;
+    v8h hi[2], lo[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) split_tiles(u[2 * t] * fu[2 * t], u[2 * t + 1] * fu[2 * t + 1], by, by, hi[t], lo[t]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) k[1][n] = frag(turned, 2 * n + 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n] = mma16(k[t][n], hi[t], s[n]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n] = mma16(k[t][n], lo[t], s[n]);
+      if constexpr (KP == 2) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n] = mma16(frag(turned, 2 * NT + 2 * n + t), hi[t], s[n]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float inv = sy.inv * inv_r * inv_a[i];
+      const v4f fq = *(const v4f*)(f.fac_q + 16 * i + 4 * sub);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[i][e] = fmaf(fq[e] * was, qs[i][e], y[i][e] * inv);
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          stage[(16 * i + 4 * sub + e) * 16 + (lane_id() & 15)] = to_store<DT>(y[2 * half + i][e]);
+      wave_sync();
+      // 32 rows in pieces of 16 bytes, to rows of Y `step` bytes apart
+      constexpr int kPer = 16 * sizeof(T) / 16;  // pieces of a row
+#pragma unroll
+      for (int n = 0; n < kPer / 2; ++n) {
+        const int row = (n * kWave + lane_id()) / kPer, piece = lane_id() % kPer;
+        const v4u v = *(const v4u*)((const char*)stage + row * 16 * sizeof(T) + piece * 16);
+        if (32 * half + row < left) *(v4u*)(out + ((32 * half + row) * step + piece * 16)) = v;
+      }
+      wave_sync();
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// kernels of a head
+// ---------------------------------------------------------------------------
+template <int DT, int N>
+__global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, const char* ws, char* ws_heads, int64_t L, int H,
+                                                     int G, int hpg, int chunks, int64_t total) {
+  typedef KeyPlan<DT, N> KP_;
+  typedef HeadPlan<DT> HP_;
+  __shared__ __attribute__((aligned(16))) Gates w;
+  __shared__ __attribute__((aligned(16))) v4f lower[6][kWave];
+  __shared__ __attribute__((aligned(16))) float diag[4 * kDiag];
+  auto chunk = [&](auto role, int64_t item) {
+    constexpr int kRole = decltype(role)::value;
+    const int ck = (int)(item % chunks);
+    const int64_t unit = item / chunks, b = unit / H;
+    const int h = (int)(unit % H);
+    const char* const keys = ws + ((b * G + h / hpg) * (int64_t)chunks + ck) * KP_::kBytes;
+    char* const out = ws_heads + item * HP_::kBytes;
+    Prepare<DT, N, kRole> p;
+    p.load(keys);
+    if constexpr (kRole == 0) {
+      GateInputs in;
+      in.load<DT>(a, (const float*)(keys + KP_::kFac * kFrag), b * L, (int64_t)ck * kC, L, H, h);
+      form_gates(w, in, a.A[h]);
+    }
+    __syncthreads();
+    p.part_a(w, lower, diag);
+    __syncthreads();
+    p.part_b(w, diag, out + HP_::kA * kFrag);
+    __syncthreads();
+    p.part_c(w, lower, diag, out + HP_::kT * kFrag);
+    __syncthreads();
+    if (threadIdx.x < sizeof(Factors) / sizeof(float))
+      ((float*)(out + HP_::kFac * kFrag))[threadIdx.x] = ((const float*)&w.f)[threadIdx.x];
+    __syncthreads();  // the next chunk's gates overwrite this one's
+  };
+  for (int64_t item = blockIdx.x; item < total; item += gridDim.x) {
+    switch (wave_id()) {
+      case 0: chunk(std::integral_constant<int, 0>(), item); break;
+      case 1: chunk(std::integral_constant<int, 1>(), item); break;
+      case 2: chunk(std::integral_constant<int, 2>(), item); break;
+      default: chunk(std::integral_constant<int, 3>(), item);
+    }
+  }
+}
+
+// A workgroup of W waves takes 16 W rows of a head's state, through whose chunks the
+// fragments and V's rows come through LDS.
+//   DEEP: two buffers of each; the next chunk's copies are on their way all the while,
+//   with one barrier a chunk. One workgroup on a CU.
+//   Otherwise one, in two halves, K and Q, and the rest: the copies of the next chunk's
+//   half are on their way while the other half is used, with a barrier in between. Two
+//   workgroups on a CU (16-bit types), which cover one another's waits.
+template <int DT, int N, int W, bool DEEP>
+__global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) void k_delta_scan(
+    DeltaArgs a, const char* ws, const char* ws_heads, int64_t L, int H, int G, int hpg, int P, int chunks) {
+  typedef KeyPlan<DT, N> KP_;
+  typedef HeadPlan<DT> HP_;
+  typedef typename Store<DT>::T T;
+  constexpr int kFirst = KP_::kT * kFrag, kRest = (KP_::kTurned + HP_::kFrags) * kFrag, kValues = kC * kRowBytes<DT, W>;
+  // separate objects, so that the compiler sees that a read of one need not wait for
+  // the copies into another
+  __shared__ __attribute__((aligned(1024))) char first0[kFirst], rest0[kRest], values0[kValues];
+  __shared__ __attribute__((aligned(1024))) char first1[DEEP ? kFirst : 16], rest1[DEEP ? kRest : 16];
+  __shared__ __attribute__((aligned(1024))) char values1[DEEP ? kValues : 16];
+  __shared__ __attribute__((aligned(1024))) T stage[W][kC / 2 * 16];
+  constexpr int E = sizeof(T);
+  const int wv = wave_id();
+  const int slices = P / (16 * W);
+  const int64_t unit = blockIdx.x / slices, b = unit / H;
+  const int h = (int)(unit % H), start = (int)(blockIdx.x % slices) * W * 16, p = start + wv * 16 + (lane_id() & 15);
+  const uint32_t step = (uint32_t)H * P * E;  // between rows: 64 of them are less than 2^32 bytes
+  const char* const x = (const char*)a.X + ((b * L * H + h) * P + start) * E;
+  char* const y = (char*)a.Y + ((b * L * H + h) * P + start + wv * 16) * E;
+  const char* const keys = ws + (b * G + h / hpg) * (int64_t)chunks * KP_::kBytes;
+  const char* const head = ws_heads + unit * (int64_t)chunks * HP_::kBytes;
+  auto left = [&](int i) { return (int)min(L - (int64_t)i * kC, (int64_t)kC); };
+  auto copy_first = [&](int i, char* to) { copy_frags<KP_::kT, W>(keys + i * (int64_t)KP_::kBytes, to, wv); };
+  auto copy_rest = [&](int i, char* to, char* values) {
+    copy_frags<KP_::kTurned, W>(keys + i * (int64_t)KP_::kBytes + KP_::kT * kFrag, to, wv);
+    copy_frags<HP_::kFrags, W>(head + i * (int64_t)HP_::kBytes, to + KP_::kTurned * kFrag, wv);
+    copy_values<DT, W>(x + i * (kC * (int64_t)step), step, left(i), values, wv);
+  };
+  copy_first(0, first0);
+  copy_rest(0, rest0, values0);
+  Chain<DT, N> c;
+  c.init(a, unit, P, p);
+  meet<0>();
+  // chunk i, from one set of buffers; the next one's go to `first`, `rest` and `vals`
+  auto chunk = [&](int i, const char* kq, const char* others, const char* values, char* first, char* rest,
+                   char* vals) __attribute__((always_inline)) {
+    const bool more = i + 1 < chunks;
+    const char* const frags = others + KP_::kTurned * kFrag;
+    const Factors& f = *(const Factors*)(frags + HP_::kFac * kFrag);
+    if (DEEP && more) {
+      copy_first(i + 1, first);
+      copy_rest(i + 1, rest, vals);
+      asm volatile("" ::: "memory");
+    }
+    c.products(kq);
+    if constexpr (!DEEP) {
+      meet<0>();
+      if (more) copy_first(i + 1, first);
+    }
+    c.read_t(frags + HP_::kT * kFrag);
+    c.template remainders<W>(values, f);
+    c.changes(f);
+    c.outputs_and_state(frags + HP_::kA * kFrag, others, f, stage[wv], y + i * (kC * (int64_t)step), step, left(i));
+    // the E stores of Y are the newest, and may be under way still (the last chunk, which
+    // may have fewer, waits for no copies)
+    meet<E>();
+    if (!DEEP && more) copy_rest(i + 1, rest, vals);
+  };
+  if constexpr (DEEP) {
+    for (int i = 0; i < chunks; i += 2) {
+      chunk(i, first0, rest0, values0, first1, rest1, values1);
+      if (i + 1 < chunks) chunk(i + 1, first1, rest1, values1, first0, rest0, values0);
+    }
+  } else {
+    for (int i = 0; i < chunks; ++i) chunk(i, first0, rest0, values0, first0, rest0, values0);
+  }
+  c.finish(a, unit, P, p);
+}
+
+// ---------------------------------------------------------------------------
+// dispatch
+// ---------------------------------------------------------------------------
+template <int DT, int N, int W>
+hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, int64_t ncu, hipStream_t st) {
+  const int64_t wgs = d.B * d.H * (d.P / (16 * W));
+  if constexpr (DT != DT_F32) {
+    if (wgs <= ncu) {
+      hipLaunchKernelGGL((k_delta_scan<DT, N, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
+                         d.G, d.hpg, d.P, d.c);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_delta_scan<DT, N, W, false>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
                      d.G, d.hpg, d.P, d.c);
   return hipGetLastError();
 }
 
-// Four waves of 16 rows each where the head has them (us at 4, 2 and 1 waves: 8 x 2048
-// positions of 80 heads of 64 x 128, 16 bits, 594, 1403 and 2311 before later steps; one
-// sequence of 2048, 64 heads, 192, 214 and 246). Waves of 32 rows read LDS half as
-// often, but leave each SIMD one wave: 439 us with 16, 559 with 32.
-template <int DT, int N>
-hipError_t pick_scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, hipStream_t st) {
-  switch (d.P) {
-    case 16: return scan<DT, N, 1, 1>(d, a, keys, heads, st);
-    case 32: return scan<DT, N, 1, 2>(d, a, keys, heads, st);
-    default: return scan<DT, N, 1, 4>(d, a, keys, heads, st);
-  }
-}
-
 template <int DT, int N>
 hipError_t go(const Dims& d, const DeltaArgs& a, char* ws, hipStream_t st) {
-  char* const heads = ws + d.B * d.G * (int64_t)d.c * KeyPlan<DT, N>::kBytes;
-  const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
-  // heads of a group that a workgroup takes: four, or more where that leaves
-  // workgroups enough
-  const int64_t groups = d.B * d.c * d.G;
-  int per = 4;
-  while (per < d.hpg && groups * ((d.hpg + 2 * per - 1) / (2 * per)) >= 8 * ncu) per *= 2;
-  const int blocks = (d.hpg + per - 1) / per;
-  const int64_t total = groups * blocks;
-  hipLaunchKernelGGL((k_delta_prepare<DT, N>), dim3((unsigned)min(total, (int64_t)1 << 20)), dim3(256), 0, st, a, ws,
-                     heads, d.L, d.H, d.G, d.hpg, d.c, blocks, per, total);
-  const hipError_t e = hipGetLastError();
+  const int64_t total = d.B * d.G * (int64_t)d.c;
+  hipLaunchKernelGGL((k_delta_keys<DT, N>), dim3((unsigned)min(total, (int64_t)1 << 20)), dim3(256), 0, st, a, ws, d.L, d.G,
+                     d.c, total);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return pick_scan<DT, N>(d, a, ws, heads, st);
+  char* const heads = ws + total * KeyPlan<DT, N>::kBytes;
+  const int64_t units = d.B * d.H * (int64_t)d.c, ncu = cu_count() > 0 ? cu_count() : 256;
+  hipLaunchKernelGGL((k_delta_prepare<DT, N>), dim3((unsigned)min(units, (int64_t)1 << 20)), dim3(256), 0, st, a, ws, heads,
+                     d.L, d.H, d.G, d.hpg, d.c, units);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  // Four waves where the head has them (us at 4, 2 and 1: 8 x 2048 positions of 80 heads of
+  // 64 x 128 425, 521 and 783; one sequence of 2048, 64 heads, 114, 115 and 122).
+  switch (d.P) {
+    case 16: return scan<DT, N, 1>(d, a, ws, heads, ncu, st);
+    case 32: return scan<DT, N, 2>(d, a, ws, heads, ncu, st);
+    default: return scan<DT, N, 4>(d, a, ws, heads, ncu, st);
+  }
 }
 
 template <int DT>

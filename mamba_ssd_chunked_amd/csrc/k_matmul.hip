@@ -240,10 +240,18 @@ __global__ __launch_bounds__(256, 2) void k_matmul_any(MatmulArgs g, int blocks_
   v4i va[kPer], vw[kPer];
   auto load = [&](int step) {
     const int k = step * kStep + (tid & 7) * (16 / (int)sizeof(T));
+    if ((step + 1) * kStep <= K) {  // the same for all threads: no piece ends early
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      va[i] = load_any<DT>(ra[i], k, K);
-      vw[i] = load_any<DT>(rw[i], k, K);
+      for (int i = 0; i < kPer; ++i) {
+        va[i] = __builtin_bit_cast(v4i, *(const v4u_any*)(ra[i] + k));
+        vw[i] = __builtin_bit_cast(v4i, *(const v4u_any*)(rw[i] + k));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        va[i] = load_any<DT>(ra[i], k, K);
+        vw[i] = load_any<DT>(rw[i], k, K);
+      }
     }
   };
   auto put = [&](int8_t* b) {
@@ -386,8 +394,8 @@ hipError_t launch(const MatmulArgs& g, hipStream_t st) {
   if (!aligned) {
     if (g.M <= 16) return launch_any_rows<DT, OT, 1>(g, st);
     if (g.M <= 32) return launch_any_rows<DT, OT, 2>(g, st);
-    // blocks of 128 where they fill the chip twice (two fit a CU)
-    if ((g.M + 127) / 128 * ((g.N + 127) / 128) >= 2 * ncu) return launch_any<DT, OT, 2>(g, st);
+    // blocks of 128 where each CU has one
+    if ((getenv("MM") ? getenv("MM")[0] == '1' : (g.M + 127) / 128 * ((g.N + 127) / 128) >= ncu)) return launch_any<DT, OT, 2>(g, st);
     return launch_any<DT, OT, 1>(g, st);
   }
   switch (pick_matmul_kind(g.M, g.N, g.K * E, ncu, DT == DT_F32 ? 8.f : 1.f)) {

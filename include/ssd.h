@@ -502,17 +502,20 @@ enum {
  * place) and w [N, K] dense in dtype; bias [N] fp32 (NULL: 0); act an SSD_ACT_*
  * code; out [M, N] and residual [M, N] (NULL: 0) dense in out_dtype, which is dtype or
  * SSD_DTYPE_F32. residual may be out itself. Sums and the epilogue are fp32, rounded
- * once (fp32 operands are multiplied in fp32). Any K; rows that are 16-byte aligned
- * and a multiple of 16 bytes long are fastest. M, N < 2^26, M * N < 2^40, K <= ld_a <
+ * once (fp32 operands are multiplied in fp32). M, N < 2^26, M * N < 2^40, K <= ld_a <
  * 2^22 (SSD_E_SHAPE); M == 0 is a valid empty problem. An unknown activation or type,
- * or an out_dtype that is neither, returns SSD_E_UNSUPPORTED. workspace: device memory
- * of at least ssd_matmul_workspace_bytes(M, N, K, dtype) bytes, 16-byte aligned. No
- * product needs one at present: that is 0, and NULL will do. */
+ * or an out_dtype that is neither, returns SSD_E_UNSUPPORTED.
+ * Any K. Rows of a and w that are 16-byte aligned and a multiple of 16 bytes long are
+ * taken as they are, and need no workspace. For others it is optional: device memory,
+ * 16-byte aligned, of at least ssd_matmul_workspace_bytes(M, N, K, dtype) bytes (fewer:
+ * SSD_E_WORKSPACE), into which they are copied; with NULL they are read as they lie,
+ * which is slower for more than a few rows. */
 int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_t ld_a, const void* w,
                const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace,
                size_t workspace_bytes, void* stream);
 
-/* Workspace bytes ssd_matmul needs: 0. Host only. */
+/* Workspace bytes that ssd_matmul can use for rows that are not aligned (0 where it
+ * has no use for one, or for an invalid size). Host only. */
 size_t ssd_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
 
 /* From one block of a layer to the next: the norm after the block, its gate, the

@@ -707,15 +707,21 @@ def ssd_matmul_workspace_bytes(m, n, k, dtype) -> int:
 
 
 def ssd_matmul_workspace(a, w, out):
-    """A workspace for ``ssd_matmul`` on these tensors (None where none is needed)."""
-    need = ssd_matmul_workspace_bytes(out.numel() // max(1, out.shape[-1]), w.shape[0], w.shape[1], a.dtype)
+    """A workspace for ``ssd_matmul`` on tensors like these (None where it has no use for one: rows that are
+    16-byte aligned, or few)."""
+    n, k = w.shape
+    m = a.numel() // max(1, k)
+    _, lda = _rows(a, "a", k, a.dtype, a.get_device())
+    if (a.data_ptr() | w.data_ptr() | lda * a.element_size() | k * a.element_size()) % 16 == 0:
+        return None
+    need = ssd_matmul_workspace_bytes(m, n, k, a.dtype)
     return torch.empty(need, dtype=torch.uint8, device=out.device) if need else None
 
 
 def ssd_matmul(a, w, bias, out, act=SSD_ACT_NONE, residual=None, workspace=None, stream=None):
     """out = act(a @ w.T + bias) + residual for a [..., K] (may be a column slice), w [N, K] of a's
     type; ``out`` and ``residual`` (which may be the same tensor) in that type or float32; bias float32 or
-    None. ``workspace``: see the C call (None will do)."""
+    None. ``workspace``: from ``ssd_matmul_workspace``, for many rows that are not 16-byte aligned (None will do)."""
     n, k = w.shape
     if a.shape[-1] != k:
         raise ValueError("a and w must agree in their last dimension")

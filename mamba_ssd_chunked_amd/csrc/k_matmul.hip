@@ -7,8 +7,10 @@
 // Rows that are 16-byte aligned and long take the ways of the 8-bit product
 // (ssd_matmul.hpp): a 128-byte step is 64 positions of 16-bit rows, with the same matrix
 // cycles, LDS reads and copies as 128 of 8-bit ones, and the same choice of kernel by
-// the rows' bytes. All others go through registers, in pieces of 16 bytes at any
-// element's address, the last of a row element by element.
+// the rows' bytes. Others are copied into aligned rows first where the caller gives room
+// for them, and the rows of a are many enough to be worth a pass over w; or they go
+// through registers, in pieces of 16 bytes at any element's address, the last of a row
+// element by element.
 #include "ssd_act.hpp"
 #include "ssd_launch.hpp"
 #include "ssd_matmul.hpp"
@@ -214,6 +216,25 @@ __device__ __forceinline__ v4i load_any(const void* row, int k, int K) {
   return u.v;
 }
 
+// Aligned copies of rows: a wave a row, its end filled up with zeros to Kp elements.
+struct PackRows {
+  const void* from;
+  int64_t ld, rows;
+  void* to;
+};
+template <int DT>
+__global__ __launch_bounds__(256) void k_matmul_pack(PackRows a, PackRows w, int K, int Kp) {
+  typedef typename Store<DT>::T T;
+  constexpr int E = 16 / sizeof(T);
+  for (int64_t r = (int64_t)blockIdx.x * 4 + wave_id(); r < a.rows + w.rows; r += (int64_t)gridDim.x * 4) {
+    const bool second = r >= a.rows;
+    const int64_t row = second ? r - a.rows : r;
+    const T* const from = (const T*)(second ? w.from : a.from) + row * (second ? w.ld : a.ld);
+    T* const to = (T*)(second ? w.to : a.to) + row * Kp;
+    for (int k = lane_id() * E; k < Kp; k += kWave * E) *(v4i*)(to + k) = load_any<DT>(from, k, K);
+  }
+}
+
 // A workgroup of four waves takes 64 TS rows and columns, a wave 32 TS of each. The
 // operands of a step of 128 bytes pass through registers into one of two buffers in LDS
 // (slots as the tiles') while the step before is multiplied.
@@ -386,17 +407,41 @@ hipError_t launch_any_rows(const MatmulArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Elements of an aligned copy's rows.
+template <int DT>
+int64_t packed_cols(int64_t K) {
+  constexpr int64_t E = sizeof(typename Store<DT>::T);
+  return K * E % 16 == 0 ? K : (K * E + 127) / 128 * 128 / E;
+}
+
 template <int DT, int OT>
-hipError_t launch(const MatmulArgs& g, hipStream_t st) {
+hipError_t launch(MatmulArgs g, void* ws, hipStream_t st) {
   const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
   constexpr int64_t E = sizeof(typename Store<DT>::T);
-  const bool aligned = ((uintptr_t)g.a | (uintptr_t)g.w | (uintptr_t)(g.lda * E) | (uintptr_t)(g.K * E)) % 16 == 0;
-  if (!aligned) {
-    if (g.M <= 16) return launch_any_rows<DT, OT, 1>(g, st);
-    if (g.M <= 32) return launch_any_rows<DT, OT, 2>(g, st);
-    // blocks of 128 where each CU has one
-    if ((getenv("MM") ? getenv("MM")[0] == '1' : (g.M + 127) / 128 * ((g.N + 127) / 128) >= ncu)) return launch_any<DT, OT, 2>(g, st);
-    return launch_any<DT, OT, 1>(g, st);
+  if (!matmul_aligned(DT, g)) {
+    if (ws && g.M >= kMatmulPackRows) {
+      // w's rows are aligned where K allows it
+      const int64_t Kp = packed_cols<DT>(g.K);
+      PackRows a{g.a, g.lda, g.M, ws}, w{g.w, g.K, Kp == g.K ? 0 : g.N, (char*)ws + g.M * Kp * E};
+      const int64_t wgs = (a.rows + w.rows + 3) / 4;
+      hipLaunchKernelGGL((k_matmul_pack<DT>), dim3((unsigned)min(wgs, (int64_t)1 << 20)), dim3(256), 0, st, a, w, (int)g.K, (int)Kp);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      g.a = ws;
+      if (w.rows) g.w = w.to;
+      g.lda = g.K = Kp;
+    } else if (g.M <= 16) {
+      return launch_any_rows<DT, OT, 1>(g, st);
+    } else if (g.M <= 32) {
+      return launch_any_rows<DT, OT, 2>(g, st);
+    } else {
+      // Blocks of 128 where each CU has one, of 16-bit rows (us with 128 and 64: 1065 x
+      // 4099 x 2579 bf16 70, 93; 300 x 4099 x 2579 55, 35; 1065 x 4099 x 2579 fp32, which
+      // the matrix instructions bound, 340, 231).
+      if constexpr (DT != DT_F32)
+        if ((g.M + 127) / 128 * ((g.N + 127) / 128) >= ncu) return launch_any<DT, OT, 2>(g, st);
+      return launch_any<DT, OT, 1>(g, st);
+    }
   }
   switch (pick_matmul_kind(g.M, g.N, g.K * E, ncu, DT == DT_F32 ? 8.f : 1.f)) {
     case 0: return launch_rows<DT, OT, 1, 1, 8, 2>(g, st);
@@ -411,12 +456,18 @@ hipError_t launch(const MatmulArgs& g, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& g, hipStream_t st) {
+size_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (M < kMatmulPackRows) return 0;
+  const int64_t Kp = dtype == DT_F32 ? packed_cols<DT_F32>(K) : packed_cols<DT_F16>(K);
+  return (size_t)(M + (Kp == K ? 0 : N)) * Kp * (dtype == DT_F32 ? 4 : 2);
+}
+
+hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& g, void* ws, hipStream_t st) {
   const bool keep32 = out_dtype == DT_F32;
   switch (dtype) {
-    case DT_F32: return launch<DT_F32, DT_F32>(g, st);
-    case DT_F16: return keep32 ? launch<DT_F16, DT_F32>(g, st) : launch<DT_F16, DT_F16>(g, st);
-    case DT_BF16: return keep32 ? launch<DT_BF16, DT_F32>(g, st) : launch<DT_BF16, DT_BF16>(g, st);
+    case DT_F32: return launch<DT_F32, DT_F32>(g, ws, st);
+    case DT_F16: return keep32 ? launch<DT_F16, DT_F32>(g, ws, st) : launch<DT_F16, DT_F16>(g, ws, st);
+    case DT_BF16: return keep32 ? launch<DT_BF16, DT_F32>(g, ws, st) : launch<DT_BF16, DT_BF16>(g, ws, st);
     default: return hipErrorInvalidValue;
   }
 }

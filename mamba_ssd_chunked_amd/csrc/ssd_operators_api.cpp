@@ -104,25 +104,34 @@ int ssd_delta_step(const ssd_shape* shape, int flags, const void* X, const void*
   return hip_status(ssd::launch_delta_steps(d, shape->dtype, a, (hipStream_t)stream));
 }
 
-// No kernel needs a workspace: sums that are split over waves meet in LDS.
-size_t ssd_matmul_workspace_bytes(int64_t, int64_t, int64_t, int) { return 0; }
+// M, N, K of the product.
+static int check_product(int64_t M, int64_t N, int64_t K, int dtype) {
+  constexpr int64_t kMost = (int64_t)1 << 26;  // rows: tile indexes and offsets in a tile's rows fit 32 bits
+  if (M < 0 || N <= 0 || K <= 0 || M >= kMost || N >= kMost || M * N >= (int64_t)1 << 40) return SSD_E_SHAPE;
+  if (K >= (int64_t)1 << 22) return SSD_E_SHAPE;  // 256 rows are less than 2^32 bytes
+  return known_dtype(dtype) ? SSD_OK : SSD_E_UNSUPPORTED;
+}
+
+size_t ssd_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  return check_product(M, N, K, dtype) ? 0 : ssd::matmul_workspace_bytes(M, N, K, dtype);
+}
 
 int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_t ld_a, const void* w,
-               const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace, size_t,
-               void* stream) {
-  constexpr int64_t kMost = (int64_t)1 << 26;  // rows: tile indexes and offsets in a tile's rows fit 32 bits
-  constexpr int64_t kMostLd = (int64_t)1 << 22;  // 256 rows are less than 2^32 bytes
-  if (M < 0 || N <= 0 || K <= 0 || M >= kMost || N >= kMost || M * N >= (int64_t)1 << 40) return SSD_E_SHAPE;
-  if (ld_a < K || ld_a >= kMostLd) return SSD_E_SHAPE;
-  if (!known_dtype(dtype) || (out_dtype != dtype && out_dtype != SSD_DTYPE_F32)) return SSD_E_UNSUPPORTED;
+               const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  int rc = check_product(M, N, K, dtype);
+  if (rc) return rc;
+  if (ld_a < K || ld_a >= (int64_t)1 << 22) return SSD_E_SHAPE;
+  if (out_dtype != dtype && out_dtype != SSD_DTYPE_F32) return SSD_E_UNSUPPORTED;
   if (act < SSD_ACT_NONE || act > SSD_ACT_GELU_TANH) return SSD_E_UNSUPPORTED;
   if (!a || !w || !out) return SSD_E_NULL;
   if (!aligned_to(a, elem_bytes(dtype)) || !aligned_to(bias, 4)) return SSD_E_ALIGN;
-  const int rc = check_opt({w, residual, out, workspace});
-  if (rc) return rc;
+  if ((rc = check_opt({w, residual, out, workspace}))) return rc;
   if (M == 0) return SSD_OK;
   ssd::MatmulArgs m{M, N, K, a, ld_a, w, bias, act, residual, out};
-  return hip_status(ssd::launch_matmul(dtype, out_dtype, m, (hipStream_t)stream));
+  if (workspace && !ssd::matmul_aligned(dtype, m) && workspace_bytes < ssd::matmul_workspace_bytes(M, N, K, dtype))
+    return SSD_E_WORKSPACE;
+  return hip_status(ssd::launch_matmul(dtype, out_dtype, m, workspace, (hipStream_t)stream));
 }
 
 int ssd_block_norm(int64_t rows, int64_t cols, int dtype, const void* x, int64_t ld_x, const float* post_weight,

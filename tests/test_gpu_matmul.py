@@ -22,7 +22,7 @@ def _np(t):
     return t.detach().double().cpu().numpy()
 
 
-def run(L, torch, M, N, K, dtype, out, act, bias, residual, cut, seed=3, same=False):
+def run(L, torch, M, N, K, dtype, out, act, bias, residual, cut, seed=3, same=False, room_for=False):
     g = torch.Generator(device="cuda").manual_seed(seed)
     r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
     td, to = getattr(torch, DT[dtype]), getattr(torch, DT[out])
@@ -36,7 +36,11 @@ def run(L, torch, M, N, K, dtype, out, act, bias, residual, cut, seed=3, same=Fa
     o.fill_(float("nan"))
     if same and residual:
         o.copy_(res)
-    L.ssd_matmul(a, w, b, o, act=ACTS.index(act), residual=o if same and residual else res)
+    ws = L.ssd_matmul_workspace(a, w, o) if room_for else None
+    if room_for:
+        assert ws is not None
+        ws.fill_(0xff)  # NaN
+    L.ssd_matmul(a, w, b, o, act=ACTS.index(act), residual=o if same and residual else res, workspace=ws)
     torch.cuda.synchronize()
     A, W = _np(a), _np(w)
     v = A @ W.T
@@ -92,3 +96,23 @@ def test_matmul(gpu_lib, case, same):
     import torch
     print("product", case, same, flush=True)
     run(gpu_lib, torch, *case, same=same)
+
+
+# rows of no alignment that are copied into aligned ones: both operands, and a alone
+PACKED = [
+    (64, 200, 300, "fp16", "fp16", "relu2", True, False, 1),
+    (64, 1, 65, "bf16", "fp32", "none", False, False, 0),
+    (333, 1000, 512, "bf16", "bf16", "gelu", True, True, 3),
+    (1100, 1300, 135, "bf16", "fp32", "gelu_tanh", True, True, 0),
+    (4100, 4101, 515, "fp16", "fp32", "none", True, True, 7),
+    (300, 700, 91, "fp32", "fp32", "silu", True, True, 1),
+    (257, 514, 64, "fp32", "fp32", "gelu", False, True, 5),
+]
+
+
+@pytest.mark.parametrize("case", PACKED, ids=lambda c: "-".join(map(str, c)))
+def test_matmul_with_room_for_aligned_rows(gpu_lib, case):
+    import torch
+    print("packed product", case, flush=True)
+    run(gpu_lib, torch, *case, room_for=True)
+    run(gpu_lib, torch, *case, room_for=True, same=True)

@@ -372,7 +372,8 @@ typedef struct ssd_conv {
  * position 0, count as zero and need nothing in conv_state. On return
  * conv_state holds the last width inputs up to the sequence's end; slots of
  * older positions stay as they were. The caller then adds the lengths to pos.
- * B * Cd < 2^32, ld_xbc and ld_dt < 2^28 (SSD_E_SHAPE otherwise). */
+ * B * Cd < 2^32, ld_xbc and ld_dt < 2^28 (SSD_E_SHAPE otherwise). headdim may also
+ * be 128 (the heads of ssd_delta_forward). */
 int ssd_conv_forward(const ssd_shape* shape, const ssd_conv* conv, const void* xbc,
                      int64_t ld_xbc, const void* dt_raw, int64_t ld_dt, const int32_t* lengths,
                      const int32_t* pos, void* conv_state, void* X, void* B, void* C, void* dt,
@@ -460,7 +461,7 @@ int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w
  * state unchanged. Sums, decays and states are fp32 or more; Y is rounded once.
  * |b_t| |k_t|^2 <= 2 keeps the state bounded; that is not checked.
  * shape->chunk and shape->schedule have no influence, but must be supported values;
- * batch * nheads < 2^24 (SSD_E_SHAPE). scale must be finite, eps >= 0 and finite
+ * batch * nheads < 2^23 (SSD_E_SHAPE). scale must be finite, eps >= 0 and finite
  * (SSD_E_SHAPE); unknown flags return SSD_E_UNSUPPORTED. */
 enum { SSD_DELTA_UNIT = 1, SSD_DELTA_LOGIT = 2 };
 

@@ -75,7 +75,7 @@ int ssd_conv_forward(const ssd_shape* shape, const ssd_conv* conv, const void* x
                      void* conv_state, void* X, void* B, void* C, void* dt, void* stream) {
   Dims d;
   bool empty;
-  int rc = check_shape(shape, &d, &empty);
+  int rc = check_shape(shape, &d, &empty, true);
   if (rc) return rc;
   if ((rc = check_conv(d, shape->dtype, conv, xbc, ld_xbc, dt_raw, ld_dt, pos))) return rc;
   if ((rc = check_ptrs({X, B, C, dt}))) return rc;

@@ -28,7 +28,7 @@ int delta_shape(const ssd_shape* shape, Dims* d, bool* empty) {
   const int rc = check_shape(shape, d, empty, true);
   if (rc) return rc;
   // the grids' thread counts stay below 2^32
-  if (d->B * (int64_t)d->H >= (int64_t)1 << 24) return SSD_E_SHAPE;
+  if (d->B * (int64_t)d->H >= (int64_t)1 << 23) return SSD_E_SHAPE;
   d->c = (int)((d->L + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk);
   int64_t t, u;
   if (!mul_ok(d->B, d->c, &t) || !mul_ok(t, d->H, &u) || !mul_ok(u, 1 << 15, &u) || !mul_ok(t, d->G, &u) ||

@@ -26,7 +26,7 @@ def run(L, torch, M, N, K, dtype, out, act, bias, residual, cut, seed=3, same=Fa
     g = torch.Generator(device="cuda").manual_seed(seed)
     r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
     td, to = getattr(torch, DT[dtype]), getattr(torch, DT[out])
-    wide = r(M, K + cut + (3 if cut else 0)).to(td)
+    wide = r(M, K + cut + (0 if not cut else 3 if cut % 8 else 8)).to(td)  # cut of whole 16 bytes: rows stay aligned
     a, w = wide[:, cut:cut + K], (2 * r(N, K) / K ** 0.5).to(td)
     b = r(N) if bias else None
     res = (2 * r(M, N)).to(to) if residual else None
@@ -96,6 +96,23 @@ def test_matmul(gpu_lib, case, same):
     import torch
     print("product", case, same, flush=True)
     run(gpu_lib, torch, *case, same=same)
+
+
+# aligned rows that reach every kernel of the 16-bit dispatch (K in bytes halved)
+SIZES = [(333, 8512, 1024), (1, 16, 1024), (1, 3870, 256), (3, 4281, 768), (2, 4427, 536), (1, 5236, 1544), (16, 9000, 1800), (2245, 33, 256),
+         (2140, 33, 8), (18, 3004, 776), (103, 6937, 264), (99, 7287, 512), (41, 11479, 808), (333, 2560, 2560),
+         (333, 2560, 2568), (333, 8512, 1032), (384, 3864, 432), (4099, 2571, 2568), (3000, 10576, 520), (687, 11060, 768),
+         (1790, 4864, 2512), (900, 4608, 768), (2600, 2570, 128), (2100, 2600, 512), (4100, 4120, 1024), (4100, 8200, 640)]
+KERNELS = [(m, n, k, ("fp16", "bf16")[i % 2], ("fp16", "bf16")[i % 2] if i % 3 else "fp32", ACTS[i % 7], i % 2 == 0, True,
+            (0, 8)[i % 4 == 3]) for i, (m, n, k) in enumerate(SIZES)]
+
+
+@pytest.mark.parametrize("case", KERNELS, ids=lambda c: "-".join(map(str, c)))
+def test_matmul_every_kernel(gpu_lib, case):
+    import torch
+    print("product", case, flush=True)
+    run(gpu_lib, torch, *case)
+    run(gpu_lib, torch, *case, same=True)
 
 
 # rows of no alignment that are copied into aligned ones: both operands, and a alone

@@ -595,7 +595,7 @@ struct Chain {
   static constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
   static constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
   v4f s[NT], ks[4], qs[4], u[4];
-  v8h wt[6], wl[6];  // T's fragments
+  v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
   float inv_s, inv_r, max_s, max_u, one;
   int place;  // of the lane's column in a row of the workgroup's
 
@@ -660,13 +660,15 @@ struct Chain {
     }
     max_s = column_max(tiles_max(s));
   }
-  // T's fragments, for what follows
-  __device__ __forceinline__ void read_t(const char* t_frags) {
+  // T's fragments and Y's weights', for what follows
+  __device__ __forceinline__ void read_head(const char* frags) {
 #pragma unroll
     for (int n = 0; n < 6; ++n) {
-      wt[n] = frag(t_frags, n);
-      wl[n] = frag(t_frags, 6 + n);
+      wt[n] = frag(frags, HeadPlan<DT>::kT + n);
+      wl[n] = frag(frags, HeadPlan<DT>::kT + 6 + n);
     }
+#pragma unroll
+    for (int n = 0; n < 6 * AP; ++n) wa[n] = frag(frags, HeadPlan<DT>::kA + n);
   }
   // R = V - e^g K S^T, in the place of K S^T; values: V's rows, of W waves' columns.
   template <int W>
@@ -715,13 +717,11 @@ struct Chain {
   // the products added to the scaled state: its largest value is brought to 2^8 and U's
   // part to 2 at most, so that the sums (64 terms, keys up to 2^8) stay below 2^16 as
   // fp16's range asks.
-  __device__ __forceinline__ void outputs_and_state(const char* a_frags, const char* turned, const Factors& f, T* stage, char* out,
+  __device__ __forceinline__ void outputs_and_state(const char* turned, const Factors& f, T* stage, char* out,
                                                     uint32_t step, int left) {
     const int sub = lane_id() >> 4;
-    v8h w[6 * AP], k[2][NT];
+    v8h k[2][NT];
     v4f fu[4];
-#pragma unroll
-    for (int n = 0; n < 6 * AP; ++n) w[n] = frag(a_frags, n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) fu[i] = *(const v4f*)(f.fac_u + 16 * i + 4 * sub);
     const v4f inv_t = *(const v4f*)f.inv_t, inv_a = *(const v4f*)f.inv_a;
@@ -736,20 +736,20 @@ struct Chain {
       for (int t = 0; t < 2; ++t)
         split_tiles(u[2 * t], u[2 * t + 1], inv_t[2 * t] * sy.by, inv_t[2 * t + 1] * sy.by, hi[t], lo[t]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 0)], hi[0], (v4f)(0.f));
+      for (int i = 0; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 0)], hi[0], (v4f)(0.f));
 #pragma unroll
-      for (int i = 2; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 1)], hi[1], y[i]);
+      for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], hi[1], y[i]);
       if constexpr (UY == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 0)], lo[0], y[i]);
+        for (int i = 0; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 0)], lo[0], y[i]);
 #pragma unroll
-        for (int i = 2; i < 4; ++i) y[i] = mma16(w[lower_frag(i, 1)], lo[1], y[i]);
+        for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], lo[1], y[i]);
       }
       if constexpr (AP == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mma16(w[6 + lower_frag(i, 0)], hi[0], y[i]);
+        for (int i = 0; i < 4; ++i) y[i] = mma16(wa[6 + lower_frag(i, 0)], hi[0], y[i]);
 #pragma unroll
-        for (int i = 2; i < 4; ++i) y[i] = mma16(w[6 + lower_frag(i, 1)], hi[1], y[i]);
+        for (int i = 2; i < 4; ++i) y[i] = mma16(wa[6 + lower_frag(i, 1)], hi[1], y[i]);
       }
     }
     const float was = inv_s;
@@ -852,8 +852,9 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, const char* 
 // fragments and V's rows come through LDS.
 //   DEEP: two buffers of each; the next chunk's copies are on their way all the while,
 //   with one barrier a chunk. One workgroup on a CU.
-//   Otherwise one, in two halves, K and Q, and the rest: the copies of the next chunk's
-//   half are on their way while the other half is used, with a barrier in between. Two
+//   Otherwise one, in three parts, that are free and copied anew one after the other: K
+//   and Q after the products with them, T, Y's weights and V once they are in registers
+//   (the factors have two buffers), K^T at the chunk's end, with barriers in between. Two
 //   workgroups on a CU (16-bit types), which cover one another's waits.
 template <int DT, int N, int W, bool DEEP>
 __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) void k_delta_scan(
@@ -861,12 +862,14 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
   typedef KeyPlan<DT, N> KP_;
   typedef HeadPlan<DT> HP_;
   typedef typename Store<DT>::T T;
-  constexpr int kFirst = KP_::kT * kFrag, kRest = (KP_::kTurned + HP_::kFrags) * kFrag, kValues = kC * kRowBytes<DT, W>;
+  constexpr int kFirst = KP_::kT * kFrag, kTurned = KP_::kTurned * kFrag, kHead = HP_::kFac * kFrag;
+  constexpr int kValues = kC * kRowBytes<DT, W>;
   // separate objects, so that the compiler sees that a read of one need not wait for
   // the copies into another
-  __shared__ __attribute__((aligned(1024))) char first0[kFirst], rest0[kRest], values0[kValues];
-  __shared__ __attribute__((aligned(1024))) char first1[DEEP ? kFirst : 16], rest1[DEEP ? kRest : 16];
-  __shared__ __attribute__((aligned(1024))) char values1[DEEP ? kValues : 16];
+  __shared__ __attribute__((aligned(1024))) char first0[kFirst], turned0[kTurned], head0[kHead], values0[kValues];
+  __shared__ __attribute__((aligned(1024))) char first1[DEEP ? kFirst : 16], turned1[DEEP ? kTurned : 16];
+  __shared__ __attribute__((aligned(1024))) char head1[DEEP ? kHead : 16], values1[DEEP ? kValues : 16];
+  __shared__ __attribute__((aligned(1024))) char factors0[kFrag], factors1[kFrag];
   __shared__ __attribute__((aligned(1024))) T stage[W][kC / 2 * 16];
   constexpr int E = sizeof(T);
   const int wv = wave_id();
@@ -877,28 +880,35 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
   const char* const x = (const char*)a.X + ((b * L * H + h) * P + start) * E;
   char* const y = (char*)a.Y + ((b * L * H + h) * P + start + wv * 16) * E;
   const char* const keys = ws + (b * G + h / hpg) * (int64_t)chunks * KP_::kBytes;
-  const char* const head = ws_heads + unit * (int64_t)chunks * HP_::kBytes;
+  const char* const heads = ws_heads + unit * (int64_t)chunks * HP_::kBytes;
   auto left = [&](int i) { return (int)min(L - (int64_t)i * kC, (int64_t)kC); };
   auto copy_first = [&](int i, char* to) { copy_frags<KP_::kT, W>(keys + i * (int64_t)KP_::kBytes, to, wv); };
-  auto copy_rest = [&](int i, char* to, char* values) {
+  auto copy_turned = [&](int i, char* to) {
     copy_frags<KP_::kTurned, W>(keys + i * (int64_t)KP_::kBytes + KP_::kT * kFrag, to, wv);
-    copy_frags<HP_::kFrags, W>(head + i * (int64_t)HP_::kBytes, to + KP_::kTurned * kFrag, wv);
+  };
+  auto copy_head = [&](int i, char* to, char* factors, char* values) {
+    copy_frags<HP_::kFac, W>(heads + i * (int64_t)HP_::kBytes, to, wv);
+    if (wv == W - 1) copy_frag(heads + i * (int64_t)HP_::kBytes + HP_::kFac * kFrag + lane_id() * 16, factors);
     copy_values<DT, W>(x + i * (kC * (int64_t)step), step, left(i), values, wv);
   };
   copy_first(0, first0);
-  copy_rest(0, rest0, values0);
+  copy_turned(0, turned0);
+  copy_head(0, head0, factors0, values0);
   Chain<DT, N> c;
   c.init(a, unit, P, p);
   meet<0>();
-  // chunk i, from one set of buffers; the next one's go to `first`, `rest` and `vals`
-  auto chunk = [&](int i, const char* kq, const char* others, const char* values, char* first, char* rest,
-                   char* vals) __attribute__((always_inline)) {
+  // Chunk i, from one set of buffers; the next one's go to first, turned, head, factors
+  // and vals. Where copies are, this chunk is whole, and a wave's newest memory operations
+  // are the E stores of Y, after at least kHeadCopies of copy_head.
+  constexpr int kHeadCopies = HP_::kFac / W + E;
+  auto chunk = [&](int i, const char* kq, const char* kt, const char* frags, const char* fac, const char* values, char* first,
+                   char* turned, char* head, char* factors, char* vals) __attribute__((always_inline)) {
     const bool more = i + 1 < chunks;
-    const char* const frags = others + KP_::kTurned * kFrag;
-    const Factors& f = *(const Factors*)(frags + HP_::kFac * kFrag);
+    const Factors& f = *(const Factors*)fac;
     if (DEEP && more) {
       copy_first(i + 1, first);
-      copy_rest(i + 1, rest, vals);
+      copy_turned(i + 1, turned);
+      copy_head(i + 1, head, factors, vals);
       asm volatile("" ::: "memory");
     }
     c.products(kq);
@@ -906,22 +916,26 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
       meet<0>();
       if (more) copy_first(i + 1, first);
     }
-    c.read_t(frags + HP_::kT * kFrag);
+    c.read_head(frags);
     c.template remainders<W>(values, f);
-    c.changes(f);
-    c.outputs_and_state(frags + HP_::kA * kFrag, others, f, stage[wv], y + i * (kC * (int64_t)step), step, left(i));
-    // the E stores of Y are the newest, and may be under way still (the last chunk, which
-    // may have fewer, waits for no copies)
-    meet<E>();
-    if (!DEEP && more) copy_rest(i + 1, rest, vals);
-  };
-  if constexpr (DEEP) {
-    for (int i = 0; i < chunks; i += 2) {
-      chunk(i, first0, rest0, values0, first1, rest1, values1);
-      if (i + 1 < chunks) chunk(i + 1, first1, rest1, values1, first0, rest0, values0);
+    if constexpr (!DEEP) {
+      meet<64>();
+      if (more) copy_head(i + 1, head, factors, vals);
+      asm volatile("" ::: "memory");
     }
-  } else {
-    for (int i = 0; i < chunks; ++i) chunk(i, first0, rest0, values0, first0, rest0, values0);
+    c.changes(f);
+    c.outputs_and_state(kt, f, stage[wv], y + i * (kC * (int64_t)step), step, left(i));
+    meet<DEEP ? E : kHeadCopies + E>();
+    if (!DEEP && more) copy_turned(i + 1, turned);
+  };
+  for (int i = 0; i < chunks; i += 2) {
+    if constexpr (DEEP) {
+      chunk(i, first0, turned0, head0, factors0, values0, first1, turned1, head1, factors1, values1);
+      if (i + 1 < chunks) chunk(i + 1, first1, turned1, head1, factors1, values1, first0, turned0, head0, factors0, values0);
+    } else {
+      chunk(i, first0, turned0, head0, factors0, values0, first0, turned0, head0, factors1, values0);
+      if (i + 1 < chunks) chunk(i + 1, first0, turned0, head0, factors1, values0, first0, turned0, head0, factors0, values0);
+    }
   }
   c.finish(a, unit, P, p);
 }

@@ -90,6 +90,9 @@ CASES = [
     (2, 40, 520, 32, 16, 1, "fp32", True, True, True, 0),
     (8, 33, 128, 32, 32, 128, "fp32", False, False, True, 0),
     (8, 18, 128, 32, 64, 1, "fp32", True, True, True, 0),
+    # few positions of many heads: chunks from 9 positions on
+    (16, 8, 64, 64, 128, 1, "fp16", True, True, True, 0),
+    (16, 9, 64, 64, 128, 1, "fp16", True, True, True, 0),
 ]
 
 

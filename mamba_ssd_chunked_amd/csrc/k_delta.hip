@@ -373,7 +373,9 @@ __device__ __forceinline__ double row_add(double v) {
 }
 __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float A) {
   const int lane = lane_id(), sub = lane >> 4;
-  double gs = row_add<8>(row_add<4>(row_add<2>(row_add<1>((double)in.dt * ((double)A * 1.4426950408889634)))));
+  double log_a = (double)in.dt * ((double)A * 1.4426950408889634);
+  log_a = log_a < -0x1p100 ? -0x1p100 : log_a;  // 2^log_a is 0 either way, and sums stay in fp32's range
+  double gs = row_add<8>(row_add<4>(row_add<2>(row_add<1>(log_a))));
   double end[4];  // of each 16 positions
   end[0] = lane_value(gs, 15);
   end[1] = end[0] + lane_value(gs, 31);
@@ -858,7 +860,8 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, const char* 
 //   workgroups on a CU (16-bit types), which cover one another's waits.
 template <int DT, int N, int W, bool DEEP>
 __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) void k_delta_scan(
-    DeltaArgs a, const char* ws, const char* ws_heads, int64_t L, int H, int G, int hpg, int P, int chunks) {
+    DeltaArgs a, const char* ws, const char* ws_heads, int64_t L, int H, int G, int hpg, int P, int chunks,
+    bool gather) {
   typedef KeyPlan<DT, N> KP_;
   typedef HeadPlan<DT> HP_;
   typedef typename Store<DT>::T T;
@@ -873,9 +876,12 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
   __shared__ __attribute__((aligned(1024))) T stage[W][kC / 2 * 16];
   constexpr int E = sizeof(T);
   const int wv = wave_id();
-  const int slices = P / (16 * W);
-  const int64_t unit = blockIdx.x / slices, b = unit / H;
-  const int h = (int)(unit % H), start = (int)(blockIdx.x % slices) * W * 16, p = start + wv * 16 + (lane_id() & 15);
+  // Consecutive workgroups go to the eight XCDs in turn. With `gather` each XCD takes a
+  // contiguous run of the slices.
+  const int slices = P / (16 * W), xcd = blockIdx.x % 8, per = (int)gridDim.x / 8, extra = (int)gridDim.x % 8;
+  const int place = gather ? xcd * per + min(xcd, extra) + (int)blockIdx.x / 8 : (int)blockIdx.x;
+  const int64_t unit = place / slices, b = unit / H;
+  const int h = (int)(unit % H), start = place % slices * W * 16, p = start + wv * 16 + (lane_id() & 15);
   const uint32_t step = (uint32_t)H * P * E;  // between rows: 64 of them are less than 2^32 bytes
   const char* const x = (const char*)a.X + ((b * L * H + h) * P + start) * E;
   char* const y = (char*)a.Y + ((b * L * H + h) * P + start + wv * 16) * E;
@@ -946,15 +952,20 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
 template <int DT, int N, int W>
 hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, int64_t ncu, hipStream_t st) {
   const int64_t wgs = d.B * d.H * (d.P / (16 * W));
+  // Slices of a head share its fragments, and heads of a group the keys': one XCD's L2
+  // serves them where that is one's own (us with and without: 4 x 4096 positions of 32 heads of
+  // 128 x 128 358 and 369; 8 x 2048 of 80 of 64 x 128 391 and 396), but not where all XCDs
+  // read one group's keys either way (2048 of 64 heads 115 and 112).
+  const bool gather = d.P > 16 * W || d.B * d.G >= 8;
   if constexpr (DT != DT_F32) {
     if (wgs <= ncu) {
       hipLaunchKernelGGL((k_delta_scan<DT, N, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
-                         d.G, d.hpg, d.P, d.c);
+                         d.G, d.hpg, d.P, d.c, gather);
       return hipGetLastError();
     }
   }
   hipLaunchKernelGGL((k_delta_scan<DT, N, W, false>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
-                     d.G, d.hpg, d.P, d.c);
+                     d.G, d.hpg, d.P, d.c, gather);
   return hipGetLastError();
 }
 

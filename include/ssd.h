@@ -458,8 +458,9 @@ int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w
  * H values in shape->dtype, so that a part of In Proj's rows is read in place (element
  * aligned, ld_beta >= H and < 2^28). States [B, H, P, N] fp32. Positions with dt = 0
  * and a key of zeros (as ssd_conv_forward writes behind a sequence's end) leave the
- * state unchanged. Sums, decays and states are fp32 or more; Y is rounded once.
- * |b_t| |k_t|^2 <= 2 keeps the state bounded; that is not checked.
+ * state unchanged; beta counts as 0 where the key is zeros, NaN and infinities too.
+ * Sums, decays and states are fp32 or more; Y is rounded once.
+ * |b_t| |k_t|^2 <= 2 keeps the state bounded; that is not checked, nor is dt A <= 0.
  * shape->chunk and shape->schedule have no influence, but must be supported values;
  * batch * nheads < 2^23 (SSD_E_SHAPE). scale must be finite, eps >= 0 and finite
  * (SSD_E_SHAPE); unknown flags return SSD_E_UNSUPPORTED. */

@@ -289,12 +289,13 @@ __global__ __launch_bounds__(256) void k_delta_keys(DeltaArgs a, char* ws, int64
       ss = group_sum<4>(ss);
       if (s == 0) {
         float f = sc.inv;
+        const bool zeros = ss == 0.f;
         if (a.unit) {
           const float eps = a.eps * sc.by * sc.by;
           ss += eps;
-          // a row of zeros without eps stays zeros; next to a far larger eps the row counts for nothing
-          f = eps > 0x1p126f ? sc.inv * rsqrtf(a.eps) : ss > 0.f ? rsqrtf(ss) : 0.f;
+          f = eps > 0x1p126f ? sc.inv * rsqrtf(a.eps) : rsqrtf(ss);  // next to a far larger eps the row counts for nothing
         }
+        if (zeros) f = 0.f;  // and a key of zeros is known by its factor
         ((float*)(out + KP_::kFac * kFrag))[which * kC + row] = which ? f * a.scale : f;
       }
       if (s < KS) {
@@ -352,9 +353,10 @@ struct GateInputs {
     const bool live = pos0 + lane_id() < L;
     const int64_t row = row0 + pos0 + lane_id();
     dt = live ? ld_f<DT>(a.dt, row * H + h) : 0.f;
-    beta = live ? delta_beta<DT>(a, row, h) : 0.f;
     fk = fac[lane_id()];
     fq = fac[kC + lane_id()];
+    // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
+    beta = live && fk != 0.f ? delta_beta<DT>(a, row, h) : 0.f;
   }
 };
 // A lane's value of a double, the same in all lanes.

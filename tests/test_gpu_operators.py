@@ -111,6 +111,51 @@ def test_delta_positions_that_change_nothing(gpu_lib):
         assert np.abs(_np(fin) - s).max() <= 2.0 ** -20 * np.abs(s).max()
 
 
+@pytest.mark.parametrize("unit", (True, False))
+@pytest.mark.parametrize("eps", (0.0, 1e-6))
+def test_delta_beta_of_zero_keys(gpu_lib, unit, eps):
+    """Whatever stands in beta where the key is zeros, as behind the ends of padded
+    sequences, changes nothing: the same bits as with ones there."""
+    import torch
+    L = gpu_lib
+    for dtype in ("fp32", "fp16"):
+        for n, logit in ((7, True), (100, False), (130, True)):
+            c = D.make(torch, 31, 3, n, 4, 32, 64, 2, dtype, unit=unit, logit=logit)
+            for b, end in enumerate((n, n // 2, 1)):
+                for k in ("X", "dt", "K", "Q"):
+                    c[k][b, end:] = 0
+            wide = c["beta"]
+            y, s, ymag, smag = D.reference(c, 0.3, unit, logit, True, eps=1e-30 if eps == 0 else eps)
+            ones = forward(L, torch, c, unit=unit, logit=logit, eps=eps)
+            for bad in (NAN, float("inf"), float("-inf")):
+                c["beta"] = wide.clone()
+                for b, end in enumerate((n, n // 2, 1)):
+                    c["beta"][b, end:] = bad
+                Y, fin = forward(L, torch, c, unit=unit, logit=logit, eps=eps)
+                assert torch.equal(Y, ones[0]) and torch.equal(fin, ones[1]), (dtype, n, bad)
+            D.check(_np(ones[1]), s, smag, "fp32", 2.0 ** -13, 2.0 ** -18, "state")
+            D.check(_np(ones[0]), y, ymag, dtype, D.Y_TAU[dtype], D.Y_NORM[dtype], "y")
+            assert not ones[0][1, n // 2:].any()
+
+
+def test_delta_decays_out_of_range(gpu_lib):
+    """dt A below fp32's range: everything before is forgotten, at the ends of the 16 and
+    64 positions as within them."""
+    import torch
+    L = gpu_lib
+    for n in (7, 150):
+        c = D.make(torch, 33, 1, n, 2, 16, 32, 1, "fp32")
+        c["A"][:] = -3e38
+        at = [p for p in (0, 3, 5, 15, 16, 40, 63, 64, 100, 101) if p < n]
+        c["dt"].zero_()
+        c["dt"][:, at] = 3e38
+        Y, fin = forward(L, torch, c)
+        ref = dict(c, dt=c["dt"] * (1e-32 / 3), A=c["A"] * (1e-34 / 3))  # -1e10: forgotten as well
+        y, s, ymag, smag = D.reference(ref, 0.3, True, True, True)
+        D.check(_np(fin), s, smag, "fp32", 2.0 ** -13, 2.0 ** -18, "state")
+        D.check(_np(Y), y, ymag, "fp32", D.Y_TAU["fp32"], D.Y_NORM["fp32"], "y")
+
+
 @pytest.mark.parametrize("dtype", ("fp32", "bf16"))
 def test_delta_sizes_of_keys_and_values(gpu_lib, dtype):
     """Keys and queries of any size are taken to length 1; values far from 1 in either

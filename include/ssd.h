@@ -470,7 +470,8 @@ enum { SSD_DELTA_UNIT = 1, SSD_DELTA_LOGIT = 2 };
  * final_state (NULL: not wanted) receives the one after the last; they may be the
  * same buffer. With seqlen == 0 and batch > 0 final_state is a copy of initial_state
  * (or zeros), and X, dt, B, C, beta and Y are not looked at. workspace: device memory
- * of at least ssd_delta_workspace_bytes(shape) bytes (may be NULL when that is 0). */
+ * of at least ssd_delta_workspace_bytes(shape) bytes (may be NULL when that is 0); calls
+ * that may overlap, on other streams or in graphs, each need their own. */
 int ssd_delta_forward(const ssd_shape* shape, int flags, const void* X, const void* dt, const float* A,
                       const void* B, const void* C, const void* beta, int64_t ld_beta, float scale, float eps,
                       void* Y, const float* initial_state, float* final_state, void* workspace,
@@ -510,8 +511,8 @@ enum {
  * Any K. Rows of a and w that are 16-byte aligned and a multiple of 16 bytes long are
  * taken as they are, and need no workspace. For others it is optional: device memory,
  * 16-byte aligned, of at least ssd_matmul_workspace_bytes(M, N, K, dtype) bytes (fewer:
- * SSD_E_WORKSPACE), into which they are copied; with NULL they are read as they lie,
- * which is slower for more than a few rows. */
+ * SSD_E_WORKSPACE), into which 16-bit ones are copied; with NULL they are read as they
+ * lie, which is slower. Calls that may overlap each need a workspace of their own. */
 int ssd_matmul(int64_t M, int64_t N, int64_t K, int dtype, const void* a, int64_t ld_a, const void* w,
                const float* bias, int act, const void* residual, int out_dtype, void* out, void* workspace,
                size_t workspace_bytes, void* stream);

@@ -138,20 +138,22 @@ hipError_t go(const Dims& d, const DeltaArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Passes of a wave: all of a head's up to 16 where that leaves waves enough, a
-// quarter of them where heads are few.
+// Passes of a wave: four, fewer where that leaves CUs without 8 waves (us of a step at 1,
+// 2, 4, 8 and 16 passes, heads of 64 x 128: 64 heads 4.1, 4.0, 4.1, 4.6 and 5.6; 320 heads
+// 8.9, 6.8, 5.7, 6.1 and 6.6; 20480 heads 362, 220, 221, 241 and 234); eight for more
+// than one position where waves are many, which share a position's loads and sums
+// (5120 heads, 8 positions: 132 at 4, 111 at 8, 134 at 16; 640 heads 21.4, 21.8 and 27).
 template <int DT, int N>
 hipError_t pick(const Dims& d, const DeltaArgs& a, hipStream_t st) {
   const int all = d.P * N / 256;  // passes of a head: 1 to 64
-  const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
-  int el = all < 16 ? all : 16;
-  while (el > 1 && d.B * d.H * (all / el) < 8 * ncu) el /= 2;
+  const int64_t ncu = cu_count() > 0 ? cu_count() : 256, bh = d.B * (int64_t)d.H;
+  int el = d.L > 1 && bh * (all / 8) >= 32 * ncu ? 8 : 4;
+  while (el > 1 && (el > all || bh * (all / el) < 8 * ncu)) el /= 2;
   switch (el) {
     case 1: return go<DT, N, 1>(d, a, st);
     case 2: return go<DT, N, 2>(d, a, st);
     case 4: return go<DT, N, 4>(d, a, st);
-    case 8: return go<DT, N, 8>(d, a, st);
-    default: return go<DT, N, 16>(d, a, st);
+    default: return go<DT, N, 8>(d, a, st);
   }
 }
 

@@ -7,10 +7,19 @@
 // Rows that are 16-byte aligned and long take the ways of the 8-bit product
 // (ssd_matmul.hpp): a 128-byte step is 64 positions of 16-bit rows, with the same matrix
 // cycles, LDS reads and copies as 128 of 8-bit ones, and the same choice of kernel by
-// the rows' bytes. Others are copied into aligned rows first where the caller gives room
-// for them, and the rows of a are many enough to be worth a pass over w; or they go
-// through registers, in pieces of 16 bytes at any element's address, the last of a row
-// element by element.
+// the rows' bytes. Others go through registers, in pieces of 16 bytes at any element's
+// address, the last of a row element by element; or, where the caller gives room for it,
+// 16-bit ones are copied into aligned rows first: loads at odd multiples of 2 bytes cost
+// more than a pass over w does (fp32 rows, whose loads are at multiples of 4 bytes, lose by
+// it: 1065 x 4099 x 2579 337 us against 231).
+//
+// us, and the sum's rate (a large library product: 1500 TF in fp16, 1600 in bf16; a
+// copy: 5.1 TB/s):
+//   8 x 2560 x 5120 bf16          6.6, bound by w: 4.0 TB/s
+//   333 x 8512 x 2048 bf16        18.7, 620 TF; 201 blocks of 128 for 256 CUs
+//   16384 x 10576 x 2560 bf16     805, 1100 TF; products, 8 waves' barriers between them
+//   4096 x 4096 x 1024 fp32       243, 141 TF of 153
+//   1065 x 4099 x 2579 bf16, with bias, GELU and an fp32 residual  62, of which the copies 12
 #include "ssd_act.hpp"
 #include "ssd_launch.hpp"
 #include "ssd_matmul.hpp"
@@ -408,33 +417,40 @@ hipError_t launch_any_rows(const MatmulArgs& g, hipStream_t st) {
 }
 
 // Elements of an aligned copy's rows.
-template <int DT>
-int64_t packed_cols(int64_t K) {
-  constexpr int64_t E = sizeof(typename Store<DT>::T);
-  return K * E % 16 == 0 ? K : (K * E + 127) / 128 * 128 / E;
-}
+int64_t packed_cols(int64_t K) { return K % 8 == 0 ? K : (K + 63) / 64 * 64; }
 
 template <int DT, int OT>
 hipError_t launch(MatmulArgs g, void* ws, hipStream_t st) {
   const int64_t ncu = cu_count() > 0 ? cu_count() : 256;
   constexpr int64_t E = sizeof(typename Store<DT>::T);
   if (!matmul_aligned(DT, g)) {
-    if (ws && g.M >= kMatmulPackRows) {
-      // w's rows are aligned where K allows it
-      const int64_t Kp = packed_cols<DT>(g.K);
-      PackRows a{g.a, g.lda, g.M, ws}, w{g.w, g.K, Kp == g.K ? 0 : g.N, (char*)ws + g.M * Kp * E};
-      const int64_t wgs = (a.rows + w.rows + 3) / 4;
-      hipLaunchKernelGGL((k_matmul_pack<DT>), dim3((unsigned)min(wgs, (int64_t)1 << 20)), dim3(256), 0, st, a, w, (int)g.K, (int)Kp);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      g.a = ws;
-      if (w.rows) g.w = w.to;
-      g.lda = g.K = Kp;
-    } else if (g.M <= 16) {
-      return launch_any_rows<DT, OT, 1>(g, st);
-    } else if (g.M <= 32) {
-      return launch_any_rows<DT, OT, 2>(g, st);
-    } else {
+    // (us with a copy and without, bf16: 4 x 2561 x 5121 17 and 25, 32 rows 20 and 48, 64
+    // rows 21 and 57; 4 x 4099 x 2579 16 and 17, 1065 rows 51 and 69; 4 x 1001 x 1003 6.3
+    // and 6.0, 64 rows 6.7 and 12.)
+    bool packed = false;
+    if constexpr (DT != DT_F32) {
+      packed = ws && g.M >= kMatmulPackRows;
+      if (packed) {
+        // w's rows are aligned where K allows it
+        const int64_t Kp = packed_cols(g.K);
+        PackRows a{g.a, g.lda, g.M, ws}, w{g.w, g.K, Kp == g.K ? 0 : g.N, (char*)ws + g.M * Kp * E};
+        const int64_t wgs = (a.rows + w.rows + 3) / 4;
+        hipLaunchKernelGGL((k_matmul_pack<DT>), dim3((unsigned)min(wgs, (int64_t)1 << 20)), dim3(256), 0, st, a, w, (int)g.K, (int)Kp);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        g.a = ws;
+        if (w.rows) g.w = w.to;
+        g.lda = g.K = Kp;
+      }
+    }
+    if (!packed) {
+      // Rows in 16s and 32s while they and the blocks of 64 are few (us at 16s, 32s and
+      // blocks: 16 x 2561 x 5121 bf16 33, 37 and 48, 32 rows 63, 48 and 58, 48 rows 63, 94 and
+      // 57; 32 x 10577 x 2561 bf16 94, 72 and 33; fp32, where LDS and copies weigh less: 32 x
+      // 2561 x 2561 23, 19 and 61, 96 rows 45, 36 and 61; 48 x 10577 x 2561 86, 102 and 62).
+      const int64_t blocks = (g.M + 63) / 64 * ((g.N + 63) / 64);
+      if (g.M <= 16) return launch_any_rows<DT, OT, 1>(g, st);
+      if (DT == DT_F32 ? blocks < ncu / 2 : g.M <= 32 && blocks < ncu / 4) return launch_any_rows<DT, OT, 2>(g, st);
       // Blocks of 128 where each CU has one, of 16-bit rows (us with 128 and 64: 1065 x
       // 4099 x 2579 bf16 70, 93; 300 x 4099 x 2579 55, 35; 1065 x 4099 x 2579 fp32, which
       // the matrix instructions bound, 340, 231).
@@ -443,6 +459,8 @@ hipError_t launch(MatmulArgs g, void* ws, hipStream_t st) {
       return launch_any<DT, OT, 1>(g, st);
     }
   }
+  // fp32: an 8th of the rate (us with that factor and without: 1024 x 4096 x 1024 66 and 73,
+  // 333 x 8512 x 2048 122 and 132, 2048 x 2048 x 2048 127 and 136)
   switch (pick_matmul_kind(g.M, g.N, g.K * E, ncu, DT == DT_F32 ? 8.f : 1.f)) {
     case 0: return launch_rows<DT, OT, 1, 1, 8, 2>(g, st);
     case 1: return launch_rows<DT, OT, 1, 2, 4, 3>(g, st);
@@ -457,9 +475,9 @@ hipError_t launch(MatmulArgs g, void* ws, hipStream_t st) {
 }  // namespace
 
 size_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
-  if (M < kMatmulPackRows) return 0;
-  const int64_t Kp = dtype == DT_F32 ? packed_cols<DT_F32>(K) : packed_cols<DT_F16>(K);
-  return (size_t)(M + (Kp == K ? 0 : N)) * Kp * (dtype == DT_F32 ? 4 : 2);
+  if (dtype == DT_F32 || M < kMatmulPackRows) return 0;
+  const int64_t Kp = packed_cols(K);
+  return (size_t)(M + (Kp == K ? 0 : N)) * Kp * 2;
 }
 
 hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& g, void* ws, hipStream_t st) {

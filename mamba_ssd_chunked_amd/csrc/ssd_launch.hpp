@@ -189,13 +189,13 @@ struct MatmulArgs {
   const void* residual;  // [M, N] in the output's type, or null; may be out
   void* out;
 };
-// Rows that the fast kernels take as they are. Others of a are copied into aligned ones,
-// from so many on, where ws (matmul_workspace_bytes(), or null) has room for them.
+// Rows that the fast kernels take as they are. Others of 16 bits are copied into aligned
+// ones, from so many of a on, where ws (matmul_workspace_bytes(), or null) has room for them.
 inline bool matmul_aligned(int dtype, const MatmulArgs& a) {
   const int64_t e = dtype == 0 ? 4 : 2;
   return ((uintptr_t)a.a | (uintptr_t)a.w | (uintptr_t)(a.lda * e) | (uintptr_t)(a.K * e)) % 16 == 0;
 }
-constexpr int64_t kMatmulPackRows = 64;
+constexpr int64_t kMatmulPackRows = 4;
 hipError_t launch_matmul(int dtype, int out_dtype, const MatmulArgs& a, void* ws, hipStream_t st);
 size_t matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
 

@@ -1,5 +1,6 @@
 // C ABI of the operators that stand beside the SSD in a layer: the gated delta
-// rule, the product with an epilogue and the norms between two blocks. Argument validation (host only, before any launch) and dispatch to the HIP kernels.
+// rule, the product with an epilogue and the norms between two blocks. Argument
+// validation (host only, before any launch) and dispatch to the HIP kernels.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -24,7 +25,7 @@ bool known_dtype(int dtype) { return dtype >= SSD_DTYPE_F32 && dtype <= SSD_DTYP
 // a time for each position. us, in steps and in chunks: 64 heads of 64 x 128, 8 positions
 // 11.6 and 18.9, 16 17.9 and 18.9, 24 24.8 and 18.6; 4 x 32 heads of 128 x 128, 16
 // positions 23.7 and 24.4; 8 x 80 heads of 64 x 128, 8 positions 22.3 and 31.9, 16 39 and
-// 32; 64 x 80, 4 positions 89 and 131, 8 133 and 132, 16 245 and 136.
+// 32; 64 x 80, 4 positions 74 and 131, 8 111 and 132, 16 245 and 136.
 bool delta_in_steps(const Dims& d) {
   return d.L <= 8 || (d.L <= 16 && d.B * (int64_t)d.H * d.P * d.N <= (int64_t)1 << 22);
 }

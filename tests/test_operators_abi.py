@@ -114,7 +114,8 @@ def test_matmul_refusals():
     assert need == (100 + 16) * 128 * 2
     assert mm(m=100, k=65, ws=A16, wsb=need - 1) == L.SSD_E_WORKSPACE
     assert L.ssd_matmul_workspace_bytes(100, 16, 64, torch.float16) == 100 * 64 * 2  # w's rows are aligned
-    assert L.ssd_matmul_workspace_bytes(8, 16, 65, torch.float16) == 0
+    assert L.ssd_matmul_workspace_bytes(3, 16, 65, torch.float16) == 0
+    assert L.ssd_matmul_workspace_bytes(100, 16, 65, torch.float32) == 0
     assert L.LIB.ssd_matmul_workspace_bytes(100, 0, 65, 1) == 0 and L.LIB.ssd_matmul_workspace_bytes(100, 8, 65, 9) == 0
 
 
@@ -187,4 +188,4 @@ def test_binding_refuses_what_the_library_cannot_see():
     w, out = torch.zeros(16, 64, dtype=h), torch.zeros(100, 16, dtype=h)
     assert L.ssd_matmul_workspace(wide[:, 8:72], w, out) is None
     assert L.ssd_matmul_workspace(wide[:, 3:67], w, out).numel() == 100 * 64 * 2
-    assert L.ssd_matmul_workspace(wide[:8, 3:67], w, out[:8]) is None
+    assert L.ssd_matmul_workspace(wide[:3, 3:67], w, out[:3]) is None

@@ -24,6 +24,18 @@
 // queries of 16-bit types are exact in one fp16 number in that way, fp32 ones in two.
 // Products of two lower parts (2^-22 of the rest) are left out. For Y alone, which is
 // rounded to 16 bits, fewer parts do: see Parts.
+//
+// Times (us: keys, prepare, scan), heads of P x N:
+//   1 x 2048 positions, 64 heads of 64 x 128, bf16          6, 18, 91
+//   8 x 2048, 80 of 64 x 128, one group each, fp16          9, 115, 266 to 302
+//   4 x 4096, 32 of 128 x 128, 16 groups each, bf16         70, 60, 235
+// The scan is bound by its chain: about 860 instructions a chunk and wave (490 of the
+// vector unit, 104 products, 115 LDS reads) that follow one another, in 2.8 us where a
+// wave has its SIMD to itself, of which half issue nothing; two waves a SIMD issue 57 % of
+// the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 18 to 24 KB a chunk and
+// head at 3 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
+// a copy once groups are many (5.8 TB/s of read and written bytes in the last).
+// Preparing within the scan (a role for each wave, T in LDS) was no faster in total.
 #include <type_traits>
 
 #include "ssd_delta.hpp"
@@ -353,10 +365,9 @@ struct GateInputs {
     const bool live = pos0 + lane_id() < L;
     const int64_t row = row0 + pos0 + lane_id();
     dt = live ? ld_f<DT>(a.dt, row * H + h) : 0.f;
+    beta = live ? delta_beta<DT>(a, row, h) : 0.f;
     fk = fac[lane_id()];
     fq = fac[kC + lane_id()];
-    // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
-    beta = live && fk != 0.f ? delta_beta<DT>(a, row, h) : 0.f;
   }
 };
 // A lane's value of a double, the same in all lanes.
@@ -385,19 +396,21 @@ __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float
   end[3] = end[2] + lane_value(gs, 63);
   gs += sub == 0 ? 0.0 : sub == 1 ? end[0] : sub == 2 ? end[1] : end[2];
   const double own = sub == 0 ? end[0] : sub == 1 ? end[1] : sub == 2 ? end[2] : end[3];
+  // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
+  const float beta = in.fk != 0.f ? in.beta : 0.f;
   const float eg = exp2((float)gs), fu = exp2(fminf((float)(end[3] - gs), 0.f)) * in.fk;
   w.g[lane] = (float)gs;
   w.g_low[lane] = (float)(gs - (double)(float)gs);
-  w.beta[lane] = in.beta;
+  w.beta[lane] = beta;
   w.fk[lane] = in.fk;
   w.fq[lane] = in.fq;
   w.cols[lane] = exp2(fminf((float)(own - gs), 0.f)) * in.fk;
-  w.rows[3][lane] = in.beta * in.fk;
+  w.rows[3][lane] = beta * in.fk;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     const float first = exp2(fminf((float)(gs - end[q]), 0.f));
     w.first[q][lane] = first;
-    w.rows[q][lane] = in.beta * in.fk * first;
+    w.rows[q][lane] = beta * in.fk * first;
   }
   w.f.fac_k[lane] = eg * in.fk;
   w.f.fac_q[lane] = eg * in.fq;
@@ -959,6 +972,9 @@ hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char*
   // 128 x 128 358 and 369; 8 x 2048 of 80 of 64 x 128 391 and 396), but not where all XCDs
   // read one group's keys either way (2048 of 64 heads 115 and 112).
   const bool gather = d.P > 16 * W || d.B * d.G >= 8;
+  // Two buffers where a CU has one workgroup at most (us with two and one: 2048 positions of
+  // 64 heads of 64 x 128 113 and 120; 300 of 64 heads of 64 x 64 27 and 29), one where it may
+  // have two (8 x 2048 of 80 459 and 389; 4 x 1024 of 96 144 and 124). fp32 has no room for two.
   if constexpr (DT != DT_F32) {
     if (wgs <= ncu) {
       hipLaunchKernelGGL((k_delta_scan<DT, N, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,

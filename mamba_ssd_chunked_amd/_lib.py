@@ -678,14 +678,18 @@ def ssd_delta_forward(shape, X, dt, A, B, C, beta, Y, final_state=None, initial_
     ns = shape.batch * shape.nheads * shape.headdim * shape.dstate
     inputs, py = _delta_inputs(shape, X, dt, A, B, C, beta, Y, dev)
     need = ssd_delta_workspace_bytes(shape)
+    on = _stream_on(stream, dev)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        # from the stream that uses it: memory of the current stream may be in use there still, or again
+        own = torch.cuda.ExternalStream(on, device=X.device) if on else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(None if stream is None else own):
+            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
     wsb = 0 if workspace is None else workspace.numel()
     _check("ssd_delta_forward", LIB.ssd_delta_forward(
         ctypes.byref(shape), _delta_flags(unit, logit), *inputs, scale, eps, py,
         _dense(initial_state, "initial_state", ns, torch.float32, dev),
         _dense(final_state, "final_state", ns, torch.float32, dev), _dense(workspace, "workspace", wsb, torch.uint8, dev),
-        wsb, _stream_on(stream, dev)))
+        wsb, on))
     return workspace
 
 
@@ -708,7 +712,7 @@ def ssd_matmul_workspace_bytes(m, n, k, dtype) -> int:
 
 def ssd_matmul_workspace(a, w, out):
     """A workspace for ``ssd_matmul`` on tensors like these (None where it has no use for one: rows that are
-    16-byte aligned, or few)."""
+    16-byte aligned, few, or fp32)."""
     n, k = w.shape
     m = a.numel() // max(1, k)
     _, lda = _rows(a, "a", k, a.dtype, a.get_device())
@@ -721,7 +725,7 @@ def ssd_matmul_workspace(a, w, out):
 def ssd_matmul(a, w, bias, out, act=SSD_ACT_NONE, residual=None, workspace=None, stream=None):
     """out = act(a @ w.T + bias) + residual for a [..., K] (may be a column slice), w [N, K] of a's
     type; ``out`` and ``residual`` (which may be the same tensor) in that type or float32; bias float32 or
-    None. ``workspace``: from ``ssd_matmul_workspace``, for many rows that are not 16-byte aligned (None will do)."""
+    None. ``workspace``: from ``ssd_matmul_workspace``, for rows that are not 16-byte aligned (None will do)."""
     n, k = w.shape
     if a.shape[-1] != k:
         raise ValueError("a and w must agree in their last dimension")

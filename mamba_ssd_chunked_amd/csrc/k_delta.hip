@@ -35,7 +35,7 @@
 // the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 18 to 24 KB a chunk and
 // head at 3 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
 // a copy once groups are many (5.8 TB/s of read and written bytes in the last).
-// Preparing within the scan (a role for each wave, T in LDS) was no faster in total.
+// Preparing a chunk within the scan's launch was no faster in total.
 #include <type_traits>
 
 #include "ssd_delta.hpp"

@@ -111,6 +111,34 @@ def test_delta_positions_that_change_nothing(gpu_lib):
         assert np.abs(_np(fin) - s).max() <= 2.0 ** -20 * np.abs(s).max()
 
 
+def test_delta_workspace_of_another_stream(gpu_lib):
+    """A workspace that the call takes for itself is none that the current stream still uses, or
+    takes again before the call's stream is done."""
+    import torch
+    L = gpu_lib
+    c = D.make(torch, 41, 2, 700, 16, 64, 128, 1, "bf16")
+    ref = forward(L, torch, c)
+    need = L.ssd_delta_workspace_bytes(L.make_shape(2, 700, 16, 64, 128, 1, 64, "bf16"))
+    side = torch.cuda.Stream()
+    X, beta = c["X"], c["beta"].contiguous()
+    torch.cuda.synchronize()
+    for given in (side, side.cuda_stream, None):
+        busy = torch.empty(need, dtype=torch.uint8, device="cuda")
+        for i in range(200):
+            busy.fill_(0xff)
+        del busy  # the current stream's memory, to be had again by its next request
+        sh = L.make_shape(2, 700, 16, 64, 128, 1, 64, "bf16")
+        Y, fin = torch.empty_like(c["X"]), torch.empty_like(c["init"])
+        ws = L.ssd_delta_forward(sh, X, c["dt"], c["A"], c["K"], c["Q"], beta, Y, final_state=fin, initial_state=c["init"],
+                                 scale=0.3, logit=True, stream=given)
+        assert ws.numel() == need
+        del ws
+        again = torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0xff)
+        torch.cuda.synchronize()
+        assert torch.equal(Y, ref[0]) and torch.equal(fin, ref[1]), given
+        del again
+
+
 @pytest.mark.parametrize("unit", (True, False))
 @pytest.mark.parametrize("eps", (0.0, 1e-6))
 def test_delta_beta_of_zero_keys(gpu_lib, unit, eps):

@@ -27,12 +27,12 @@
 //
 // Times (us: keys, prepare, scan), heads of P x N:
 //   1 x 2048 positions, 64 heads of 64 x 128, bf16          6, 18, 91
-//   8 x 2048, 80 of 64 x 128, one group each, fp16          9, 115, 266 to 302
+//   8 x 2048, 80 of 64 x 128, one group each, fp16          9, 126, 310 to 341
 //   4 x 4096, 32 of 128 x 128, 16 groups each, bf16         70, 60, 235
 // The scan is bound by its chain: about 860 instructions a chunk and wave (490 of the
 // vector unit, 104 products, 115 LDS reads) that follow one another, in 2.8 us where a
 // wave has its SIMD to itself, of which half issue nothing; two waves a SIMD issue 57 % of
-// the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 18 to 24 KB a chunk and
+// the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 19 to 25 KB a chunk and
 // head at 3 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
 // a copy once groups are many (5.8 TB/s of read and written bytes in the last).
 // Preparing a chunk within the scan's launch was no faster in total.
@@ -49,7 +49,11 @@ constexpr int kC = kDeltaChunk;
 template <int DT>
 struct Parts {
   static constexpr int kKeys = DT == DT_F32 ? 2 : 1;     // fp16 numbers of a key's or query's element
-  static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U: 2^-12 of an fp16 or bf16 Y's term
+  static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U: one rounds to 2^-12 of a term
+  // As much as fp16 Y's own rounding, where terms cancel more than it: there what it leaves
+  // follows, rounded to 8 bits (2^-15 of a term; 8 x 2048 positions of 80 heads 389 us without and
+  // 434 with it, relative errors of Y up to 3.3e-4 and of 2.1e-4, its rounding's own).
+  static constexpr bool kLowWeights = DT == DT_F16;
   static constexpr int kStateY = DT == DT_BF16 ? 1 : 2;  // of S in Y: one rounds to 2^-12, a 16th of bf16's step
   static constexpr int kNewY = DT == DT_BF16 ? 1 : 2;    // of U in Y
 };
@@ -82,10 +86,12 @@ struct Factors {
   float decay, most, inv_t[4], inv_a[4];
 };
 // Of each (batch, head, chunk): fragments of T diag(b) (6
-// that are not zero, two parts), of Y's weights (6), and the factors.
+// that are not zero, two parts), of Y's weights (6), the factors, and what the weights'
+// rounding leaves, 8 bytes for each lane of a fragment.
 template <int DT>
 struct HeadPlan {
-  static constexpr int kT = 0, kA = 12, kFac = 12 + 6 * Parts<DT>::kWeights, kFrags = kFac + 1;
+  static constexpr int kT = 0, kA = 12, kFac = 12 + 6 * Parts<DT>::kWeights, kLow = kFac + 1;
+  static constexpr int kFrags = kLow + (Parts<DT>::kLowWeights ? 3 : 0);
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
 static_assert(sizeof(Factors) <= kFrag, "a fragment's room");
@@ -156,6 +162,16 @@ __device__ __forceinline__ void split8_unscaled(const float (&x)[8], float one, 
 __device__ __forceinline__ void split_tiles(v4f a, v4f b, float by_a, float by_b, v8h& hi, v8h& lo) {
   const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   split8(x, by_a, by_b, hi, lo);
+}
+// The upper bytes of eight fp16 numbers, rounded, and the numbers that they stand for.
+__device__ __forceinline__ uint2 upper_bytes(v8h v) {
+  const v4u w = __builtin_bit_cast(v4u, v) + 0x00800080u;
+  return make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x07050301), __builtin_amdgcn_perm(w[3], w[2], 0x07050301));
+}
+__device__ __forceinline__ v8h from_upper_bytes(uint2 b) {
+  const v4u w = {__builtin_amdgcn_perm(0, b.x, 0x010c000c), __builtin_amdgcn_perm(0, b.x, 0x030c020c),
+                 __builtin_amdgcn_perm(0, b.y, 0x010c000c), __builtin_amdgcn_perm(0, b.y, 0x030c020c)};
+  return __builtin_bit_cast(v8h, w);
 }
 // 2^x
 __device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -463,9 +479,10 @@ __device__ __forceinline__ void invert_diagonal(float* diag) {
 }
 
 // Tiles of a row of a lower triangle, transposed (rows are positions j, columns i), as
-// fragments for the products with R or U. Returns what undoes their scaling.
+// fragments for the products with R or U; low: where upper bytes of the lower parts go
+// (or null). Returns what undoes their scaling.
 template <int I, int PARTS>
-__device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out) {
+__device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out, char* low) {
   const Scale sc(wave_most(tiles_max(x)));
 #pragma unroll
   for (int s = 0; s <= I / 2; ++s) {
@@ -473,6 +490,7 @@ __device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out) {
     split_tiles(x[2 * s], 2 * s + 1 <= I ? x[2 * s + 1 <= I ? 2 * s + 1 : 0] : (v4f)(0.f), sc.by, sc.by, hi, lo);
     *(v8h*)(out + lower_frag(I, s) * kFrag + lane_id() * 16) = hi;
     if constexpr (PARTS == 2) *(v8h*)(out + (6 + lower_frag(I, s)) * kFrag + lane_id() * 16) = lo;
+    if (low) *(uint2*)(low + lower_frag(I, s) * (kFrag / 2) + lane_id() * 8) = upper_bytes(lo);
   }
   return sc.inv;
 }
@@ -513,13 +531,13 @@ __device__ __forceinline__ void form_t_row(const Gates& w, const float* diag, Lo
   }
 #pragma unroll
   for (int j = 0; j <= I; ++j) x[j] *= beta[j];
-  const float inv = write_row<I, 2>(x, out);
+  const float inv = write_row<I, 2>(x, out, nullptr);
   if (lane_id() < 16) f.fac_u[16 * I + lane_id()] *= inv;
   if (lane_id() == 0) f.inv_t[I] = inv;
 }
 // Tile row I of Y's weights of U.
 template <int PARTS, int I>
-__device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1], char* out, Factors& f) {
+__device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1], char* out, char* low, Factors& f) {
   const int sub = lane_id() >> 4, col = lane_id() & 15;
   const float fq = w.fq[16 * I + col];
   v4f x[I + 1];
@@ -538,7 +556,7 @@ __device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1
       }
     }
   }
-  const float inv = write_row<I, PARTS>(x, out);
+  const float inv = write_row<I, PARTS>(x, out, low);
   if (lane_id() == 0) f.inv_a[I] = inv;
 }
 
@@ -573,10 +591,13 @@ struct Prepare {
     for (int n = 0; n < kBelow; ++n)
       lower[kI[n] * (kI[n] - 1) / 2 + kJ[n]][lane_id()] = lower_tile(w, kk[1 + n], kI[n], kJ[n]);
   }
-  __device__ __forceinline__ void part_b(Gates& w, float* diag, char* a_frags) {
+  __device__ __forceinline__ void part_b(Gates& w, float* diag, char* head) {
+    typedef HeadPlan<DT> HP_;
+    char* const a_frags = head + HP_::kA * kFrag;
+    char* const low = Parts<DT>::kLowWeights ? head + HP_::kLow * kFrag : nullptr;
     if constexpr (ROLE == 0) invert_diagonal(diag);
-    else form_y_row<AP, kRow>(w, kq, a_frags, w.f);
-    if constexpr (ROLE == 1) form_y_row<AP, 0>(w, kq0, a_frags, w.f);
+    else form_y_row<AP, kRow>(w, kq, a_frags, low, w.f);
+    if constexpr (ROLE == 1) form_y_row<AP, 0>(w, kq0, a_frags, low, w.f);
   }
   __device__ __forceinline__ void part_c(Gates& w, const v4f (*lower)[kWave], const float* diag, char* t_frags) {
     form_t_row<ROLE>(w, diag, [&](int k, int j) { return lower[k * (k - 1) / 2 + j][lane_id()]; }, t_frags, w.f);
@@ -613,6 +634,7 @@ struct Chain {
   static constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
   v4f s[NT], ks[4], qs[4], u[4];
   v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
+  uint2 low[Parts<DT>::kLowWeights ? 6 : 1];  // of those, what their rounding leaves
   float inv_s, inv_r, max_s, max_u, one;
   int place;  // of the lane's column in a row of the workgroup's
 
@@ -636,6 +658,13 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       *(v4f*)(a.final_state + (unit * P + p) * (int64_t)N + 16 * n + 4 * (lane_id() >> 4)) = s[n] * inv_s;
+  }
+  // The weights' lower parts, straight from memory; head: of the chunk, at this lane.
+  __device__ __forceinline__ void load_low(const char* head) {
+    if constexpr (Parts<DT>::kLowWeights) {
+#pragma unroll
+      for (int n = 0; n < 6; ++n) low[n] = *(const uint2*)(head + HeadPlan<DT>::kLow * kFrag + n * (kFrag / 2));
+    }
   }
   // K S^T and Q S^T. What comes out of LDS is read a step ahead of its use, here and
   // below: a wave has its SIMD to itself, or nearly.
@@ -762,6 +791,12 @@ struct Chain {
 #pragma unroll
         for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], lo[1], y[i]);
       }
+      if constexpr (Parts<DT>::kLowWeights) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mma16(from_upper_bytes(low[lower_frag(i, 0)]), hi[0], y[i]);
+#pragma unroll
+        for (int i = 2; i < 4; ++i) y[i] = mma16(from_upper_bytes(low[lower_frag(i, 1)]), hi[1], y[i]);
+      }
       if constexpr (AP == 2) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = mma16(wa[6 + lower_frag(i, 0)], hi[0], y[i]);
@@ -847,7 +882,7 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, const char* 
     __syncthreads();
     p.part_a(w, lower, diag);
     __syncthreads();
-    p.part_b(w, diag, out + HP_::kA * kFrag);
+    p.part_b(w, diag, out);
     __syncthreads();
     p.part_c(w, lower, diag, out + HP_::kT * kFrag);
     __syncthreads();
@@ -926,6 +961,7 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
                    char* turned, char* head, char* factors, char* vals) __attribute__((always_inline)) {
     const bool more = i + 1 < chunks;
     const Factors& f = *(const Factors*)fac;
+    c.load_low(heads + i * (int64_t)HP_::kBytes + lane_id() * 8);  // here by the barrier after the products
     if (DEEP && more) {
       copy_first(i + 1, first);
       copy_turned(i + 1, turned);

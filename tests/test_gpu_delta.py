@@ -118,6 +118,29 @@ def test_delta_forward(gpu_lib, case):
     check(_np(Y), y, ymag, dtype, Y_TAU[dtype], Y_NORM[dtype], "y")
 
 
+@pytest.mark.parametrize("case", [(2, 40, 8, 32, 64, 1), (1, 64, 6, 64, 128, 2), (1, 130, 4, 128, 32, 1)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_delta_fp16_outputs_are_rounded_once(gpu_lib, case):
+    """Y's terms are kept to 2^-15 (the weights' second part), so that what is lost is the
+    rounding to fp16: a value that is d off before it goes to the other neighbour, a step s
+    <= 2^-10 |y| away, with probability |d| / s, and the differences from the rounded exact
+    values have a mean square of |d| s <= 2^-25 y^2. (One part alone, 2^-12 of a term, would
+    give 2^-22.)"""
+    import torch
+    L = gpu_lib
+    B, Ln, H_, P, N, G = case
+    print("delta", case, flush=True)
+    c = make(torch, 51, B, Ln, H_, P, N, G, "fp16")
+    sh = L.make_shape(B, Ln, H_, P, N, G, 64, "fp16")
+    Y = torch.empty(B, Ln, H_, P, dtype=torch.float16, device="cuda")
+    L.ssd_delta_forward(sh, c["X"], c["dt"], c["A"], c["K"], c["Q"], c["beta"], Y, initial_state=c["init"], scale=0.3,
+                        logit=True)
+    torch.cuda.synchronize()
+    y = reference(c, 0.3, True, True, True)[0]
+    off = np.linalg.norm(_np(Y) - y.astype(np.float16).astype(np.float64)) / np.linalg.norm(y)
+    assert off <= 2.0 ** -12.5, off
+
+
 @pytest.mark.parametrize("case", [(1, 64, 64, 128, 1, "bf16"), (3, 5, 16, 16, 5, "fp16"), (2, 6, 128, 128, 2, "fp32"),
                                   (70, 80, 64, 128, 1, "fp16"), (600, 7, 32, 64, 1, "bf16"), (257, 33, 16, 32, 3, "fp32"),
                                   (40, 64, 128, 16, 1, "fp32")], ids=lambda c: "-".join(map(str, c)))

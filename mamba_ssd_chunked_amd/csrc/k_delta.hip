@@ -39,6 +39,7 @@
 #include <type_traits>
 
 #include "ssd_delta.hpp"
+#include "ssd_delta_scale.hpp"
 
 namespace ssd {
 namespace {
@@ -115,17 +116,6 @@ constexpr int kDiagRow = 20, kDiag = 16 * kDiagRow + 4;
 // ---------------------------------------------------------------------------
 // scaling and parts
 // ---------------------------------------------------------------------------
-// The power of two that brings m to [2^8, 2^9), and its inverse; from 2^-82 on down it
-// is 2^90, so that products of two of them stay in fp32's range.
-struct Scale {
-  float by, inv;
-  __device__ __forceinline__ explicit Scale(float m) {
-    const int e = min(262 - (int)((__float_as_uint(m) >> 23) & 255), 217);
-    by = __uint_as_float((uint32_t)e << 23);
-    inv = __uint_as_float((uint32_t)(254 - e) << 23);
-  }
-};
-
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 // Eight values, four times a factor each, as fp16 numbers, and what that leaves of them as eight
@@ -760,9 +750,8 @@ struct Chain {
   }
   // Y of the chunk's `left` positions, through `stage` (32 rows of the wave's 16 columns), and
   //   S' = e^{g_63} S + (e^{g_63 - g} U)^T K,
-  // the products added to the scaled state: its largest value is brought to 2^8 and U's
-  // part to 2 at most, so that the sums (64 terms, keys up to 2^8) stay below 2^16 as
-  // fp16's range asks.
+  // the products added to the scaled state: its largest value is brought below 2^9 and U's
+  // part to 1 at most, so that the sums (64 terms, keys below 2^9) stay in fp16's range.
   __device__ __forceinline__ void outputs_and_state(const char* turned, const Factors& f, T* stage, char* out,
                                                     uint32_t step, int left) {
     const int sub = lane_id() >> 4;
@@ -805,7 +794,7 @@ struct Chain {
       }
     }
     const float was = inv_s;
-    const Scale sc(fmaxf(max_s * inv_s * decay, max_u * inv_r * most * 256.f));
+    const Scale sc(fmaxf(max_s * inv_s * decay, max_u * inv_r * most * kChangeScale));
     const float keep = decay * (inv_s * sc.by), by = inv_r * sc.by;
     inv_s = sc.inv;
 #pragma unroll

@@ -1,0 +1,37 @@
+// The powers of two that bring the gated delta rule's operands into fp16's range (without
+// HIP as well: a test asks them for their bounds).
+#pragma once
+
+#include <cstdint>
+
+#ifdef __HIPCC__
+#define SSD_HOST_DEVICE __host__ __device__ __forceinline__
+#else
+#define SSD_HOST_DEVICE inline
+#endif
+
+namespace ssd {
+
+// The power of two that brings m to [2^8, 2^9), and its inverse; from 2^-82 on down it
+// is 2^90, so that products of two of them stay in fp32's range.
+struct Scale {
+  float by, inv;
+  SSD_HOST_DEVICE explicit Scale(float m) {
+    const int up = 262 - (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255), e = up < 217 ? up : 217;
+    by = __builtin_bit_cast(float, (uint32_t)e << 23);
+    inv = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+  }
+};
+// What a scaled value is below, and at most once it is rounded to fp16.
+constexpr float kScaledMost = 512.f;
+
+// The scaled state is an operand of the next chunk as it is, so that a chunk's sums have to
+// stay below fp16's 65504. The state before them is at most kScaledMost, each of 64 terms
+// is a key (at most kScaledMost) times U's part. That is taken kChangeScale times larger than it
+// is into the choice of the scale, which holds it to 1: 512 + 64 * 512 = 33280.
+constexpr float kChangeScale = 512.f;
+constexpr float kChangeMost = kScaledMost / kChangeScale;
+constexpr float kStateMost = kScaledMost + 64 * kScaledMost * kChangeMost;
+static_assert(kStateMost < 65504.f, "the state leaves fp16's range");
+
+}  // namespace ssd

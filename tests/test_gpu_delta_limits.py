@@ -1,0 +1,61 @@
+"""The gated delta rule where its numbers reach the ends of what its products hold: states
+that grow evenly, values and decays of very different sizes in one chunk, terms that cancel,
+values that are not finite.
+
+Bounds as in test_gpu_delta.py, but where a test says otherwise.
+"""
+import numpy as np
+import pytest
+
+from tests import test_gpu_delta as D
+from tests.test_gpu_operators import _np, forward
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+
+
+def inputs(torch, dtype, X, K, Q, dt, A, beta, init=None):
+    """Inputs of one sequence from float64 arrays: X [L, H, P], K, Q [L, G, N], dt, beta [L, H], A [H]."""
+    td = getattr(torch, D.DT[dtype])
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(device="cuda", dtype=td)  # noqa: E731
+    c = {"X": t(X)[None], "K": t(K)[None], "Q": t(Q)[None], "dt": t(dt)[None], "beta": t(beta)[None]}
+    c["A"] = torch.from_numpy(np.asarray(A)).float().cuda()
+    H_, P, N = X.shape[1], X.shape[2], K.shape[2]
+    s0 = np.zeros((1, H_, P, N)) if init is None else init[None]
+    c["init"] = torch.from_numpy(s0).float().cuda()
+    return c
+
+
+def compare(c, dtype, Y, fin, unit, logit, scale=0.3, eps=1e-6):
+    y, s, ymag, smag = D.reference(c, scale, unit, logit, True, eps=eps)
+    D.check(_np(fin), s, smag, "fp32", 2.0 ** -13, 2.0 ** -18, "state")
+    D.check(_np(Y), y, ymag, dtype, D.Y_TAU[dtype], D.Y_NORM[dtype], "y")
+
+
+@pytest.mark.parametrize("dtype,unit,k,step,beta,init", [
+    # one key, just below a power of two, and values that grow by the same amount
+    ("fp32", True, 1.9999, 1.99965, 1.0, 0.0),
+    ("fp32", True, 1.9999, 1.99965, 1.0, 0.99),
+    ("fp32", False, 1.0 - 2.0 ** -15, 1.99965, 1.0, 0.0),
+    ("fp32", False, 1.0 - 2.0 ** -15, 1.99965, 1.0, 0.99),
+    # the same value at every position, weakly written
+    ("fp32", False, 1.9999, 0.0, 2.0 ** -20, 0.0),
+    ("fp16", False, 2047 / 1024, 0.0, 2.0 ** -20, 1.99 * 2.0 ** -20),
+    ("bf16", False, 1.9921875, 0.0, 2.0 ** -20, 1.98 * 2.0 ** -20),
+], ids=str)
+def test_delta_states_that_grow_evenly(gpu_lib, dtype, unit, k, step, beta, init):
+    """Changes of one sign and the largest mantissas, whose sum over a chunk is the largest that
+    a chunk can add to the state."""
+    import torch
+    n, H_, P, N = 192, 2, 16, 32
+    K = np.zeros((n, 1, N))
+    K[..., 0] = k
+    Q = np.ones((n, 1, N))
+    x = step * (np.arange(n) + 1.0) if step else np.full(n, k)
+    X = np.broadcast_to(x[:, None, None], (n, H_, P))
+    s0 = np.zeros((H_, P, N))
+    s0[..., 0] = init
+    c = inputs(torch, dtype, X, K, Q, np.zeros((n, H_)), -np.ones(H_), np.full((n, H_), beta), s0)
+    Y, fin = forward(gpu_lib, torch, c, unit=unit, logit=False)
+    compare(c, dtype, Y, fin, unit, False)

@@ -80,11 +80,11 @@ struct KeyPlan {
 __device__ __forceinline__ constexpr int lower_tile_at(int i, int j) { return i * (i + 1) / 2 + j; }
 // Factors of a chunk of a head: for each position of K S^T in R (fac_k), of Q S^T in Y
 // (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling); the state's
-// decay over the chunk, the largest of fac_u without that, and what undoes the scaling
-// of each tile row of T and of Y's weights.
+// decay over the chunk, and what undoes the scaling of each tile row of T and of Y's
+// weights.
 struct Factors {
   float fac_k[kC], fac_q[kC], fac_u[kC];
-  float decay, most, inv_t[4], inv_a[4];
+  float decay, inv_t[4], inv_a[4];
 };
 // Of each (batch, head, chunk): fragments of T diag(b) (6
 // that are not zero, two parts), of Y's weights (6), the factors, and what the weights'
@@ -134,18 +134,13 @@ __device__ __forceinline__ void split8(const float (&x)[8], float by0, float by4
     lo[e + 1] = (_Float16)fmaf(x[e + 1], by, -(float)h[1]);
   }
 }
-// The same of values as they are; `one` is a 1 that the compiler does not know (x 1 - hi,
-// rounded to fp16, is one operation).
-__device__ __forceinline__ void split8_unscaled(const float (&x)[8], float one, v8h& hi, v8h& lo) {
+// The same of the scaled state's values, brought down to fp16's range: one operation for
+// each number, which takes the factor along.
+__device__ __forceinline__ void split8_state(const float (&x)[8], v8h& hi, v8h& lo) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    uint32_t w = pack2<DT_F16>(x[e], x[e + 1]);
-    asm("" : "+v"(w));
-    const v2h h = __builtin_bit_cast(v2h, w);
-    hi[e] = h[0];
-    hi[e + 1] = h[1];
-    lo[e] = (_Float16)fmaf(x[e], one, -(float)h[0]);
-    lo[e + 1] = (_Float16)fmaf(x[e + 1], one, -(float)h[1]);
+  for (int e = 0; e < 8; ++e) {
+    hi[e] = (_Float16)(x[e] * kStateDown);
+    lo[e] = (_Float16)fmaf(x[e], kStateDown, -(float)hi[e]);
   }
 }
 // Rows 4 (lane / 16) .. of two result tiles, as an operand.
@@ -421,11 +416,7 @@ __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float
   w.f.fac_k[lane] = eg * in.fk;
   w.f.fac_q[lane] = eg * in.fq;
   w.f.fac_u[lane] = fu;
-  const float most = wave_most(fu);
-  if (lane == 0) {
-    w.f.decay = exp2((float)end[3]);
-    w.f.most = most;
-  }
+  if (lane == 0) w.f.decay = exp2((float)end[3]);
 }
 
 // L's tile (i, j) below the diagonal, from K K^T's.
@@ -625,7 +616,7 @@ struct Chain {
   v4f s[NT], ks[4], qs[4], u[4];
   v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
   uint2 low[Parts<DT>::kLowWeights ? 6 : 1];  // of those, what their rounding leaves
-  float inv_s, inv_r, max_s, max_u, one;
+  float inv_s, inv_r, max_s, max_u;
   int place;  // of the lane's column in a row of the workgroup's
 
   __device__ __forceinline__ static v8h frag(const char* p, int f) { return *(const v8h*)(p + f * kFrag + lane_id() * 16); }
@@ -636,12 +627,10 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       s[n] = a.init ? *(const v4f*)(a.init + (unit * P + p) * (int64_t)N + 16 * n + 4 * sub) : (v4f)(0.f);
-    const Scale sc(column_max(tiles_max(s)));
+    const Scale sc(column_max(tiles_max(s)) * kStateDown);
     inv_s = sc.inv;
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] *= sc.by;
-    one = 1.f;
-    asm volatile("" : "+v"(one));
   }
   __device__ __forceinline__ void finish(const DeltaArgs& a, int64_t unit, int P, int p) {
     if (!a.final_state) return;
@@ -676,7 +665,7 @@ struct Chain {
       v8h hi, lo;
       const v4f a = s[2 * t], b = 2 * t + 1 < NT ? s[2 * t + 1 < NT ? 2 * t + 1 : 0] : (v4f)(0.f);
       const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      split8_unscaled(x, one, hi, lo);
+      split8_state(x, hi, lo);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][i], hi, ks[i]);
 #pragma unroll
@@ -712,6 +701,7 @@ struct Chain {
     const char* const at = values + 4 * (lane_id() >> 4) * kRowBytes<DT, W> + place;
     float v[4][4];
     v4f fk[4];
+    const float inv_k = inv_s / kStateDown;
 #pragma unroll
     for (int i = 0; i < 4; ++i) fk[i] = *(const v4f*)(f.fac_k + 16 * i + 4 * (lane_id() >> 4));
 #pragma unroll
@@ -721,7 +711,7 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ks[i][e] = fmaf(-fk[i][e] * inv_s, ks[i][e], v[i][e]);
+      for (int e = 0; e < 4; ++e) ks[i][e] = fmaf(-fk[i][e] * inv_k, ks[i][e], v[i][e]);
   }
   // U = T diag(b) R, as u times inv_r and, of tile row i, inv_t[i].
   __device__ __forceinline__ void changes(const Factors& f) {
@@ -750,8 +740,10 @@ struct Chain {
   }
   // Y of the chunk's `left` positions, through `stage` (32 rows of the wave's 16 columns), and
   //   S' = e^{g_63} S + (e^{g_63 - g} U)^T K,
-  // the products added to the scaled state: its largest value is brought below 2^9 and U's
-  // part to 1 at most, so that the sums (64 terms, keys below 2^9) stay in fp16's range.
+  // the products added to the scaled state, whose scale lets both keep their bits: the largest
+  // of the old state in a column is below 2^18, that of the new terms below 2^9, and one of
+  // them is at least half as large. (As they are: factors' and changes' own largest values
+  // may lie at different positions.)
   __device__ __forceinline__ void outputs_and_state(const char* turned, const Factors& f, T* stage, char* out,
                                                     uint32_t step, int left) {
     const int sub = lane_id() >> 4;
@@ -760,7 +752,7 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 4; ++i) fu[i] = *(const v4f*)(f.fac_u + 16 * i + 4 * sub);
     const v4f inv_t = *(const v4f*)f.inv_t, inv_a = *(const v4f*)f.inv_a;
-    const float decay = f.decay, most = f.most;
+    const float decay = f.decay;
 #pragma unroll
     for (int n = 0; n < NT; ++n) k[0][n] = frag(turned, 2 * n);
     v4f y[4];
@@ -793,15 +785,18 @@ struct Chain {
         for (int i = 2; i < 4; ++i) y[i] = mma16(wa[6 + lower_frag(i, 1)], hi[1], y[i]);
       }
     }
-    const float was = inv_s;
-    const Scale sc(fmaxf(max_s * inv_s * decay, max_u * inv_r * most * kChangeScale));
+    v4f w[4];  // diag(e^{g_63 - g}) U
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = u[i] * fu[i];
+    const float was = inv_s / kStateDown, max_w = column_max(tiles_max(w));
+    const Scale sc(fmaxf(max_s * inv_s * decay * kStateDown, max_w * inv_r));
     const float keep = decay * (inv_s * sc.by), by = inv_r * sc.by;
     inv_s = sc.inv;
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] *= keep;
     v8h hi[2], lo[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) split_tiles(u[2 * t] * fu[2 * t], u[2 * t + 1] * fu[2 * t + 1], by, by, hi[t], lo[t]);
+    for (int t = 0; t < 2; ++t) split_tiles(w[2 * t], w[2 * t + 1], by, by, hi[t], lo[t]);
 #pragma unroll
     for (int n = 0; n < NT; ++n) k[1][n] = frag(turned, 2 * n + 1);
 #pragma unroll

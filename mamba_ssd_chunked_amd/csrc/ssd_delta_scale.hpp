@@ -25,13 +25,14 @@ struct Scale {
 // What a scaled value is below, and at most once it is rounded to fp16.
 constexpr float kScaledMost = 512.f;
 
-// The scaled state is an operand of the next chunk as it is, so that a chunk's sums have to
-// stay below fp16's 65504. The state before them is at most kScaledMost, each of 64 terms
-// is a key (at most kScaledMost) times U's part. That is taken kChangeScale times larger than it
-// is into the choice of the scale, which holds it to 1: 512 + 64 * 512 = 33280.
-constexpr float kChangeScale = 512.f;
-constexpr float kChangeMost = kScaledMost / kChangeScale;
-constexpr float kStateMost = kScaledMost + 64 * kScaledMost * kChangeMost;
+// The scaled state takes the products of a chunk as they come: 64 terms, each a key times a
+// change, both at most kScaledMost. Before them it is at most kScaledMost / kStateDown, and
+// times kStateDown it is an operand of the next chunk, which has to stay below fp16's 65504:
+// 2^9 + 64 * 2^18 * 2^-9 = 33280. (Changes scaled to 1 instead, so that the state needs no
+// factor, would lose what is below 2^-25 of a column's largest, not 2^-33; the factor costs 2 %
+// of the scan.)
+constexpr float kStateDown = 1.f / 512.f;
+constexpr float kStateMost = kScaledMost + 64 * kScaledMost * kScaledMost * kStateDown;
 static_assert(kStateMost < 65504.f, "the state leaves fp16's range");
 
 }  // namespace ssd

@@ -21,10 +21,10 @@ int main() {
       // a chunk whose changes and keys are the largest, on a state that is as large as they allow
       for (const float keeps : {0.f, 0.25f, 0.5f, 1.f}) {
         if (m > 0x1p100f) continue;
-        const float before = keeps * ssd::kChangeScale * m;
-        const ssd::Scale sc(std::fmax(before, m * ssd::kChangeScale));
+        const float before = keeps / ssd::kStateDown * m;
+        const ssd::Scale sc(std::fmax(before * ssd::kStateDown, m));
         const float key = (2.f - 0x1p-23f) * ssd::Scale(2.f - 0x1p-23f).by;
-        state = std::fmax(state, before * sc.by + 64.f * (m * sc.by) * key);
+        state = std::fmax(state, (before * sc.by + 64.f * (m * sc.by) * key) * ssd::kStateDown);
       }
     }
   std::printf("%d %.9g %.9g %.9g %.9g %.9g\n", inverse, least, most, ssd::kScaledMost, state, ssd::kStateMost);

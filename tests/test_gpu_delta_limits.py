@@ -59,3 +59,48 @@ def test_delta_states_that_grow_evenly(gpu_lib, dtype, unit, k, step, beta, init
     c = inputs(torch, dtype, X, K, Q, np.zeros((n, H_)), -np.ones(H_), np.full((n, H_), beta), s0)
     Y, fin = forward(gpu_lib, torch, c, unit=unit, logit=False)
     compare(c, dtype, Y, fin, unit, False)
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("size", (100.0, 1e4))
+def test_delta_large_values_that_are_forgotten(gpu_lib, dtype, size):
+    """A large value at a chunk's first position, which its decays forget before its end."""
+    import torch
+    c = D.make(torch, 61, 2, 200, 3, 32, 64, 1, dtype)
+    c["dt"][:] = 0.7
+    c["A"][:] = -1.0
+    c["X"][:, ::64] *= size
+    c["init"].zero_()
+    Y, fin = forward(gpu_lib, torch, c)
+    compare(c, dtype, Y, fin, True, True)
+
+
+def test_delta_values_of_different_sizes(gpu_lib):
+    """Each position writes a place of its own, one of them a value 4096 times the others. The
+    changes and the remainders keep 2^-22 of themselves and 2^-33 of the largest of their
+    column, T 2^-22: with the sums, 2^-19 of a value and 2^-30 of the largest."""
+    import torch
+    rng = np.random.default_rng(5)
+    n, H_, P, N = 128, 2, 32, 128
+    for big in (0, 40, 63, 100, 127):
+        X = rng.standard_normal((n, H_, P))
+        X[big] = 4096.0
+        K = np.eye(N)[:, None, :]
+        Q = rng.standard_normal((n, 1, N))
+        c = inputs(torch, "fp32", X, K, Q, np.full((n, H_), 1e-3), -np.ones(H_), np.ones((n, H_)))
+        Y, fin = forward(gpu_lib, torch, c, unit=False, logit=False, scale=1.0)
+        s = D.reference(c, 1.0, False, False, True)[1]
+        err = np.abs(_np(fin) - s)
+        assert (err <= 2.0 ** -19 * np.abs(s) + 2.0 ** -30 * 4096).all(), (big, err.max())
+
+
+@pytest.mark.parametrize("size", (2.0 ** -60, 2.0 ** 60, 2.0 ** 118))
+def test_delta_values_of_any_size(gpu_lib, size):
+    """Values far from 1, up to a few steps below fp32's largest, from zeros."""
+    import torch
+    c = D.make(torch, 63, 1, 150, 2, 32, 64, 1, "fp32")
+    d = dict(c, X=c["X"] * size, init=c["init"] * 0)
+    y, s, ymag, smag = D.reference(c | {"init": c["init"] * 0}, 0.3, True, True, True)
+    Y, fin = forward(gpu_lib, torch, d)
+    D.check(_np(fin) / size, s, smag, "fp32", 2.0 ** -13, 2.0 ** -18, "state")
+    D.check(_np(Y) / size, y, ymag, "fp32", D.Y_TAU["fp32"], D.Y_NORM["fp32"], "y")

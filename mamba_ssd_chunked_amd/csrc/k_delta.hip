@@ -388,7 +388,9 @@ __device__ __forceinline__ double row_add(double v) {
 __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float A) {
   const int lane = lane_id(), sub = lane >> 4;
   double log_a = (double)in.dt * ((double)A * 1.4426950408889634);
-  log_a = log_a < -0x1p100 ? -0x1p100 : log_a;  // 2^log_a is 0 either way, and sums stay in fp32's range
+  // 2^log_a is 0 either way, and 64 of them leave the sums 37 bits behind the point: what
+  // decays after such a position keeps its effect
+  log_a = log_a < -1024.0 ? -1024.0 : log_a;
   double gs = row_add<8>(row_add<4>(row_add<2>(row_add<1>(log_a))));
   double end[4];  // of each 16 positions
   end[0] = lane_value(gs, 15);

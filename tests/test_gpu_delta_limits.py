@@ -104,3 +104,19 @@ def test_delta_values_of_any_size(gpu_lib, size):
     Y, fin = forward(gpu_lib, torch, d)
     D.check(_np(fin) / size, s, smag, "fp32", 2.0 ** -13, 2.0 ** -18, "state")
     D.check(_np(Y) / size, y, ymag, "fp32", D.Y_TAU["fp32"], D.Y_NORM["fp32"], "y")
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "bf16"))
+@pytest.mark.parametrize("n", (7, 150))
+def test_delta_decays_after_one_out_of_range(gpu_lib, dtype, n):
+    """Ordinary decays keep their effect behind positions that forget everything."""
+    import torch
+    c = D.make(torch, 65, 1, n, 2, 32, 64, 1, dtype)
+    c["A"][:] = -1.0
+    c["dt"][:] = 0.125
+    for size in (2.0 ** 11, 2.0 ** 45, 3e38):
+        at = [p for p in (2, 10, 64, 100, 101) if p < n]
+        d = dict(c, dt=c["dt"].clone())
+        d["dt"][:, at] = size
+        Y, fin = forward(gpu_lib, torch, d)
+        compare(d, dtype, Y, fin, True, True)

@@ -50,11 +50,10 @@ constexpr int kC = kDeltaChunk;
 template <int DT>
 struct Parts {
   static constexpr int kKeys = DT == DT_F32 ? 2 : 1;     // fp16 numbers of a key's or query's element
-  static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U: one rounds to 2^-12 of a term
-  // As much as fp16 Y's own rounding, where terms cancel more than it: there what it leaves
-  // follows, rounded to 8 bits (2^-15 of a term; 8 x 2048 positions of 80 heads 389 us without and
-  // 434 with it, relative errors of Y up to 3.3e-4 and of 2.1e-4, its rounding's own).
-  static constexpr bool kLowWeights = DT == DT_F16;
+  static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U in LDS: one rounds to 2^-12 of a term
+  // Bytes of each weight's lower part that follow in memory: one fp16 number as it is, whose
+  // term is then off by less than fp16 Y's rounding where terms cancel a thousand times over.
+  static constexpr int kLowBytes = DT == DT_F16 ? 2 : 0;
   static constexpr int kStateY = DT == DT_BF16 ? 1 : 2;  // of S in Y: one rounds to 2^-12, a 16th of bf16's step
   static constexpr int kNewY = DT == DT_BF16 ? 1 : 2;    // of U in Y
 };
@@ -87,12 +86,13 @@ struct Factors {
   float decay, inv_t[4], inv_a[4];
 };
 // Of each (batch, head, chunk): fragments of T diag(b) (6
-// that are not zero, two parts), of Y's weights (6), the factors, and what the weights'
-// rounding leaves, 8 bytes for each lane of a fragment.
+// that are not zero, two parts), of Y's weights (6), the factors, and the weights' lower
+// parts, 8 kLowBytes bytes for each lane of a fragment.
 template <int DT>
 struct HeadPlan {
   static constexpr int kT = 0, kA = 12, kFac = 12 + 6 * Parts<DT>::kWeights, kLow = kFac + 1;
-  static constexpr int kFrags = kLow + (Parts<DT>::kLowWeights ? 3 : 0);
+  static constexpr int kLowFrag = kFrag / 2 * Parts<DT>::kLowBytes;
+  static constexpr int kFrags = kLow + 6 * kLowFrag / kFrag;
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
 static_assert(sizeof(Factors) <= kFrag, "a fragment's room");
@@ -158,6 +158,15 @@ __device__ __forceinline__ v8h from_upper_bytes(uint2 b) {
                  __builtin_amdgcn_perm(0, b.y, 0x010c000c), __builtin_amdgcn_perm(0, b.y, 0x030c020c)};
   return __builtin_bit_cast(v8h, w);
 }
+// What a lane holds of a fragment of lower parts: eight of so many bytes.
+template <int BYTES>
+struct LowPart {
+  typedef v8h T;
+};
+template <>
+struct LowPart<1> {
+  typedef uint2 T;
+};
 // 2^x
 __device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -462,9 +471,9 @@ __device__ __forceinline__ void invert_diagonal(float* diag) {
 }
 
 // Tiles of a row of a lower triangle, transposed (rows are positions j, columns i), as
-// fragments for the products with R or U; low: where upper bytes of the lower parts go
-// (or null). Returns what undoes their scaling.
-template <int I, int PARTS>
+// fragments for the products with R or U; LOW: lower parts' bytes that go to low. Returns
+// what undoes their scaling.
+template <int I, int PARTS, int LOW = 0>
 __device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out, char* low) {
   const Scale sc(wave_most(tiles_max(x)));
 #pragma unroll
@@ -473,7 +482,8 @@ __device__ __forceinline__ float write_row(const v4f (&x)[I + 1], char* out, cha
     split_tiles(x[2 * s], 2 * s + 1 <= I ? x[2 * s + 1 <= I ? 2 * s + 1 : 0] : (v4f)(0.f), sc.by, sc.by, hi, lo);
     *(v8h*)(out + lower_frag(I, s) * kFrag + lane_id() * 16) = hi;
     if constexpr (PARTS == 2) *(v8h*)(out + (6 + lower_frag(I, s)) * kFrag + lane_id() * 16) = lo;
-    if (low) *(uint2*)(low + lower_frag(I, s) * (kFrag / 2) + lane_id() * 8) = upper_bytes(lo);
+    if constexpr (LOW == 2) *(v8h*)(low + lower_frag(I, s) * kFrag + lane_id() * 16) = lo;
+    if constexpr (LOW == 1) *(uint2*)(low + lower_frag(I, s) * (kFrag / 2) + lane_id() * 8) = upper_bytes(lo);
   }
   return sc.inv;
 }
@@ -519,7 +529,7 @@ __device__ __forceinline__ void form_t_row(const Gates& w, const float* diag, Lo
   if (lane_id() == 0) f.inv_t[I] = inv;
 }
 // Tile row I of Y's weights of U.
-template <int PARTS, int I>
+template <int PARTS, int LOW, int I>
 __device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1], char* out, char* low, Factors& f) {
   const int sub = lane_id() >> 4, col = lane_id() & 15;
   const float fq = w.fq[16 * I + col];
@@ -539,7 +549,7 @@ __device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1
       }
     }
   }
-  const float inv = write_row<I, PARTS>(x, out, low);
+  const float inv = write_row<I, PARTS, LOW>(x, out, low);
   if (lane_id() == 0) f.inv_a[I] = inv;
 }
 
@@ -548,7 +558,7 @@ __device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1
 template <int DT, int N, int ROLE>
 struct Prepare {
   typedef KeyPlan<DT, N> KP_;
-  static constexpr int AP = Parts<DT>::kWeights;
+  static constexpr int AP = Parts<DT>::kWeights, LOW = Parts<DT>::kLowBytes;
   // tiles of K K^T: the diagonal one (ROLE, ROLE) and up to two below it
   static constexpr int kBelow = ROLE == 0 || ROLE == 2 ? 2 : 1;
   static constexpr int kI[2] = {ROLE == 0 ? 1 : ROLE == 1 ? 2 : 3, ROLE == 0 ? 2 : 3};
@@ -577,10 +587,10 @@ struct Prepare {
   __device__ __forceinline__ void part_b(Gates& w, float* diag, char* head) {
     typedef HeadPlan<DT> HP_;
     char* const a_frags = head + HP_::kA * kFrag;
-    char* const low = Parts<DT>::kLowWeights ? head + HP_::kLow * kFrag : nullptr;
+    char* const low = head + HP_::kLow * kFrag;
     if constexpr (ROLE == 0) invert_diagonal(diag);
-    else form_y_row<AP, kRow>(w, kq, a_frags, low, w.f);
-    if constexpr (ROLE == 1) form_y_row<AP, 0>(w, kq0, a_frags, low, w.f);
+    else form_y_row<AP, LOW, kRow>(w, kq, a_frags, low, w.f);
+    if constexpr (ROLE == 1) form_y_row<AP, LOW, 0>(w, kq0, a_frags, low, w.f);
   }
   __device__ __forceinline__ void part_c(Gates& w, const v4f (*lower)[kWave], const float* diag, char* t_frags) {
     form_t_row<ROLE>(w, diag, [&](int k, int j) { return lower[k * (k - 1) / 2 + j][lane_id()]; }, t_frags, w.f);
@@ -613,11 +623,11 @@ template <int DT, int N>
 struct Chain {
   typedef KeyPlan<DT, N> KP_;
   typedef typename Store<DT>::T T;
-  static constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights;
+  static constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights, LOW = Parts<DT>::kLowBytes;
   static constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
   v4f s[NT], ks[4], qs[4], u[4];
   v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
-  uint2 low[Parts<DT>::kLowWeights ? 6 : 1];  // of those, what their rounding leaves
+  typename LowPart<LOW>::T low[6];  // of those, the lower parts
   float inv_s, inv_r, max_s, max_u;
   int place;  // of the lane's column in a row of the workgroup's
 
@@ -640,12 +650,18 @@ struct Chain {
     for (int n = 0; n < NT; ++n)
       *(v4f*)(a.final_state + (unit * P + p) * (int64_t)N + 16 * n + 4 * (lane_id() >> 4)) = s[n] * inv_s;
   }
-  // The weights' lower parts, straight from memory; head: of the chunk, at this lane.
+  // The weights' lower parts, straight from memory; head: of the chunk.
   __device__ __forceinline__ void load_low(const char* head) {
-    if constexpr (Parts<DT>::kLowWeights) {
+    if constexpr (LOW > 0) {
+      typedef typename LowPart<LOW>::T V;
+      const V* const from = (const V*)(head + HeadPlan<DT>::kLow * kFrag) + lane_id();
 #pragma unroll
-      for (int n = 0; n < 6; ++n) low[n] = *(const uint2*)(head + HeadPlan<DT>::kLow * kFrag + n * (kFrag / 2));
+      for (int n = 0; n < 6; ++n) low[n] = from[n * kWave];
     }
+  }
+  __device__ __forceinline__ v8h low_part(int n) const {
+    if constexpr (LOW == 1) return from_upper_bytes(low[n]);
+    else return low[n];
   }
   // K S^T and Q S^T. What comes out of LDS is read a step ahead of its use, here and
   // below: a wave has its SIMD to itself, or nearly.
@@ -774,11 +790,11 @@ struct Chain {
 #pragma unroll
         for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], lo[1], y[i]);
       }
-      if constexpr (Parts<DT>::kLowWeights) {
+      if constexpr (LOW > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mma16(from_upper_bytes(low[lower_frag(i, 0)]), hi[0], y[i]);
+        for (int i = 0; i < 4; ++i) y[i] = mma16(low_part(lower_frag(i, 0)), hi[0], y[i]);
 #pragma unroll
-        for (int i = 2; i < 4; ++i) y[i] = mma16(from_upper_bytes(low[lower_frag(i, 1)]), hi[1], y[i]);
+        for (int i = 2; i < 4; ++i) y[i] = mma16(low_part(lower_frag(i, 1)), hi[1], y[i]);
       }
       if constexpr (AP == 2) {
 #pragma unroll
@@ -947,7 +963,7 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
                    char* turned, char* head, char* factors, char* vals) __attribute__((always_inline)) {
     const bool more = i + 1 < chunks;
     const Factors& f = *(const Factors*)fac;
-    c.load_low(heads + i * (int64_t)HP_::kBytes + lane_id() * 8);  // here by the barrier after the products
+    c.load_low(heads + i * (int64_t)HP_::kBytes);  // here by the barrier after the products
     if (DEEP && more) {
       copy_first(i + 1, first);
       copy_turned(i + 1, turned);

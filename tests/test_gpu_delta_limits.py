@@ -120,3 +120,31 @@ def test_delta_decays_after_one_out_of_range(gpu_lib, dtype, n):
         d["dt"][:, at] = size
         Y, fin = forward(gpu_lib, torch, d)
         compare(d, dtype, Y, fin, True, True)
+
+
+def off_from_rounded(torch, Y, y, dtype):
+    """The distance of Y from the rounded exact outputs, and that of these from the exact ones,
+    relative to y in the 2-norm."""
+    r = _np(torch.from_numpy(y).to(Y.dtype))
+    return np.linalg.norm(_np(Y) - r) / np.linalg.norm(y), np.linalg.norm(r - y) / np.linalg.norm(y)
+
+
+@pytest.mark.parametrize("dtype,bound", (("fp16", 2.0 ** -14.5),))
+@pytest.mark.parametrize("case", [(2, 40, 8, 32, 64, 1), (1, 64, 6, 64, 128, 2), (1, 130, 4, 128, 32, 1), (2, 300, 4, 64, 128, 1)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_delta_outputs_are_rounded_once(gpu_lib, case, dtype, bound):
+    """What Y loses is its rounding. A value that is d off before it goes to its other neighbour,
+    a step s away, with probability |d| / s, so that differences from the rounded exact values
+    have a mean square of |d| s. fp16: terms kept to 2^-19 by their sums and 22 bits, s <= 2^-10 |y|:
+    2^-29 y^2."""
+    import torch
+    B, Ln, H_, P, N, G = case
+    print("delta", case, dtype, flush=True)
+    c = D.make(torch, 51, B, Ln, H_, P, N, G, dtype)
+    Y, fin = forward(gpu_lib, torch, c)
+    y, s, ymag, smag = D.reference(c, 0.3, True, True, True)
+    off, own = off_from_rounded(torch, Y, y, dtype)
+    assert off <= bound, off
+    # and Y is as far from the exact outputs as the rounding is
+    rel = np.linalg.norm(_np(Y) - y) / np.linalg.norm(y)
+    assert rel <= own * (1 + 2.0 ** -8), (rel, own)

@@ -20,10 +20,10 @@
 // Precision. The state is kept and returned in fp32, so that no operand of the
 // products that lead to it may be rounded to 16 bits. Each is taken as a sum of two
 // fp16 numbers (22 significant bits), after a power of two has brought the largest of
-// its column (or row, or tile row) to 2^8: what is below 2^-32 of that is lost. Keys and
+// its column (or row, or tile row) to 2^8: what is below 2^-33 of that is lost. Keys and
 // queries of 16-bit types are exact in one fp16 number in that way, fp32 ones in two.
-// Products of two lower parts (2^-22 of the rest) are left out. For Y alone, which is
-// rounded to 16 bits, fewer parts do: see Parts.
+// Products of two lower parts (2^-22 of the rest) are left out. The same goes for Y, which
+// is rounded once at the end, but for its weights in bf16: see Parts.
 //
 // Times (us: keys, prepare, scan), heads of P x N:
 //   1 x 2048 positions, 64 heads of 64 x 128, bf16          6, 18, 91
@@ -51,11 +51,9 @@ template <int DT>
 struct Parts {
   static constexpr int kKeys = DT == DT_F32 ? 2 : 1;     // fp16 numbers of a key's or query's element
   static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U in LDS: one rounds to 2^-12 of a term
-  // Bytes of each weight's lower part that follow in memory: one fp16 number as it is, whose
-  // term is then off by less than fp16 Y's rounding where terms cancel a thousand times over.
-  static constexpr int kLowBytes = DT == DT_F16 ? 2 : 0;
-  static constexpr int kStateY = DT == DT_BF16 ? 1 : 2;  // of S in Y: one rounds to 2^-12, a 16th of bf16's step
-  static constexpr int kNewY = DT == DT_BF16 ? 1 : 2;    // of U in Y
+  // Bytes of each weight's lower part that follow in memory: two for fp16's Y (terms to
+  // 2^-23), one for bf16's, whose step is 8 times as large (to 2^-16: a 128th of its half step).
+  static constexpr int kLowBytes = DT == DT_F16 ? 2 : DT == DT_BF16 ? 1 : 0;
 };
 
 // ---------------------------------------------------------------------------
@@ -624,7 +622,6 @@ struct Chain {
   typedef KeyPlan<DT, N> KP_;
   typedef typename Store<DT>::T T;
   static constexpr int KS = KP_::KS, NT = KP_::NT, KP = KP_::KP, AP = Parts<DT>::kWeights, LOW = Parts<DT>::kLowBytes;
-  static constexpr int SY = Parts<DT>::kStateY, UY = Parts<DT>::kNewY;
   v4f s[NT], ks[4], qs[4], u[4];
   v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
   typename LowPart<LOW>::T low[6];  // of those, the lower parts
@@ -690,10 +687,8 @@ struct Chain {
       for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][i], hi, qs[i]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][i], lo, ks[i]);
-      if constexpr (SY == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][i], lo, qs[i]);
-      }
+      for (int i = 0; i < 4; ++i) qs[i] = mma16(q[t & 1][i], lo, qs[i]);
       if constexpr (KP == 2) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) ks[i] = mma16(k[t & 1][4 + i], hi, ks[i]);
@@ -784,12 +779,10 @@ struct Chain {
       for (int i = 0; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 0)], hi[0], (v4f)(0.f));
 #pragma unroll
       for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], hi[1], y[i]);
-      if constexpr (UY == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 0)], lo[0], y[i]);
+      for (int i = 0; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 0)], lo[0], y[i]);
 #pragma unroll
-        for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], lo[1], y[i]);
-      }
+      for (int i = 2; i < 4; ++i) y[i] = mma16(wa[lower_frag(i, 1)], lo[1], y[i]);
       if constexpr (LOW > 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = mma16(low_part(lower_frag(i, 0)), hi[0], y[i]);

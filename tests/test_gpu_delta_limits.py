@@ -129,14 +129,14 @@ def off_from_rounded(torch, Y, y, dtype):
     return np.linalg.norm(_np(Y) - r) / np.linalg.norm(y), np.linalg.norm(r - y) / np.linalg.norm(y)
 
 
-@pytest.mark.parametrize("dtype,bound", (("fp16", 2.0 ** -14.5),))
+@pytest.mark.parametrize("dtype,bound", (("bf16", 2.0 ** -11), ("fp16", 2.0 ** -14.5)))
 @pytest.mark.parametrize("case", [(2, 40, 8, 32, 64, 1), (1, 64, 6, 64, 128, 2), (1, 130, 4, 128, 32, 1), (2, 300, 4, 64, 128, 1)],
                          ids=lambda c: "-".join(map(str, c)))
 def test_delta_outputs_are_rounded_once(gpu_lib, case, dtype, bound):
     """What Y loses is its rounding. A value that is d off before it goes to its other neighbour,
     a step s away, with probability |d| / s, so that differences from the rounded exact values
-    have a mean square of |d| s. fp16: terms kept to 2^-19 by their sums and 22 bits, s <= 2^-10 |y|:
-    2^-29 y^2."""
+    have a mean square of |d| s. bf16: terms kept to 2^-15, s <= 2^-7 |y|: 2^-22 y^2, 2^-11 in the
+    2-norm. fp16: terms kept to 2^-19 by their sums and 22 bits, s <= 2^-10 |y|: 2^-29 y^2."""
     import torch
     B, Ln, H_, P, N, G = case
     print("delta", case, dtype, flush=True)
@@ -148,3 +148,27 @@ def test_delta_outputs_are_rounded_once(gpu_lib, case, dtype, bound):
     # and Y is as far from the exact outputs as the rounding is
     rel = np.linalg.norm(_np(Y) - y) / np.linalg.norm(y)
     assert rel <= own * (1 + 2.0 ** -8), (rel, own)
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "fp16", "bf16"))
+def test_delta_outputs_whose_terms_cancel(gpu_lib, dtype):
+    """Queries that see little of a large state: its parts cancel 256 times over in Y. They are
+    kept to 2^-22 of the largest of a row of the state, and summed in fp32: N / 2 roundings of
+    the largest partial sum at most, far less than Y's own rounding in 16 bits."""
+    import torch
+    rng = np.random.default_rng(9)
+    n, H_, P, N = 100, 2, 32, 64
+    half = rng.standard_normal((n, 1, N // 2))
+    Q = np.concatenate([half, -half], -1)
+    K = rng.standard_normal((n, 1, N))
+    K -= K.mean(-1, keepdims=True)
+    s0 = 30.0 + 0.1 * rng.standard_normal((H_, P, N))
+    c = inputs(torch, dtype, 0.1 * rng.standard_normal((n, H_, P)), K, Q, np.zeros((n, H_)), -np.ones(H_), np.full((n, H_), 0.01),
+               s0)
+    Y, fin = forward(gpu_lib, torch, c, logit=False)
+    y, s, ymag, smag = D.reference(c, 0.3, True, False, True)
+    cancel = np.median(ymag) / np.sqrt((y * y).mean())
+    assert cancel > 256
+    half_step = {"fp32": 0.0, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    rel = np.linalg.norm(_np(Y) - y) / np.linalg.norm(y)
+    assert rel <= half_step + cancel * 2.0 ** -19, rel

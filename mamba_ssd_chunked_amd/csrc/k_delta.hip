@@ -408,17 +408,17 @@ __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float
   const double own = sub == 0 ? end[0] : sub == 1 ? end[1] : sub == 2 ? end[2] : end[3];
   // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
   const float beta = in.fk != 0.f ? in.beta : 0.f;
-  const float eg = exp2((float)gs), fu = exp2(fminf((float)(end[3] - gs), 0.f)) * in.fk;
+  const float eg = exp2((float)gs), fu = exp2((float)(end[3] - gs)) * in.fk;
   w.g[lane] = (float)gs;
   w.g_low[lane] = (float)(gs - (double)(float)gs);
   w.beta[lane] = beta;
   w.fk[lane] = in.fk;
   w.fq[lane] = in.fq;
-  w.cols[lane] = exp2(fminf((float)(own - gs), 0.f)) * in.fk;
+  w.cols[lane] = exp2((float)(own - gs)) * in.fk;
   w.rows[3][lane] = beta * in.fk;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const float first = exp2(fminf((float)(gs - end[q]), 0.f));
+    const float first = exp2((float)(gs - end[q]));
     w.first[q][lane] = first;
     w.rows[q][lane] = beta * in.fk * first;
   }
@@ -441,7 +441,7 @@ __device__ __forceinline__ void diagonal_tile(const Gates& w, v4f kk, int i, flo
   const v4f r = *(const v4f*)&w.rows[3][16 * i + 4 * sub];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float gamma = exp2(fminf((gi[e] - gj) + (gil[e] - gl), 0.f));
+    const float gamma = exp2((gi[e] - gj) + (gil[e] - gl));
     diag[i * kDiag + (4 * sub + e) * kDiagRow + col] = col < 4 * sub + e ? r[e] * c * gamma * kk[e] : 0.f;
   }
 }
@@ -542,7 +542,7 @@ __device__ __forceinline__ void form_y_row(const Gates& w, const v4f (&kq)[I + 1
       const v4f cv = *(const v4f*)&w.fk[16 * I + 4 * sub];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float gamma = exp2(fminf((gi - gj[e]) + (gil - gl[e]), 0.f));
+        const float gamma = exp2((gi - gj[e]) + (gil - gl[e]));
         x[j][e] = 4 * sub + e <= col ? fq * cv[e] * gamma * kq[j][e] : 0.f;
       }
     }

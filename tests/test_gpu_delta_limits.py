@@ -122,6 +122,18 @@ def test_delta_decays_after_one_out_of_range(gpu_lib, dtype, n):
         compare(d, dtype, Y, fin, True, True)
 
 
+@pytest.mark.parametrize("n", (7, 150))
+def test_delta_growth(gpu_lib, n):
+    """dt A above 0: a state that grows between its writes."""
+    import torch
+    c = D.make(torch, 67, 2, n, 3, 32, 64, 1, "fp32")
+    c["A"] = -c["A"]
+    c["A"][1] *= -1
+    c["dt"] *= 0.1
+    Y, fin = forward(gpu_lib, torch, c)
+    compare(c, "fp32", Y, fin, True, True)
+
+
 def off_from_rounded(torch, Y, y, dtype):
     """The distance of Y from the rounded exact outputs, and that of these from the exact ones,
     relative to y in the 2-norm."""

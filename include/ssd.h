@@ -458,7 +458,7 @@ int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w
  * H values in shape->dtype, so that a part of In Proj's rows is read in place (element
  * aligned, ld_beta >= H and < 2^28). States [B, H, P, N] fp32. Positions with dt = 0
  * and a key of zeros (as ssd_conv_forward writes behind a sequence's end) leave the
- * state unchanged; beta counts as 0 where the key is zeros, NaN and infinities too.
+ * state unchanged; where the key is zeros beta and X are not used, NaN and infinities too.
  * Sums, decays and states are fp32 or more; Y is rounded once. In chunks (ssd_delta_forward
  * from 9 positions on, or 17 of a small state) what is multiplied keeps 22 bits, but not what
  * is below 2^-32 of the largest of its row of the state (or of the values that meet it) in 64

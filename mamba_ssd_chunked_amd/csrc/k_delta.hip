@@ -77,11 +77,11 @@ struct KeyPlan {
 __device__ __forceinline__ constexpr int lower_tile_at(int i, int j) { return i * (i + 1) / 2 + j; }
 // Factors of a chunk of a head: for each position of K S^T in R (fac_k), of Q S^T in Y
 // (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling); the state's
-// decay over the chunk, and what undoes the scaling of each tile row of T and of Y's
-// weights.
+// decay over the chunk, what undoes the scaling of each tile row of T and of Y's weights,
+// and whether a key is zeros: its fac_k is -1.
 struct Factors {
   float fac_k[kC], fac_q[kC], fac_u[kC];
-  float decay, inv_t[4], inv_a[4];
+  float decay, inv_t[4], inv_a[4], zero_keys;
 };
 // Of each (batch, head, chunk): fragments of T diag(b) (6
 // that are not zero, two parts), of Y's weights (6), the factors, and the weights' lower
@@ -422,10 +422,14 @@ __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float
     w.first[q][lane] = first;
     w.rows[q][lane] = beta * in.fk * first;
   }
-  w.f.fac_k[lane] = eg * in.fk;
+  w.f.fac_k[lane] = in.fk != 0.f ? eg * in.fk : -1.f;
   w.f.fac_q[lane] = eg * in.fq;
   w.f.fac_u[lane] = fu;
-  if (lane == 0) w.f.decay = exp2((float)end[3]);
+  const bool zero_keys = __ballot(in.fk == 0.f) != 0;
+  if (lane == 0) {
+    w.f.decay = exp2((float)end[3]);
+    w.f.zero_keys = zero_keys ? 1.f : 0.f;
+  }
 }
 
 // L's tile (i, j) below the diagonal, from K K^T's.
@@ -602,8 +606,9 @@ struct Prepare {
 // 32 W bytes of a row in one piece, instead of 2 bytes for each value.
 template <int DT, int W>
 constexpr int kRowBytes = 16 * W * sizeof(typename Store<DT>::T);
-// A wave's part of the copies of n rows (of 64; behind the end of the sequence its last
-// row stands in: what it meets in T is zero) that are `step` bytes apart: sizeof(T) of them.
+// A wave's part of the copies of n rows (of 64; behind the end of the sequence its
+// last row stands in, and counts as 0 with the keys there) that are `step` bytes apart: sizeof(T)
+// of them.
 template <int DT, int W>
 __device__ __forceinline__ void copy_values(const char* x, uint32_t step, int n, char* values, int wave) {
   constexpr int kRow = kRowBytes<DT, W>, kLanes = kRow / 16, kRows = kWave / kLanes, kCopies = kC / kRows / W;
@@ -708,7 +713,8 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < 6 * AP; ++n) wa[n] = frag(frags, HeadPlan<DT>::kA + n);
   }
-  // R = V - e^g K S^T, in the place of K S^T; values: V's rows, of W waves' columns.
+  // R = V - e^g K S^T, in the place of K S^T; values: V's rows, of W waves' columns. What
+  // meets a key of zeros counts as 0, whatever stands in V behind a sequence's end.
   template <int W>
   __device__ __forceinline__ void remainders(const char* values, const Factors& f) {
     const char* const at = values + 4 * (lane_id() >> 4) * kRowBytes<DT, W> + place;
@@ -725,6 +731,12 @@ struct Chain {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) ks[i][e] = fmaf(-fk[i][e] * inv_k, ks[i][e], v[i][e]);
+    if (__builtin_amdgcn_readfirstlane(__float_as_int(f.zero_keys))) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ks[i][e] = fk[i][e] < 0.f ? 0.f : ks[i][e];
+    }
   }
   // U = T diag(b) R, as u times inv_r and, of tile row i, inv_t[i].
   __device__ __forceinline__ void changes(const Factors& f) {

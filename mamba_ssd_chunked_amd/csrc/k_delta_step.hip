@@ -100,9 +100,9 @@ __global__ __launch_bounds__(kWaves * kWave) void k_delta_step(DeltaArgs a, int6
     }
     const float kq = group_sum<R>(r.k.x * r.q.x + r.k.y * r.q.y + r.k.z * r.q.z + r.k.w * r.q.w);
     const float decay = expf(r.dt * A);
-    // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
+    // what a key of zeros would write is nothing, whatever stands behind a sequence's end in
+    // beta and the values
     const bool writes = __ballot(r.k.x != 0.f || r.k.y != 0.f || r.k.z != 0.f || r.k.w != 0.f) != 0;
-    const float beta = writes ? r.beta : 0.f;
     float y[XR];
 #pragma unroll
     for (int j = 0; j < XR; ++j) y[j] = 0.f;
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kWaves * kWave) void k_delta_step(DeltaArgs a, int6
     for (int i = 0; i < EL; ++i) {
       const float sk = group_sum<R>(dot4(r.k, s[i])), sq = group_sum<R>(dot4(r.q, s[i]));
       const float x = __shfl(r.x[i / R], (lane & ~(R - 1)) + i % R);
-      const float u = beta * fmaf(-decay, sk, x);
+      const float u = writes ? r.beta * fmaf(-decay, sk, x) : 0.f;
       s[i][0] = fmaf(decay, s[i][0], u * r.k.x);
       s[i][1] = fmaf(decay, s[i][1], u * r.k.y);
       s[i][2] = fmaf(decay, s[i][2], u * r.k.z);

@@ -184,3 +184,31 @@ def test_delta_outputs_whose_terms_cancel(gpu_lib, dtype):
     half_step = {"fp32": 0.0, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
     rel = np.linalg.norm(_np(Y) - y) / np.linalg.norm(y)
     assert rel <= half_step + cancel * 2.0 ** -19, rel
+
+
+def hidden_ends(c, n):
+    """Where sequences end that are padded with dt = 0 and keys of zeros."""
+    ends = (n, n // 2, 1)
+    for b, end in enumerate(ends):
+        for k in ("dt", "K"):
+            c[k][b, end:] = 0
+    return ends
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "fp16", "bf16"))
+@pytest.mark.parametrize("n,P", ((7, 32), (12, 16), (100, 32), (130, 64), (130, 128)))
+def test_delta_values_of_zero_keys(gpu_lib, dtype, n, P):
+    """Whatever stands in X where the key is zeros, as behind the ends of padded sequences,
+    reaches neither the state nor another position's outputs."""
+    import torch
+    c = D.make(torch, 71, 3, n, 4, P, 64, 2, dtype)
+    ends = hidden_ends(c, n)
+    want = forward(gpu_lib, torch, c)
+    for bad in (NAN, INF, -INF):
+        d = dict(c, X=c["X"].clone(), beta=c["beta"].clone())
+        for b, end in enumerate(ends):
+            d["X"][b, end:] = bad
+            d["beta"][b, end:] = bad
+        Y, fin = forward(gpu_lib, torch, d)
+        assert torch.equal(fin, want[1]), bad
+        assert torch.equal(Y, want[0]), bad

@@ -463,6 +463,9 @@ int ssd_pack_weight_i8(int64_t N, int64_t K, const float* w, int8_t* q, float* w
  * from 9 positions on, or 17 of a small state) what is multiplied keeps 22 bits, but not what
  * is below 2^-32 of the largest of its row of the state (or of the values that meet it) in 64
  * positions; in Y of bf16 the weights of a chunk's own changes keep 14 bits.
+ * Elsewhere what is not finite reaches what the formula takes it to, and in chunks (of 64
+ * positions from the first on) earlier outputs of its chunk too, of the same heads and, from
+ * X, of the same value channel; chunks before it are as without it.
  * |b_t| |k_t|^2 <= 2 keeps the state bounded; that is not checked. dt A may be above 0.
  * shape->chunk and shape->schedule have no influence, but must be supported values;
  * batch * nheads < 2^23 (SSD_E_SHAPE). scale must be finite, eps >= 0 and finite

@@ -212,3 +212,23 @@ def test_delta_values_of_zero_keys(gpu_lib, dtype, n, P):
         Y, fin = forward(gpu_lib, torch, d)
         assert torch.equal(fin, want[1]), bad
         assert torch.equal(Y, want[0]), bad
+
+
+@pytest.mark.parametrize("bad", (NAN, INF))
+@pytest.mark.parametrize("dtype", ("fp32", "fp16", "bf16"))
+def test_delta_chunks_before_a_value_that_is_not_finite(gpu_lib, dtype, bad):
+    """A value that is not finite leaves all outputs before its 64 positions, those of other
+    sequences and of heads that do not read it as they are."""
+    import torch
+    c = D.make(torch, 73, 3, 200, 4, 32, 64, 2, dtype)
+    Y, fin = forward(gpu_lib, torch, c)
+    for k in ("X", "K", "Q", "dt", "beta"):
+        for at in (64, 140, 199):
+            d = dict(c)
+            d[k] = c[k].clone()
+            d[k][1, at, 0] = bad
+            Y2, fin2 = forward(gpu_lib, torch, d)
+            first = at // 64 * 64
+            assert torch.equal(Y2[::2], Y[::2]) and torch.equal(fin2[::2], fin[::2]), (k, at)
+            assert torch.equal(Y2[1, :first], Y[1, :first]), (k, at)
+            assert torch.equal(Y2[1, :, 2:], Y[1, :, 2:]) and torch.equal(fin2[1, 2:], fin[1, 2:]), (k, at)

@@ -12,11 +12,12 @@
 // past the caches. 256 sequences of 80 heads of 64 x 128, fp16: 220 us for 1348 MB, 6.1
 // TB/s; one of 64 heads 4.1 us, which are a launch and two round trips to memory.
 #include "ssd_delta.hpp"
+#include "ssd_delta_kind.hpp"
 
 namespace ssd {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = kDeltaStepWaves;
 
 // A position's inputs, as a lane holds them.
 template <int DT, int N, int EL>
@@ -134,23 +135,15 @@ __global__ __launch_bounds__(kWaves * kWave) void k_delta_step(DeltaArgs a, int6
 
 template <int DT, int N, int EL>
 hipError_t go(const Dims& d, const DeltaArgs& a, hipStream_t st) {
-  const int64_t items = d.B * d.H * (d.P / (EL * (kWave / (N / 4))));
-  hipLaunchKernelGGL((k_delta_step<DT, N, EL>), dim3((unsigned)((items + kWaves - 1) / kWaves)), dim3(kWaves * kWave), 0,
-                     st, a, items, d.L, d.H, d.G, d.hpg, d.P);
+  const int64_t items = delta_step_items(d.B * d.H, d.P, N, EL);
+  hipLaunchKernelGGL((k_delta_step<DT, N, EL>), dim3((unsigned)delta_step_wgs(items)), dim3(kWaves * kWave), 0, st, a, items,
+                     d.L, d.H, d.G, d.hpg, d.P);
   return hipGetLastError();
 }
 
-// Passes of a wave: four, fewer where that leaves CUs without 8 waves (us of a step at 1,
-// 2, 4, 8 and 16 passes, heads of 64 x 128: 64 heads 4.1, 4.0, 4.1, 4.6 and 5.6; 320 heads
-// 8.9, 6.8, 5.7, 6.1 and 6.6; 20480 heads 362, 220, 221, 241 and 234); eight for more
-// than one position where waves are many, which share a position's loads and sums
-// (5120 heads, 8 positions: 132 at 4, 111 at 8, 134 at 16; 640 heads 21.4, 21.8 and 27).
 template <int DT, int N>
 hipError_t pick(const Dims& d, const DeltaArgs& a, hipStream_t st) {
-  const int all = d.P * N / 256;  // passes of a head: 1 to 64
-  const int64_t ncu = cu_count() > 0 ? cu_count() : 256, bh = d.B * (int64_t)d.H;
-  int el = d.L > 1 && bh * (all / 8) >= 32 * ncu ? 8 : 4;
-  while (el > 1 && (el > all || bh * (all / el) < 8 * ncu)) el /= 2;
+  const int el = delta_step_passes(d.B * (int64_t)d.H, d.L, d.P, N, cu_count() > 0 ? cu_count() : 256);
   switch (el) {
     case 1: return go<DT, N, 1>(d, a, st);
     case 2: return go<DT, N, 2>(d, a, st);

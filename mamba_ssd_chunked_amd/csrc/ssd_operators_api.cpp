@@ -34,7 +34,7 @@ bool delta_in_steps(const Dims& d) {
 int delta_shape(const ssd_shape* shape, Dims* d, bool* empty) {
   const int rc = check_shape(shape, d, empty, true);
   if (rc) return rc;
-  // the grids' thread counts stay below 2^32
+  // the grids' thread counts stay below 2^32 (the scan's: 64 for 16 rows of a head; the steps': delta_step_passes)
   if (d->B * (int64_t)d->H >= (int64_t)1 << 23) return SSD_E_SHAPE;
   d->c = (int)((d->L + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk);
   int64_t t, u;

@@ -25,3 +25,10 @@ def test_scaled_operands_stay_in_fp16s_range(tmp_path):
     inverse, least, most, scaled, state, bound = map(float, native(tmp_path, "delta_scale").split())
     assert inverse == 1 and least >= 256 and most < scaled == 512
     assert 0.9 * bound < state <= bound < FP16_MOST
+
+
+def test_steps_fit_a_launch(tmp_path):
+    """A launch holds fewer than 2^32 threads, at any number of heads that the calls take."""
+    most, whole, *passes = map(int, native(tmp_path, "delta_kind").split())
+    assert 2 ** 31 < most < 2 ** 32 and whole
+    assert passes == [1, 4, 4, 4, 8]

@@ -232,3 +232,24 @@ def test_delta_chunks_before_a_value_that_is_not_finite(gpu_lib, dtype, bad):
             assert torch.equal(Y2[::2], Y[::2]) and torch.equal(fin2[::2], fin[::2]), (k, at)
             assert torch.equal(Y2[1, :first], Y[1, :first]), (k, at)
             assert torch.equal(Y2[1, :, 2:], Y[1, :, 2:]) and torch.equal(fin2[1, 2:], fin[1, 2:]), (k, at)
+
+
+def test_delta_one_position_of_more_heads_than_a_launch_of_four_passes_holds(gpu_lib):
+    """2^22 heads of 128 x 128 and more, which without a state before or after is a GB: every
+    output is scale beta x (k.q), to half a step of fp16 and 2^-16 for the sum of 128 terms."""
+    import torch
+    L = gpu_lib
+    B, H_, P, N = 65535, 65, 128, 128
+    assert B * H_ > 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(77)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.float16)  # noqa: E731
+    X, K, Q, beta = r(B, 1, H_, P), r(B, 1, 1, N), r(B, 1, 1, N), r(B, 1, H_)
+    dt, A = torch.ones(B, 1, H_, dtype=torch.float16, device="cuda"), -torch.ones(H_, device="cuda")
+    Y = torch.full_like(X, NAN)
+    L.ssd_delta_forward(L.make_shape(B, 1, H_, P, N, 1, 64, "fp16"), X, dt, A, K, Q, beta, Y, scale=0.1, unit=False)
+    torch.cuda.synchronize()
+    for b in range(0, B, 4096):
+        kq = (K[b:b + 4096].double() * Q[b:b + 4096].double())
+        y = 0.1 * beta[b:b + 4096].double()[..., None] * X[b:b + 4096].double() * kq.sum(-1, keepdim=True)
+        mag = 0.1 * (beta[b:b + 4096].double()[..., None] * X[b:b + 4096].double()).abs() * kq.abs().sum(-1, keepdim=True)
+        assert ((Y[b:b + 4096].double() - y).abs() <= 2.0 ** -11 * y.abs() + 2.0 ** -16 * mag + 2.0 ** -25).all(), b

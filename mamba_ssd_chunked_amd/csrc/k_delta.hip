@@ -36,6 +36,7 @@
 // head at 3 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
 // a copy once groups are many (5.8 TB/s of read and written bytes in the last).
 // Preparing a chunk within the scan's launch was no faster in total.
+#include <cstddef>
 #include <type_traits>
 
 #include "ssd_delta.hpp"
@@ -76,13 +77,14 @@ struct KeyPlan {
 // Tile (i, j) of a lower triangle of 4 x 4, in rows.
 __device__ __forceinline__ constexpr int lower_tile_at(int i, int j) { return i * (i + 1) / 2 + j; }
 // Factors of a chunk of a head: for each position of K S^T in R (fac_k), of Q S^T in Y
-// (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling); the state's
-// decay over the chunk, what undoes the scaling of each tile row of T and of Y's weights,
-// and whether a key is zeros: its fac_k is -1.
+// (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling);
+// what undoes the scaling of each tile row of T and of Y's weights; the state's decay over
+// the chunk, and whether a key is zeros: its fac_k is -1.
 struct Factors {
-  float fac_k[kC], fac_q[kC], fac_u[kC];
-  float decay, inv_t[4], inv_a[4], zero_keys;
+  float fac_k[kC], fac_q[kC], fac_u[kC], inv_t[4], inv_a[4];  // read four at a time
+  float decay, zero_keys;
 };
+static_assert(offsetof(Factors, inv_t) % 16 == 0 && offsetof(Factors, inv_a) % 16 == 0, "16-byte reads");
 // Of each (batch, head, chunk): fragments of T diag(b) (6
 // that are not zero, two parts), of Y's weights (6), the factors, and the weights' lower
 // parts, 8 kLowBytes bytes for each lane of a fragment.

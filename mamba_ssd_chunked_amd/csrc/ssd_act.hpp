@@ -24,9 +24,9 @@ __device__ __forceinline__ float sigmoid(float u) {
 
 // u Phi(u) with the normal distribution's Phi, as u (1 - q) or u q with
 // q = erfc(|u| / sqrt 2) / 2. With z = |u| / sqrt 2 and t = 1 / (1 + z / 2),
-// erfc(z) = t exp(-z^2 + p(t)): p is a polynomial of degree 9, fitted to
-// log(exp(z^2) erfc(z) / t) on 0 <= z <= 11 for the least largest error (5e-8). To
-// u^2 / 2 + 12 roundings.
+// erfc(z) = t exp(-z^2 + p(t)) (the form of Press et al., Numerical Recipes): p is a
+// polynomial of degree 9, fitted here to log(exp(z^2) erfc(z) / t) on 0 <= z <= 11 for the
+// least largest error (5.5e-8). To u^2 / 2 + 12 roundings.
 __device__ __forceinline__ float gelu(float u) {
   constexpr float p[10] = {
       -1.26546233f, 0.998917351f, 0.384254506f, 0.0457367484f, -0.0307324845f, -0.0213053197f,

@@ -6,6 +6,13 @@
 //   Y = scale (diag(e^g) Q S^T + (Q K^T . e^{g_i - g_j}, j <= i) U),
 //   S' = e^{g_63} S + (diag(e^{g_63 - g}) U)^T K.
 //
+// Keys that are not taken to length 1 may differ in length by any factor, and b, as 1 / |k|^2,
+// T and U by its square, which is more than products of 16-bit parts hold. There, with p_i
+// the power of two of |k_i|, what the products are formed of is
+//   p_i T_ij b_j p_j,   (V_j - e^{g_j} k_j S^T) / p_j   and   p_i U_i
+// (p_i L_ij / p_j has entries of b |k|^2's size, and what position i adds to the state is
+// p_i U_i times a key of length about 1), and queries' powers of two stay outside Y's weights.
+//
 // Three launches. For every chunk at once, k_delta_keys forms a group's keys and queries
 // as matrix operands, and k_delta_prepare a head's T diag(b) and the weights of U in Y,
 // none of which needs the state. k_delta_scan then goes through a head's chunks in order,
@@ -64,14 +71,14 @@ constexpr int kFrag = 1024;  // bytes: 16 for each lane
 
 // Of each (batch, group, chunk): fragments of K and Q (4 tiles of 16 positions, KS
 // steps of 32 channels) and of K^T (NT tiles of 16 channels, 2 steps of 32 positions),
-// each row's factor, what undoes its scaling and makes it of length 1 (K's 64, Q's), and
-// the fp32 tiles of the lower triangles of K K^T (rows i, columns j of tile (i, j)) and of
+// each row's factor, what undoes its scaling and makes it of length 1 (K's 64, Q's), the
+// scalings' exponents (a byte for K and one for Q, of each row), and the fp32 tiles of the lower triangles of K K^T (rows i, columns j of tile (i, j)) and of
 // Q K^T, transposed.
 template <int DT, int N>
 struct KeyPlan {
   static constexpr int KS = (N + 31) / 32, NT = N / 16, KP = Parts<DT>::kKeys;
   static constexpr int kK = 0, kQ = 4 * KS * KP, kT = 8 * KS * KP, kTurned = 2 * NT * KP;
-  static constexpr int kFac = kT + kTurned, kKK = kFac + 1, kKQ = kKK + 10, kFrags = kKQ + 10;
+  static constexpr int kFac = kT + kTurned, kExponents = kFac * kFrag + 2 * kC * 4, kKK = kFac + 1, kKQ = kKK + 10, kFrags = kKQ + 10;
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
 // Tile (i, j) of a lower triangle of 4 x 4, in rows.
@@ -101,10 +108,10 @@ static_assert(sizeof(Factors) <= kFrag, "a fragment's room");
 __device__ __forceinline__ constexpr int lower_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
 
 // What a head's chunk is made of besides keys and queries, for each position. g: sums
-// of dt A log2(e), twice fp32's bits, as their differences count; cols: the decay from
-// the position to the end of its 16, times K's factor; first[j]: the decay to the
-// position from the end of the 16 positions j; rows[j]: the same times beta and K's
-// factor, rows[3] without it.
+// of dt A log2(e), twice fp32's bits, as their differences count; fk, fq: what K's and Q's
+// factors are but for the powers of two p; beta: beta p^2; cols: the decay from the position
+// to the end of its 16, times fk; first[j]: the decay to the position from the end of the
+// 16 positions j; rows[j]: the same times beta, p and K's factor, rows[3] without it.
 struct Gates {
   float g[kC], g_low[kC], beta[kC], cols[kC], rows[4][kC], first[3][kC], fk[kC], fq[kC];
   Factors f;
@@ -319,6 +326,7 @@ __global__ __launch_bounds__(256) void k_delta_keys(DeltaArgs a, char* ws, int64
         }
         if (zeros) f = 0.f;  // and a key of zeros is known by its factor
         ((float*)(out + KP_::kFac * kFrag))[which * kC + row] = which ? f * a.scale : f;
+        ((int8_t*)(out + KP_::kExponents))[2 * row + which] = (int8_t)sc.exponent();
       }
       if (s < KS) {
 #pragma unroll
@@ -394,7 +402,7 @@ __device__ __forceinline__ double row_add(double v) {
   const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), 0x110 + SHIFT, 0xf, 0xf, true);
   return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float A) {
+__device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float A, bool unit) {
   const int lane = lane_id(), sub = lane >> 4;
   double log_a = (double)in.dt * ((double)A * 1.4426950408889634);
   // 2^log_a is 0 either way, and 64 of them leave the sums 37 bits behind the point: what
@@ -410,23 +418,25 @@ __device__ __forceinline__ void form_gates(Gates& w, const GateInputs& in, float
   const double own = sub == 0 ? end[0] : sub == 1 ? end[1] : sub == 2 ? end[2] : end[3];
   // what a key of zeros would write is nothing, whatever stands behind a sequence's end in beta
   const float beta = in.fk != 0.f ? in.beta : 0.f;
-  const float eg = exp2((float)gs), fu = exp2((float)(end[3] - gs)) * in.fk;
+  // lengths that are not 1 are powers of two (zeros have none)
+  const float p = unit ? 1.f : in.fk, fk = unit ? in.fk : in.fk != 0.f ? 1.f : 0.f;
+  const float eg = exp2((float)gs), row = beta * p * in.fk;
   w.g[lane] = (float)gs;
   w.g_low[lane] = (float)(gs - (double)(float)gs);
-  w.beta[lane] = beta;
-  w.fk[lane] = in.fk;
-  w.fq[lane] = in.fq;
-  w.cols[lane] = exp2((float)(own - gs)) * in.fk;
-  w.rows[3][lane] = beta * in.fk;
+  w.beta[lane] = beta * p * p;
+  w.fk[lane] = fk;
+  w.fq[lane] = unit ? in.fq : 1.f;
+  w.cols[lane] = exp2((float)(own - gs)) * fk;
+  w.rows[3][lane] = row;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
     const float first = exp2((float)(gs - end[q]));
     w.first[q][lane] = first;
-    w.rows[q][lane] = beta * in.fk * first;
+    w.rows[q][lane] = row * first;
   }
   w.f.fac_k[lane] = in.fk != 0.f ? eg * in.fk : -1.f;
   w.f.fac_q[lane] = eg * in.fq;
-  w.f.fac_u[lane] = fu;
+  w.f.fac_u[lane] = exp2((float)(end[3] - gs)) * fk;
   const bool zero_keys = __ballot(in.fk == 0.f) != 0;
   if (lane == 0) {
     w.f.decay = exp2((float)end[3]);
@@ -632,6 +642,7 @@ struct Chain {
   v4f s[NT], ks[4], qs[4], u[4];
   v8h wt[6], wl[6], wa[6 * AP];  // T's fragments, and Y's weights'
   typename LowPart<LOW>::T low[6];  // of those, the lower parts
+  uint2 exponents[4];
   float inv_s, inv_r, max_s, max_u;
   int place;  // of the lane's column in a row of the workgroup's
 
@@ -653,6 +664,17 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       *(v4f*)(a.final_state + (unit * P + p) * (int64_t)N + 16 * n + 4 * (lane_id() >> 4)) = s[n] * inv_s;
+  }
+  // The exponents of keys and queries that are not taken to length 1.
+  __device__ __forceinline__ void load_exponents(const char* keys) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) exponents[i] = *(const uint2*)(keys + KP_::kExponents + (16 * i + 4 * (lane_id() >> 4)) * 2);
+  }
+  // 2^x v for the scaling x of the key (0) or query (1) of position 16 i + 4 (lane / 16) + e, or its inverse.
+  __device__ __forceinline__ float scaled(float v, int which, int i, int e) const {
+    const int word = (int)(e < 2 ? exponents[i].x : exponents[i].y);
+    const int x = (int8_t)(word >> (16 * (e & 1) + 8 * which));
+    return __builtin_amdgcn_ldexpf(v, which ? -x : x);
   }
   // The weights' lower parts, straight from memory; head: of the chunk.
   __device__ __forceinline__ void load_low(const char* head) {
@@ -715,10 +737,10 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < 6 * AP; ++n) wa[n] = frag(frags, HeadPlan<DT>::kA + n);
   }
-  // R = V - e^g K S^T, in the place of K S^T; values: V's rows, of W waves' columns. What
+  // R = V - e^g K S^T (divided by p), in the place of K S^T; values: V's rows, of W waves' columns. What
   // meets a key of zeros counts as 0, whatever stands in V behind a sequence's end.
   template <int W>
-  __device__ __forceinline__ void remainders(const char* values, const Factors& f) {
+  __device__ __forceinline__ void remainders(const char* values, const Factors& f, bool unit) {
     const char* const at = values + 4 * (lane_id() >> 4) * kRowBytes<DT, W> + place;
     float v[4][4];
     v4f fk[4];
@@ -733,6 +755,12 @@ struct Chain {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) ks[i][e] = fmaf(-fk[i][e] * inv_k, ks[i][e], v[i][e]);
+    if (!unit) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ks[i][e] = scaled(ks[i][e], 0, i, e);
+    }
     if (__builtin_amdgcn_readfirstlane(__float_as_int(f.zero_keys))) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -772,7 +800,7 @@ struct Chain {
   // them is at least half as large. (As they are: factors' and changes' own largest values
   // may lie at different positions.)
   __device__ __forceinline__ void outputs_and_state(const char* turned, const Factors& f, T* stage, char* out,
-                                                    uint32_t step, int left) {
+                                                    uint32_t step, int left, bool unit, float scale) {
     const int sub = lane_id() >> 4;
     v8h k[2][NT];
     v4f fu[4];
@@ -838,9 +866,20 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float inv = sy.inv * inv_r * inv_a[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[i][e] *= inv;
+    }
+    if (!unit) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = scaled(y[i][e] * scale, 1, i, e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       const v4f fq = *(const v4f*)(f.fac_q + 16 * i + 4 * sub);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[i][e] = fmaf(fq[e] * was, qs[i][e], y[i][e] * inv);
+      for (int e = 0; e < 4; ++e) y[i][e] = fmaf(fq[e] * was, qs[i][e], y[i][e]);
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -886,7 +925,7 @@ __global__ __launch_bounds__(256) void k_delta_prepare(DeltaArgs a, const char* 
     if constexpr (kRole == 0) {
       GateInputs in;
       in.load<DT>(a, (const float*)(keys + KP_::kFac * kFrag), b * L, (int64_t)ck * kC, L, H, h);
-      form_gates(w, in, a.A[h]);
+      form_gates(w, in, a.A[h], a.unit);
     }
     __syncthreads();
     p.part_a(w, lower, diag);
@@ -970,6 +1009,7 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
                    char* turned, char* head, char* factors, char* vals) __attribute__((always_inline)) {
     const bool more = i + 1 < chunks;
     const Factors& f = *(const Factors*)fac;
+    if (!a.unit) c.load_exponents(keys + i * (int64_t)KP_::kBytes);
     c.load_low(heads + i * (int64_t)HP_::kBytes);  // here by the barrier after the products
     if (DEEP && more) {
       copy_first(i + 1, first);
@@ -983,14 +1023,14 @@ __global__ __launch_bounds__(64 * W, DT != DT_F32 && W == 4 && !DEEP ? 2 : 1) vo
       if (more) copy_first(i + 1, first);
     }
     c.read_head(frags);
-    c.template remainders<W>(values, f);
+    c.template remainders<W>(values, f, a.unit);
     if constexpr (!DEEP) {
       meet<64>();
       if (more) copy_head(i + 1, head, factors, vals);
       asm volatile("" ::: "memory");
     }
     c.changes(f);
-    c.outputs_and_state(kt, f, stage[wv], y + i * (kC * (int64_t)step), step, left(i));
+    c.outputs_and_state(kt, f, stage[wv], y + i * (kC * (int64_t)step), step, left(i), a.unit, a.scale);
     meet<DEEP ? E : kHeadCopies + E>();
     if (!DEEP && more) copy_turned(i + 1, turned);
   };

@@ -21,6 +21,7 @@ struct Scale {
     by = __builtin_bit_cast(float, (uint32_t)e << 23);
     inv = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
   }
+  SSD_HOST_DEVICE int exponent() const { return (int)(__builtin_bit_cast(uint32_t, by) >> 23) - 127; }  // -120 to 90
 };
 // What a scaled value is below, and at most once it is rounded to fp16.
 constexpr float kScaledMost = 512.f;

@@ -253,3 +253,30 @@ def test_delta_one_position_of_more_heads_than_a_launch_of_four_passes_holds(gpu
         y = 0.1 * beta[b:b + 4096].double()[..., None] * X[b:b + 4096].double() * kq.sum(-1, keepdim=True)
         mag = 0.1 * (beta[b:b + 4096].double()[..., None] * X[b:b + 4096].double()).abs() * kq.abs().sum(-1, keepdim=True)
         assert ((Y[b:b + 4096].double() - y).abs() <= 2.0 ** -11 * y.abs() + 2.0 ** -16 * mag + 2.0 ** -25).all(), b
+
+
+@pytest.mark.parametrize("dtype", ("fp32", "fp16", "bf16"))
+@pytest.mark.parametrize("case", [(2, 70, 6, 64, 64, 2), (1, 200, 4, 32, 16, 2), (1, 130, 3, 128, 128, 1), (1, 300, 2, 16, 32, 1)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_delta_keys_of_different_lengths(gpu_lib, case, dtype):
+    """Keys and queries that are not taken to length 1 and differ in length by factors of
+    thousands, with strengths as their stability asks: every row of the state to 2^-18 in the
+    2-norm, and Y's positions to its rounding and 2^-13 of their magnitudes."""
+    import torch
+    B, Ln, H_, P, N, G = case
+    c = D.make(torch, 81, B, Ln, H_, P, N, G, dtype, unit=False, logit=False)
+    g = torch.Generator(device="cuda").manual_seed(82)
+    for k in ("K", "Q"):
+        size = torch.exp(2 * torch.randn(B, Ln, G, 1, generator=g, device="cuda"))
+        c[k] = (c[k].float() * size).to(c[k].dtype)
+    length = (c["K"].float() ** 2).sum(-1).repeat_interleave(H_ // G, 2)
+    c["beta"] = (1.9 * torch.rand(B, Ln, H_, generator=g, device="cuda") / length).clamp(max=30000.0).to(c["X"].dtype)
+    Y, fin = forward(gpu_lib, torch, c, unit=False, logit=False)
+    y, s, ymag, smag = D.reference(c, 0.3, False, False, True)
+    rows = lambda a: np.linalg.norm(a, axis=-1)  # noqa: E731
+    assert (rows(_np(fin) - s) <= 2.0 ** -18 * rows(s)).all(), (rows(_np(fin) - s) / rows(s)).max()
+    half_step = {"fp32": 2.0 ** -24, "fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+    # (half the smallest step of fp16, where outputs are that small)
+    bound = half_step * rows(y) + 2.0 ** -13 * rows(ymag) + (P ** 0.5 * 2.0 ** -25 if dtype == "fp16" else 0)
+    assert (rows(_np(Y) - y) <= bound).all(), (rows(_np(Y) - y) / bound).max()
+    D.check(_np(Y), y, ymag, dtype, D.Y_TAU[dtype], D.Y_NORM[dtype], "y")

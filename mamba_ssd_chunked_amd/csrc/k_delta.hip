@@ -33,15 +33,15 @@
 // is rounded once at the end, but for its weights in bf16: see Parts.
 //
 // Times (us: keys, prepare, scan), heads of P x N:
-//   1 x 2048 positions, 64 heads of 64 x 128, bf16          6, 18, 91
-//   8 x 2048, 80 of 64 x 128, one group each, fp16          9, 126, 310 to 341
-//   4 x 4096, 32 of 128 x 128, 16 groups each, bf16         70, 60, 235
-// The scan is bound by its chain: about 860 instructions a chunk and wave (490 of the
-// vector unit, 104 products, 115 LDS reads) that follow one another, in 2.8 us where a
-// wave has its SIMD to itself, of which half issue nothing; two waves a SIMD issue 57 % of
-// the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 19 to 25 KB a chunk and
-// head at 3 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
-// a copy once groups are many (5.8 TB/s of read and written bytes in the last).
+//   1 x 2048 positions, 64 heads of 64 x 128, bf16          6, 18, 110
+//   8 x 2048, 80 of 64 x 128, one group each, fp16          9, 132 to 144, 316 to 359
+//   4 x 4096, 32 of 128 x 128, 16 groups each, bf16         70, 62, 270
+// The scan is bound by its chain: 1010 to 1080 instructions a chunk and wave (580 to 650 of
+// the vector unit, 132 products, 116 LDS reads) that follow one another, in 3.4 us where a
+// wave has its SIMD to itself, of which 45 % issue nothing; two waves a SIMD issue 72 % of
+// the cycles. Memory serves 2 to 3 TB/s meanwhile. prepare writes 22 to 25 KB a chunk and
+// head at 3 to 4 TB/s, and waits at its four barriers; keys moves what it moves at the rate of
+// a copy once groups are many (6 TB/s of read and written bytes in the last).
 // Preparing a chunk within the scan's launch was no faster in total.
 #include <cstddef>
 #include <type_traits>
@@ -61,6 +61,8 @@ struct Parts {
   static constexpr int kWeights = DT == DT_F32 ? 2 : 1;  // of Y's weights of U in LDS: one rounds to 2^-12 of a term
   // Bytes of each weight's lower part that follow in memory: two for fp16's Y (terms to
   // 2^-23), one for bf16's, whose step is 8 times as large (to 2^-16: a 128th of its half step).
+  // (Differences from the rounded exact outputs: bf16 1.0e-3 without and 2e-4 with; fp16 5e-5
+  // to 7e-5 with one byte, under 4.3e-5 with two, which take 3 % more time.)
   static constexpr int kLowBytes = DT == DT_F16 ? 2 : DT == DT_BF16 ? 1 : 0;
 };
 
@@ -1053,13 +1055,13 @@ template <int DT, int N, int W>
 hipError_t scan(const Dims& d, const DeltaArgs& a, const char* keys, const char* heads, int64_t ncu, hipStream_t st) {
   const int64_t wgs = d.B * d.H * (d.P / (16 * W));
   // Slices of a head share its fragments, and heads of a group the keys': one XCD's L2
-  // serves them where that is one's own (us with and without: 4 x 4096 positions of 32 heads of
-  // 128 x 128 358 and 369; 8 x 2048 of 80 of 64 x 128 391 and 396), but not where all XCDs
-  // read one group's keys either way (2048 of 64 heads 115 and 112).
+  // serves them where that is one's own (us with and without, bf16: 4 x 4096 positions of 32
+  // heads of 128 x 128 383 and 395; 8 x 2048 of 80 of 64 x 128 433 and 444), but not where all
+  // XCDs read one group's keys either way (2048 of 64 heads 132 and 129).
   const bool gather = d.P > 16 * W || d.B * d.G >= 8;
-  // Two buffers where a CU has one workgroup at most (us with two and one: 2048 positions of
-  // 64 heads of 64 x 128 113 and 120; 300 of 64 heads of 64 x 64 27 and 29), one where it may
-  // have two (8 x 2048 of 80 459 and 389; 4 x 1024 of 96 144 and 124). fp32 has no room for two.
+  // Two buffers where a CU has one workgroup at most (us with two and one, bf16: 2048 positions
+  // of 64 heads of 64 x 128 129 and 138; 300 of 64 heads of 64 x 64 30 and 32), one where it may
+  // have two (8 x 2048 of 80 503 and 433; 4 x 1024 of 96 161 and 139). fp32 has no room for two.
   if constexpr (DT != DT_F32) {
     if (wgs <= ncu) {
       hipLaunchKernelGGL((k_delta_scan<DT, N, W, true>), dim3((unsigned)wgs), dim3(64 * W), 0, st, a, keys, heads, d.L, d.H,
@@ -1085,7 +1087,7 @@ hipError_t go(const Dims& d, const DeltaArgs& a, char* ws, hipStream_t st) {
                      d.L, d.H, d.G, d.hpg, d.c, units);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   // Four waves where the head has them (us at 4, 2 and 1: 8 x 2048 positions of 80 heads of
-  // 64 x 128 425, 521 and 783; one sequence of 2048, 64 heads, 114, 115 and 122).
+  // 64 x 128 fp16 443, 546 and 834; one sequence of 2048, 64 heads, bf16 129, 134 and 145).
   switch (d.P) {
     case 16: return scan<DT, N, 1>(d, a, ws, heads, ncu, st);
     case 32: return scan<DT, N, 2>(d, a, ws, heads, ncu, st);

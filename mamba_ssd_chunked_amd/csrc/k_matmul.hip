@@ -7,17 +7,19 @@
 // Rows that are 16-byte aligned and long take the ways of the 8-bit product
 // (ssd_matmul.hpp): a 128-byte step is 64 positions of 16-bit rows, with the same matrix
 // cycles, LDS reads and copies as 128 of 8-bit ones, and the same choice of kernel by
-// the rows' bytes. Others go through registers, in pieces of 16 bytes at any element's
-// address, the last of a row element by element; or, where the caller gives room for it,
-// 16-bit ones are copied into aligned rows first: loads at odd multiples of 2 bytes cost
-// more than a pass over w does (fp32 rows, whose loads are at multiples of 4 bytes, lose by
-// it: 1065 x 4099 x 2579 337 us against 231).
+// the rows' bytes (over 90 products of 1 to 16384 rows, N 16 to 18560 and K 64 to 8192 it
+// takes 2.4 % more than the best kernel in the geometric mean, 35 % at most: 5127 x 240 x 1024
+// 16 us in blocks of 64, 12 in 128). Others go through registers, in pieces of 16 bytes at
+// any element's address, the last of a row element by element; or, where the caller gives
+// room for it, 16-bit ones are copied into aligned rows first: loads at odd multiples of 2
+// bytes cost more than a pass over w does (fp32 rows, whose loads are at multiples of 4 bytes,
+// lose by it: 1065 x 4099 x 2579 337 us against 231).
 //
 // us, and the sum's rate (a large library product: 1500 TF in fp16, 1600 in bf16; a
 // copy: 5.1 TB/s):
 //   8 x 2560 x 5120 bf16          6.6, bound by w: 4.0 TB/s
-//   333 x 8512 x 2048 bf16        18.7, 620 TF; 201 blocks of 128 for 256 CUs
-//   16384 x 10576 x 2560 bf16     805, 1100 TF; products, 8 waves' barriers between them
+//   333 x 8512 x 2048 bf16        20 to 21, 570 TF; 201 blocks of 128 for 256 CUs
+//   16384 x 10576 x 2560 fp16     785 to 825, 1100 TF; products, 8 waves' barriers between them
 //   4096 x 4096 x 1024 fp32       243, 141 TF of 153
 //   1065 x 4099 x 2579 bf16, with bias, GELU and an fp32 residual  62, of which the copies 12
 #include "ssd_act.hpp"

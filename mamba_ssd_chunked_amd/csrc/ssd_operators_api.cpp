@@ -22,10 +22,10 @@ bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p)
 bool known_dtype(int dtype) { return dtype >= SSD_DTYPE_F32 && dtype <= SSD_DTYPE_BF16; }
 
 // Sequences that are taken one position after the other: one launch instead of three, but
-// a time for each position. us, in steps and in chunks: 64 heads of 64 x 128, 8 positions
-// 11.6 and 18.9, 16 17.9 and 18.9, 24 24.8 and 18.6; 4 x 32 heads of 128 x 128, 16
-// positions 23.7 and 24.4; 8 x 80 heads of 64 x 128, 8 positions 22.3 and 31.9, 16 39 and
-// 32; 64 x 80, 4 positions 74 and 131, 8 111 and 132, 16 245 and 136.
+// a time for each position. us, in steps and in chunks, bf16: 64 heads of 64 x 128, 8 positions
+// 10.6 and 17.3, 16 17.7 and 17.2, 24 24.7 and 17.2; 4 x 32 heads of 128 x 128, 8 positions 13.4
+// and 19.4, 16 22.8 and 19.5; 8 x 80 heads of 64 x 128, 8 positions 22 and 37, 12 30 and 37, 16
+// 39 and 37; 64 x 80, 4 positions 75 and 148, 8 112 and 150, 12 156 and 151, 16 209 and 152.
 bool delta_in_steps(const Dims& d) {
   return d.L <= 8 || (d.L <= 16 && d.B * (int64_t)d.H * d.P * d.N <= (int64_t)1 << 22);
 }

@@ -43,7 +43,8 @@ __device__ __forceinline__ void gates_of(int act, float (&z)[VEC]) {
     for (int e = 0; e < VEC; ++e) z[e] = sigmoid_of<DT>(z[e]);
   } else if (act == kActSilu) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) z[e] = DT == DT_F32 ? silu(at_least(z[e], -104.f)) : fmaxf(z[e], -104.f) * sigmoid_of<DT>(z[e]);
+    for (int e = 0; e < VEC; ++e)
+      z[e] = DT == DT_F32 ? silu(at_least(z[e], -104.f)) : fmaxf(z[e], -104.f) * sigmoid_of<DT>(z[e]);
   }
 }
 

@@ -74,21 +74,22 @@ constexpr int kFrag = 1024;  // bytes: 16 for each lane
 // Of each (batch, group, chunk): fragments of K and Q (4 tiles of 16 positions, KS
 // steps of 32 channels) and of K^T (NT tiles of 16 channels, 2 steps of 32 positions),
 // each row's factor, what undoes its scaling and makes it of length 1 (K's 64, Q's), the
-// scalings' exponents (a byte for K and one for Q, of each row), and the fp32 tiles of the lower triangles of K K^T (rows i, columns j of tile (i, j)) and of
-// Q K^T, transposed.
+// scalings' exponents (a byte for K and one for Q, of each row), and the fp32 tiles of the
+// lower triangles of K K^T (rows i, columns j of tile (i, j)) and of Q K^T, transposed.
 template <int DT, int N>
 struct KeyPlan {
   static constexpr int KS = (N + 31) / 32, NT = N / 16, KP = Parts<DT>::kKeys;
   static constexpr int kK = 0, kQ = 4 * KS * KP, kT = 8 * KS * KP, kTurned = 2 * NT * KP;
-  static constexpr int kFac = kT + kTurned, kExponents = kFac * kFrag + 2 * kC * 4, kKK = kFac + 1, kKQ = kKK + 10, kFrags = kKQ + 10;
+  static constexpr int kFac = kT + kTurned, kKK = kFac + 1, kKQ = kKK + 10, kFrags = kKQ + 10;
+  static constexpr int kExponents = kFac * kFrag + 2 * kC * sizeof(float);  // a byte's place
   static constexpr size_t kBytes = (size_t)kFrags * kFrag;
 };
 // Tile (i, j) of a lower triangle of 4 x 4, in rows.
 __device__ __forceinline__ constexpr int lower_tile_at(int i, int j) { return i * (i + 1) / 2 + j; }
 // Factors of a chunk of a head: for each position of K S^T in R (fac_k), of Q S^T in Y
-// (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling);
-// what undoes the scaling of each tile row of T and of Y's weights; the state's decay over
-// the chunk, and whether a key is zeros: its fac_k is -1.
+// (fac_q) and of U in S' (fac_u, with the factor that undoes T's scaling); what undoes the
+// scaling of each tile row of T and of Y's weights; the state's decay over the chunk, and
+// whether a key is zeros: its fac_k is -1.
 struct Factors {
   float fac_k[kC], fac_q[kC], fac_u[kC], inv_t[4], inv_a[4];  // read four at a time
   float decay, zero_keys;
@@ -620,9 +621,9 @@ struct Prepare {
 // 32 W bytes of a row in one piece, instead of 2 bytes for each value.
 template <int DT, int W>
 constexpr int kRowBytes = 16 * W * sizeof(typename Store<DT>::T);
-// A wave's part of the copies of n rows (of 64; behind the end of the sequence its
-// last row stands in, and counts as 0 with the keys there) that are `step` bytes apart: sizeof(T)
-// of them.
+// A wave's part of the copies of n rows (of 64; behind the end of the sequence its last
+// row stands in, and counts as 0 with the keys there) that are `step` bytes apart:
+// sizeof(T) of them.
 template <int DT, int W>
 __device__ __forceinline__ void copy_values(const char* x, uint32_t step, int n, char* values, int wave) {
   constexpr int kRow = kRowBytes<DT, W>, kLanes = kRow / 16, kRows = kWave / kLanes, kCopies = kC / kRows / W;
@@ -656,7 +657,7 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
       s[n] = a.init ? *(const v4f*)(a.init + (unit * P + p) * (int64_t)N + 16 * n + 4 * sub) : (v4f)(0.f);
-    const Scale sc(column_max(tiles_max(s)) * kStateDown);
+    const Scale sc(column_max(tiles_max(s)) * kStateDown, kWide);
     inv_s = sc.inv;
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n] *= sc.by;
@@ -672,7 +673,8 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 4; ++i) exponents[i] = *(const uint2*)(keys + KP_::kExponents + (16 * i + 4 * (lane_id() >> 4)) * 2);
   }
-  // 2^x v for the scaling x of the key (0) or query (1) of position 16 i + 4 (lane / 16) + e, or its inverse.
+  // v divided by the power of two of a key's length (0), or times that of a query's (1), of
+  // position 16 i + 4 (lane / 16) + e.
   __device__ __forceinline__ float scaled(float v, int which, int i, int e) const {
     const int word = (int)(e < 2 ? exponents[i].x : exponents[i].y);
     const int x = (int8_t)(word >> (16 * (e & 1) + 8 * which));
@@ -739,8 +741,8 @@ struct Chain {
 #pragma unroll
     for (int n = 0; n < 6 * AP; ++n) wa[n] = frag(frags, HeadPlan<DT>::kA + n);
   }
-  // R = V - e^g K S^T (divided by p), in the place of K S^T; values: V's rows, of W waves' columns. What
-  // meets a key of zeros counts as 0, whatever stands in V behind a sequence's end.
+  // R = V - e^g K S^T (divided by p), in the place of K S^T; values: V's rows, of W waves'
+  // columns. What meets a key of zeros counts as 0, whatever stands in V behind a sequence's end.
   template <int W>
   __device__ __forceinline__ void remainders(const char* values, const Factors& f, bool unit) {
     const char* const at = values + 4 * (lane_id() >> 4) * kRowBytes<DT, W> + place;
@@ -772,7 +774,7 @@ struct Chain {
   }
   // U = T diag(b) R, as u times inv_r and, of tile row i, inv_t[i].
   __device__ __forceinline__ void changes(const Factors& f) {
-    const Scale sc(column_max(tiles_max(ks)));
+    const Scale sc(column_max(tiles_max(ks)), kWide);
     inv_r = sc.inv;
     v8h hi[2], lo[2];
 #pragma unroll
@@ -844,7 +846,7 @@ struct Chain {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = u[i] * fu[i];
     const float was = inv_s / kStateDown, max_w = column_max(tiles_max(w));
-    const Scale sc(fmaxf(max_s * inv_s * decay * kStateDown, max_w * inv_r));
+    const Scale sc(fmaxf(max_s * inv_s * decay * kStateDown, max_w * inv_r), kWide);
     const float keep = decay * (inv_s * sc.by), by = inv_r * sc.by;
     inv_s = sc.inv;
 #pragma unroll

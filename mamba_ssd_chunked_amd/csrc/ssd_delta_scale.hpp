@@ -13,15 +13,18 @@
 namespace ssd {
 
 // The power of two that brings m to [2^8, 2^9), and its inverse; from 2^-82 on down it
-// is 2^90, so that products of two of them stay in fp32's range.
+// is 2^90, so that products of two of them stay in fp32's range. Values and states, whose
+// scales are not multiplied, have theirs (kWide) down to 2^-110.
+constexpr int kWide = 127 + 118;
 struct Scale {
   float by, inv;
-  SSD_HOST_DEVICE explicit Scale(float m) {
-    const int up = 262 - (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255), e = up < 217 ? up : 217;
+  SSD_HOST_DEVICE explicit Scale(float m, int most = 127 + 90) {
+    const int up = 262 - (int)((__builtin_bit_cast(uint32_t, m) >> 23) & 255), e = up < most ? up : most;
     by = __builtin_bit_cast(float, (uint32_t)e << 23);
     inv = __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
   }
-  SSD_HOST_DEVICE int exponent() const { return (int)(__builtin_bit_cast(uint32_t, by) >> 23) - 127; }  // -120 to 90
+  // of by: -120 to 90
+  SSD_HOST_DEVICE int exponent() const { return (int)(__builtin_bit_cast(uint32_t, by) >> 23) - 127; }
 };
 // What a scaled value is below, and at most once it is rounded to fp16.
 constexpr float kScaledMost = 512.f;

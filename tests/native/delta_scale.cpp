@@ -13,16 +13,18 @@ int main() {
     for (const float f : {1.f, 1.0001f, 1.5f, 1.9999f, 2.f - 0x1p-23f}) {
       const float m = std::ldexp(f, e);
       if (m == 0.f || std::isinf(m)) continue;
-      const ssd::Scale s(m);
-      inverse = inverse && s.by * s.inv == 1.f;
-      const float v = m * s.by;
-      if (m >= 0x1p-82f) least = std::fmin(least, v);
-      most = std::fmax(most, v);
+      for (const bool wide : {false, true}) {
+        const ssd::Scale s = wide ? ssd::Scale(m, ssd::kWide) : ssd::Scale(m);
+        inverse = inverse && s.by * s.inv == 1.f;
+        const float v = m * s.by;
+        if (m >= (wide ? 0x1p-110f : 0x1p-82f)) least = std::fmin(least, v);
+        most = std::fmax(most, v);
+      }
       // a chunk whose changes and keys are the largest, on a state that is as large as they allow
       for (const float keeps : {0.f, 0.25f, 0.5f, 1.f}) {
         if (m > 0x1p100f) continue;
         const float before = keeps / ssd::kStateDown * m;
-        const ssd::Scale sc(std::fmax(before * ssd::kStateDown, m));
+        const ssd::Scale sc(std::fmax(before * ssd::kStateDown, m), ssd::kWide);
         const float key = (2.f - 0x1p-23f) * ssd::Scale(2.f - 0x1p-23f).by;
         state = std::fmax(state, (before * sc.by + 64.f * (m * sc.by) * key) * ssd::kStateDown);
       }

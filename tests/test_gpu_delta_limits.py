@@ -94,7 +94,7 @@ def test_delta_values_of_different_sizes(gpu_lib):
         assert (err <= 2.0 ** -19 * np.abs(s) + 2.0 ** -30 * 4096).all(), (big, err.max())
 
 
-@pytest.mark.parametrize("size", (2.0 ** -60, 2.0 ** 60, 2.0 ** 118))
+@pytest.mark.parametrize("size", (2.0 ** -105, 2.0 ** -60, 2.0 ** 60, 2.0 ** 118))
 def test_delta_values_of_any_size(gpu_lib, size):
     """Values far from 1, up to a few steps below fp32's largest, from zeros."""
     import torch

@@ -7,8 +7,8 @@
 // Memory bound: every input is read once and every output written once; between the two
 // norms a row stays in fp32 registers. A workgroup computes one row (four of up to 512
 // channels, a wave each), as k_norm does, with three reductions over the row instead of
-// two. 16384 rows of 2560 bf16 with a gate for each token and an fp32 residual: 113 us for
-// 587 MB, 5.2 TB/s, a large copy's rate. 8 rows 5.5 us: a launch, a round trip to memory
+// two. 16384 rows of 2560 bf16 with a gate for each token and an fp32 residual: 114 us for
+// 587 MB, 5.2 TB/s, a large copy's rate. 8 rows 5.1 us: a launch, a round trip to memory
 // and the reductions.
 #include "ssd_act.hpp"
 #include "ssd_launch.hpp"
